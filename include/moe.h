@@ -292,6 +292,93 @@ int moe_combine(const void* x, const void* y, const int32_t* topk_idx, const flo
                 const int32_t* slot, int64_t T, int64_t d, int32_t E, int32_t k, int64_t C,
                 moe_dtype_t dtype, void* out, void* stream);
 
+/* ---- The layer for a few tokens, and 4-bit weights ----
+ *
+ * A 4-bit weight matrix stack [E, N, K] (N outputs, K inputs: as W_gate,
+ * W_up with N = d_ff, K = d and W_down with N = d, K = d_ff), with one scale for
+ * every `group` columns of a row:
+ *   MOE_Q4_U4:   W = scale * (q - zero), q = 0 .. 15; zero per group, or 8
+ *                everywhere where `zero` is NULL
+ *   MOE_Q4_E2M1: W = scale * v, v = 0, .5, 1, 1.5, 2, 3, 4, 6 by q's low three
+ *                bits and negative where the fourth is set; `zero` must be NULL
+ * group is 32, 64 or 128 (the last group of a row may be shorter), K a
+ * multiple of 8. Layout (device memory, 16-byte aligned):
+ *   codes [E][ceil(N/16)][ceil(K/128)][1024 bytes]: tiles of 16 rows by 128
+ *     columns. Little-endian 32-bit word s (0 .. 3) of 16-byte piece l (0 .. 63)
+ *     holds row l % 16 and the columns 32 s + 8 (l / 16) + i, i = 0 .. 7 of the
+ *     tile: U4 has column i at bit 2 i (i even) or 14 + 2 i (i odd), E2M1 at
+ *     bit 4 i.
+ *   scale [E][ceil(N/16)][ceil(K/128) * 128/group][16] bf16: group, then row.
+ *   zero  [E][ceil(N/16)][ceil(K/128) * 128/group][16] uint8, 0 .. 15.
+ * Codes of rows and columns past N and K may hold anything; scale and zero of
+ * rows past N and of groups that begin past K too. */
+enum { MOE_Q4_U4 = 0, MOE_Q4_E2M1 = 1 };
+typedef struct {
+  void* codes;
+  void* scale;
+  void* zero;
+  int32_t kind;
+  int32_t group;
+} moe_q4_t;
+
+/* Bytes of codes, scale and zero (each pointer may be NULL; zero_bytes is the
+ * size that zero points take where they are kept). Host only. */
+int moe_q4_size(int32_t E, int64_t N, int64_t K, int32_t group, size_t* codes_bytes, size_t* scale_bytes,
+                size_t* zero_bytes);
+
+/* Quantises W [E, N, K] (dtype) into q's arrays. In fp32, per group of W's
+ * values w (round: to the nearest, ties to even; the scale by a product with
+ * the fp32 reciprocal r6 = 1/6, r7 = 1/7 or r15 = 1/15, the codes by a division):
+ *   U4 with zero:    lo = min(0, w), hi = max(0, w), s = bf16((hi - lo) r15),
+ *                    z = clamp(round(-lo / s), 0, 15), q = clamp(round(w / s) + z, 0, 15)
+ *   U4 without zero: s = bf16(max |w| r7), q = clamp(round(w / s), -8, 7) + 8
+ *   E2M1:            s = bf16(max |w| r6), q = the nearest value to w / s (of
+ *                    two equally near the one with the even code)
+ * A group with s = 0 gets codes that stand for 0 (z = 0). Padding gets scale
+ * 0. W must be finite with (hi - lo) finite. moe_q4_dequantize writes the
+ * values that q stands for, rounded to dtype, as W [E, N, K]: the way back to
+ * the weights that the other entry points take. */
+int moe_q4_quantize(const void* W, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, const moe_q4_t* q, void* stream);
+int moe_q4_dequantize(const moe_q4_t* q, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, void* W, void* stream);
+
+/* out[r] = W[expert[r]] x[r] for R <= 64 rows: x [R, K], out [R, N] (dtype, out
+ * must not overlap x), W [E, N, K] 4-bit, expert [R] int32 or NULL (matrix 0
+ * for every row). A row whose expert is outside [0, E) is left as it was.
+ * Products are exact and summed in fp32, out is rounded once. R == 0 returns
+ * MOE_OK. workspace: moe_q4_matvec_workspace_size() bytes (0 for bf16),
+ * 256-byte aligned. */
+int moe_q4_matvec_workspace_size(int32_t R, int64_t K, moe_dtype_t dtype, size_t* bytes);
+int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32_t R, int32_t E, int64_t N, int64_t K,
+                  moe_dtype_t dtype, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The layer for few tokens, T <= 64 and E <= 1024 (else MOE_ERR_UNSUPPORTED):
+ * the formula, arguments and checks of moe_layer_forward, computed by reading
+ * each chosen expert's weights once instead of through capacity-padded
+ * buckets. Differences:
+ *  - the scores are summed in fp64 and compared so (moe_layer_forward compares
+ *    fp32 sums): experts whose scores differ by less than fp32's rounding may
+ *    be ordered differently by the two;
+ *  - y is not rounded between the down product and the combine;
+ *  - no buckets are built: of stats, topk_idx, topk_w, slot, routed_count,
+ *    kept_count, send_count and totals are written; the others must be NULL;
+ *  - x, W_router, out and the weights must be 16-byte aligned.
+ * Dropless serving takes cf = E / k (C = T). moe_layer_forward_few_q4 takes
+ * the experts' matrices in 4 bits (kind, group and the use of zero the same
+ * for all three; d and d_ff multiples of 8); dtype is that of x, W_router and
+ * out, and the activations keep its precision (h is rounded to it). workspace:
+ * moe_few_workspace_size() bytes, 256-byte aligned; q4 is 1 for 4-bit weights,
+ * else 0. */
+int moe_few_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P,
+                           moe_dtype_t dtype, int32_t q4, size_t* bytes);
+int moe_layer_forward_few(const void* x, const void* W_router, const float* router_bias, const void* W_gate,
+                          const void* W_up, const void* W_down, int64_t T, int64_t d, int64_t d_ff, int32_t E,
+                          int32_t k, float cf, int32_t P, int32_t max_ranks, moe_dtype_t dtype, void* out,
+                          moe_stats_t* stats, void* workspace, size_t workspace_bytes, void* stream);
+int moe_layer_forward_few_q4(const void* x, const void* W_router, const float* router_bias, const moe_q4_t* W_gate,
+                             const moe_q4_t* W_up, const moe_q4_t* W_down, int64_t T, int64_t d, int64_t d_ff,
+                             int32_t E, int32_t k, float cf, int32_t P, int32_t max_ranks, moe_dtype_t dtype,
+                             void* out, moe_stats_t* stats, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Stages of moe_layer_forward (and of moe_layer_forward_replicated, whose
  * ROUTE stage also ranks each expert's copies and deals them to instances),
  * in launch order. */

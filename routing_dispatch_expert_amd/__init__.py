@@ -20,12 +20,17 @@ LIB_PATH = os.path.join(HERE, "libmoe_hip.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1, -2, -3, -4
 MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
+MOE_Q4_U4, MOE_Q4_E2M1 = 0, 1
+Q4_KINDS = {"u4": MOE_Q4_U4, "e2m1": MOE_Q4_E2M1}
+FEW_MAX_TOKENS = 64   # tokens of moe_layer_forward_few, rows of moe_q4_matvec
 TOTALS = ("dropped", "fully_dropped_tokens", "padded_rows", "offrank_bytes")
 
 EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_layer_forward", "moe_backward_workspace_size",
            "moe_layer_backward", "moe_layer_backward_saved", "moe_replica_plan", "moe_replicated_workspace_size", "moe_layer_forward_replicated", "moe_router_workspace_size", "moe_router", "moe_route",
            "moe_permute_workspace_size", "moe_permute", "moe_permute_static", "moe_grouped_gemm_workspace_size",
-           "moe_grouped_gemm", "moe_combine", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
+           "moe_grouped_gemm", "moe_combine", "moe_q4_size", "moe_q4_quantize", "moe_q4_dequantize",
+           "moe_q4_matvec_workspace_size", "moe_q4_matvec", "moe_few_workspace_size", "moe_layer_forward_few",
+           "moe_layer_forward_few_q4", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
 STAGES = ("router", "route", "slots", "scatter", "gate_up", "down", "combine")
 
 
@@ -41,6 +46,11 @@ class moe_stats_t(ctypes.Structure):
                 ("kept_count", ctypes.c_void_p), ("send_count", ctypes.c_void_p),
                 ("totals", ctypes.c_void_p), ("buckets", ctypes.c_void_p), ("instance", ctypes.c_void_p),
                 ("g", ctypes.c_void_p), ("u", ctypes.c_void_p), ("h", ctypes.c_void_p)]
+
+
+class moe_q4_t(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("kind", ctypes.c_int32), ("group", ctypes.c_int32)]
 
 
 _lib = None
@@ -70,6 +80,17 @@ _SIGS = {
     "moe_grouped_gemm_workspace_size": [_I32, _I64, _P],
     "moe_grouped_gemm": [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P, _SZ, _P],
     "moe_combine": [_P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I64, ctypes.c_int, _P, _P],
+    "moe_q4_size": [_I32, _I64, _I64, _I32, _P, _P, _P],
+    "moe_q4_quantize": [_P, _I32, _I64, _I64, ctypes.c_int, ctypes.POINTER(moe_q4_t), _P],
+    "moe_q4_dequantize": [ctypes.POINTER(moe_q4_t), _I32, _I64, _I64, ctypes.c_int, _P, _P],
+    "moe_q4_matvec_workspace_size": [_I32, _I64, ctypes.c_int, _P],
+    "moe_q4_matvec": [_P, _P, ctypes.POINTER(moe_q4_t), _I32, _I32, _I64, _I64, ctypes.c_int, _P, _P, _SZ, _P],
+    "moe_few_workspace_size": [_I64, _I64, _I64, _I32, _I32, _F32, _I32, ctypes.c_int, _I32, _P],
+    "moe_layer_forward_few": [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _F32, _I32, _I32, ctypes.c_int,
+                              _P, ctypes.POINTER(moe_stats_t), _P, _SZ, _P],
+    "moe_layer_forward_few_q4": [_P, _P, _P, ctypes.POINTER(moe_q4_t), ctypes.POINTER(moe_q4_t),
+                                 ctypes.POINTER(moe_q4_t), _I64, _I64, _I64, _I32, _I32, _F32, _I32, _I32,
+                                 ctypes.c_int, _P, ctypes.POINTER(moe_stats_t), _P, _SZ, _P],
     "moe_set_stage_events": [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int],
     "moe_stage_ran": [ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
 }
@@ -283,6 +304,66 @@ def moe_combine(x, y, topk_idx, topk_w, slot, T, d, E, k, C, dtype, out, stream=
                              _dtype(dtype), _ptr(out), _stream(stream)), "moe_combine")
 
 
+def moe_q4_size(E, N, K, group) -> tuple[int, int, int]:
+    """Bytes of a 4-bit matrix stack's codes, scales and (where kept) zero points."""
+    n = [ctypes.c_size_t(0) for _ in range(3)]
+    _check(lib().moe_q4_size(E, N, K, group, *(ctypes.byref(v) for v in n)), "moe_q4_size")
+    return tuple(v.value for v in n)
+
+
+def _q4(q) -> "ctypes.POINTER(moe_q4_t) | None":
+    """q: None, a Q4Weights, or (codes, scale, zero, kind, group)."""
+    if q is None:
+        return None
+    if isinstance(q, Q4Weights):
+        return q._ref
+    codes, scale, zero, kind, group = q
+    return ctypes.pointer(moe_q4_t(_ptr(codes), _ptr(scale), _ptr(zero), Q4_KINDS.get(kind, kind), group))
+
+
+def moe_q4_quantize(W, E, N, K, dtype, q, stream=None):
+    _check(lib().moe_q4_quantize(_ptr(W), E, N, K, _dtype(dtype), _q4(q), _stream(stream)), "moe_q4_quantize")
+
+
+def moe_q4_dequantize(q, E, N, K, dtype, W, stream=None):
+    _check(lib().moe_q4_dequantize(_q4(q), E, N, K, _dtype(dtype), _ptr(W), _stream(stream)), "moe_q4_dequantize")
+
+
+def moe_q4_matvec_workspace_size(R, K, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_q4_matvec_workspace_size(R, K, _dtype(dtype), ctypes.byref(n)), "moe_q4_matvec_workspace_size")
+    return n.value
+
+
+def moe_q4_matvec(x, expert, W, R, E, N, K, dtype, out, workspace, workspace_bytes, stream=None):
+    _check(lib().moe_q4_matvec(_ptr(x), _ptr(expert), _q4(W), R, E, N, K, _dtype(dtype), _ptr(out), _ptr(workspace),
+                               workspace_bytes, _stream(stream)), "moe_q4_matvec")
+
+
+def moe_few_workspace_size(T, d, d_ff, E, k, cf, P, dtype, q4) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_few_workspace_size(T, d, d_ff, E, k, cf, P, _dtype(dtype), q4, ctypes.byref(n)),
+           "moe_few_workspace_size")
+    return n.value
+
+
+def moe_layer_forward_few(x, W_router, router_bias, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, max_ranks, dtype,
+                          out, stats, workspace, workspace_bytes, stream=None):
+    _check(lib().moe_layer_forward_few(_ptr(x), _ptr(W_router), _ptr(router_bias), _ptr(W_gate), _ptr(W_up),
+                                       _ptr(W_down), T, d, d_ff, E, k, cf, P, max_ranks, _dtype(dtype), _ptr(out),
+                                       _stats(stats), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "moe_layer_forward_few")
+
+
+def moe_layer_forward_few_q4(x, W_router, router_bias, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, max_ranks,
+                             dtype, out, stats, workspace, workspace_bytes, stream=None):
+    """W_gate, W_up, W_down: as for _q4 (a Q4Weights each)."""
+    _check(lib().moe_layer_forward_few_q4(_ptr(x), _ptr(W_router), _ptr(router_bias), _q4(W_gate), _q4(W_up),
+                                          _q4(W_down), T, d, d_ff, E, k, cf, P, max_ranks, _dtype(dtype), _ptr(out),
+                                          _stats(stats), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "moe_layer_forward_few_q4")
+
+
 def moe_set_stage_events(events):
     """events: None (off) or 2 * len(STAGES) raw hipEvent_t handles (ints)."""
     if events is None:
@@ -423,4 +504,192 @@ def forward_replicated(x, W_router, W_gate, W_up, W_down, k, cf, replicas, P=1, 
     moe_layer_forward_replicated(x, W_router, router_bias, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, max_ranks,
                                  replicas, R, dt, res["out"], res, workspace, nbytes, stream)
     res["workspace"] = workspace
+    return res
+
+
+# ---------------------------------------------------- few tokens, 4-bit weights
+
+class Q4Weights:
+    """A 4-bit matrix stack [E, N, K] (the layout of moe_q4_t in moe.h): codes
+    uint8 [E, ceil(N/16), ceil(K/128), 1024], scale bfloat16 and zero uint8 (or
+    None) [E, ceil(N/16), ceil(K/128) 128/group, 16]; kind "u4" or "e2m1". Made
+    by quantize_q4(), or from a checkpoint laid out so. The tensors are kept
+    and read in place."""
+
+    def __init__(self, codes, scale, zero, shape, group, kind):
+        import torch
+        E, N, K = (int(v) for v in shape)
+        if kind not in Q4_KINDS:
+            raise ValueError(f"kind: need one of {sorted(Q4_KINDS)}, got {kind!r}")
+        moe_q4_size(E, N, K, group)   # checks the sizes
+        nt, kt = -(-N // 16), -(-K // 128)
+        _require(codes, "codes", torch.uint8, (E, nt, kt, 1024))
+        _require(scale, "scale", torch.bfloat16, (E, nt, kt * (128 // group), 16))
+        if zero is not None:
+            _require(zero, "zero", torch.uint8, tuple(scale.shape))
+            if kind == "e2m1":
+                raise ValueError("zero: e2m1 codes take none")
+        for t in (codes, scale, zero):
+            if t is not None and t.device != codes.device:
+                raise ValueError("codes, scale and zero must be on one device")
+        self.codes, self.scale, self.zero = codes, scale, zero
+        self.shape, self.group, self.kind = (E, N, K), int(group), kind
+        self._ref = ctypes.pointer(moe_q4_t(_ptr(codes), _ptr(scale), _ptr(zero), Q4_KINDS[kind], self.group))
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+class _On:
+    """The device and stream of a call on `device`: the given stream, or
+    torch's current one of that device. Tensors allocated for the call on
+    another stream than torch's current one are marked as used there."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.torch, self.device = torch, device
+        self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+        self.other = None
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            if stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
+                self.other = stream
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard:
+            self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
+
+def _same_device(device, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{n}: need a tensor on {device}, got {t.device}")
+
+
+def quantize_q4(W, group=128, kind="u4", zero_points=True, stream=None):
+    """W [E, N, K] (bf16 or fp32) in 4 bits: a Q4Weights. kind "u4" keeps a zero
+    point a group (zero_points) or is symmetric; "e2m1" has none. Runs on
+    torch's current stream unless one is given."""
+    import torch
+    if W.dim() != 3:
+        raise ValueError(f"W: need [E, N, K], got {tuple(W.shape)}")
+    E, N, K = W.shape
+    _require(W, "W", W.dtype, (E, N, K))
+    dt = _dtype(W.dtype)
+    if kind not in Q4_KINDS:
+        raise ValueError(f"kind: need one of {sorted(Q4_KINDS)}, got {kind!r}")
+    moe_q4_size(E, N, K, group)
+    nt, kt = -(-N // 16), -(-K // 128)
+    with _On(W.device, stream) as on:
+        groups = (E, nt, kt * (128 // group), 16)
+        q = Q4Weights(on.empty((E, nt, kt, 1024), torch.uint8), on.empty(groups, torch.bfloat16),
+                      on.empty(groups, torch.uint8) if kind == "u4" and zero_points else None, (E, N, K), group, kind)
+        moe_q4_quantize(W, E, N, K, dt, q, on.stream)
+    return q
+
+
+def dequantize_q4(q, dtype, stream=None):
+    """The weights that a Q4Weights stands for, rounded to dtype: [E, N, K]."""
+    import torch
+    dt = _dtype(dtype)
+    with _On(q.device, stream) as on:
+        W = on.empty(q.shape, torch.bfloat16 if dt == MOE_DTYPE_BF16 else torch.float32)
+        moe_q4_dequantize(q, *q.shape, dt, W, on.stream)
+    return W
+
+
+def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
+    """out[r] = W[expert[r]] x[r] for up to 64 rows x [R, K] and a Q4Weights W
+    [E, N, K]; expert int32 [R], or None for matrix 0. Rows whose expert is
+    outside [0, E) are left as they are in `out` (zero if it is not given).
+    Returns a dict out, workspace, which may be passed in again."""
+    import torch
+    E, N, K = W.shape
+    R = x.shape[0]
+    dt = _dtype(x.dtype)
+    _require(x, "x", x.dtype, (R, K))
+    if expert is not None:
+        _require(expert, "expert", torch.int32, (R,))
+    _same_device(x.device, W=W, expert=expert, out=out, workspace=workspace)
+    with _On(x.device, stream) as on:
+        if out is None:
+            out = on.empty((R, N), x.dtype)
+            if expert is not None:
+                with torch.cuda.stream(on.stream):
+                    out.zero_()
+        else:
+            _require(out, "out", x.dtype, (R, N))
+        nbytes = moe_q4_matvec_workspace_size(R, K, dt)
+        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+            workspace = on.empty(max(nbytes, 1), torch.uint8)
+        moe_q4_matvec(x, expert, W, R, E, N, K, dt, out, workspace, nbytes, on.stream)
+    return {"out": out, "workspace": workspace}
+
+
+class FewResult(dict):
+    """What forward_few returns. Passed to a later call as `out` it lends that
+    call its outputs and workspace."""
+
+
+def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None, stream=None, max_ranks=0, out=None):
+    """The layer for up to 64 tokens, as forward(), reading each chosen expert's
+    weights once; W_gate, W_up and W_down are tensors of x's dtype or, all three,
+    Q4Weights. Returns a dict as forward() does, without buckets or
+    activations. out: the result of an earlier call with the same sizes, whose
+    tensors this call writes instead of allocating new ones. Runs on torch's
+    current stream unless one is given."""
+    import torch
+    T, d = x.shape
+    E = W_router.shape[0]
+    q4 = isinstance(W_gate, Q4Weights)
+    if any(isinstance(w, Q4Weights) != q4 for w in (W_up, W_down)):
+        raise ValueError("W_gate, W_up, W_down: either all tensors or all Q4Weights")
+    d_ff = W_gate.shape[1]
+    dt, dev = x.dtype, x.device
+    dtype = _dtype(dt)
+    _require(x, "x", dt, (T, d))
+    _require(W_router, "W_router", dt, (E, d))
+    for w, n, s in ((W_gate, "W_gate", (E, d_ff, d)), (W_up, "W_up", (E, d_ff, d)), (W_down, "W_down", (E, d, d_ff))):
+        if not q4:
+            _require(w, n, dt, s)
+        elif w.shape != s:
+            raise ValueError(f"{n}: need 4-bit weights of shape {s}, got {w.shape}")
+    if router_bias is not None:
+        _require(router_bias, "router_bias", torch.float32, (E,))
+    _same_device(dev, W_router=W_router, W_gate=W_gate, W_up=W_up, W_down=W_down, router_bias=router_bias)
+    with _On(dev, stream) as on:
+        key = (T, d, d_ff, E, k, cf, P, dt, q4, dev)
+        if out is None:
+            nbytes = moe_few_workspace_size(T, d, d_ff, E, k, cf, P, dtype, int(q4))
+            i32 = torch.int32
+            res = FewResult(C=moe_capacity(T, E, k, cf), out=on.empty((T, d), dt), topk_idx=on.empty((T, k), i32),
+                            topk_w=on.empty((T, k), torch.float32), slot=on.empty((T, k), i32),
+                            routed_count=on.empty(E, i32), kept_count=on.empty(E, i32), send_count=on.empty(P, i32),
+                            totals=on.empty(4, torch.int64), workspace=on.empty(max(nbytes, 1), torch.uint8))
+            # what a later call may write: held here, so that it stays valid whatever becomes of the dict's entries
+            res._bound = (key, nbytes, dict(res))
+        else:
+            res = out
+            if not isinstance(res, FewResult) or res._bound[0] != key:
+                raise ValueError("out: need the result of a forward_few call with the same sizes, types and device")
+        _, nbytes, t = res._bound
+        call = moe_layer_forward_few_q4 if q4 else moe_layer_forward_few
+        call(x, W_router, router_bias, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, max_ranks, dtype, t["out"], t,
+             t["workspace"], nbytes, on.stream)
     return res

@@ -1019,4 +1019,248 @@ int moe_combine(const void* x, const void* y, const int32_t* topk_idx, const flo
   return MOE_OK;
 }
 
+namespace {
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+int check_q4_shape(int32_t E, int64_t N, int64_t K, int32_t group) {
+  if (E < 1 || N < 1 || K < 1) return fail(MOE_ERR_INVALID_ARG, "need E, N, K >= 1");
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MOE_ERR_INVALID_ARG, "group=%d must be 32, 64 or 128", group);
+  if (K % 8) return fail(MOE_ERR_UNSUPPORTED, "K=%lld must be a multiple of 8", static_cast<long long>(K));
+  const int64_t lim = int64_t{1} << 31;
+  if (N >= lim || K >= lim || moe::ceil_div(N, 16) * moe::ceil_div(K, 128) >= lim / E)
+    return fail(MOE_ERR_UNSUPPORTED, "the weights must have fewer than 2^31 tiles");
+  return MOE_OK;
+}
+
+int check_q4(const moe_q4_t* q, const char* name) {
+  if (!q) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  if (q->kind != MOE_Q4_U4 && q->kind != MOE_Q4_E2M1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown kind %d", name, q->kind);
+  if (!q->codes || !q->scale) return fail(MOE_ERR_INVALID_ARG, "%s: codes or scale is NULL", name);
+  if (q->kind == MOE_Q4_E2M1 && q->zero) return fail(MOE_ERR_INVALID_ARG, "%s: E2M1 codes take no zero", name);
+  if (!aligned16(q->codes) || !aligned16(q->scale) || !aligned16(q->zero))
+    return fail(MOE_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  return MOE_OK;
+}
+
+// Workspace of the few-token layer.
+struct FewPlan {
+  int32_t *idx, *n_act, *act_e, *act_off, *token, *pos;
+  float *w, *y;
+  double* part;
+  moe::bf16_t* xparts;
+  void* h;
+  size_t bytes;
+};
+
+FewPlan plan_few(void* ws, int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, int eb, bool q4) {
+  Carver c(ws);
+  FewPlan p;
+  const size_t n = static_cast<size_t>(T) * k;
+  const bool split = q4 && eb == 4;  // fp32 activations as three bf16 parts
+  p.idx = c.take<int32_t>(n);
+  p.w = c.take<float>(n);
+  p.n_act = c.take<int32_t>(1);
+  p.act_e = c.take<int32_t>(E);
+  p.act_off = c.take<int32_t>(static_cast<size_t>(E) + 1);
+  p.token = c.take<int32_t>(n);
+  p.pos = c.take<int32_t>(n);
+  p.part = c.take<double>(static_cast<size_t>(moe::few_router_splits(T, d, E)) * T * E);
+  p.xparts = c.take<moe::bf16_t>(split ? 3 * static_cast<size_t>(T) * d : 0);
+  p.h = c.take<char>(n * moe::few_ld_h(d_ff) * (split ? 6 : eb));
+  p.y = c.take<float>(n * moe::few_ld_y(d));
+  p.bytes = align_up(c.off);
+  if (!split) p.xparts = nullptr;
+  return p;
+}
+
+int check_few_shape(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P, int dtype, bool q4,
+                    int64_t* C) {
+  int st = check_layer_shape(T, d, d_ff, E, k, cf, P, dtype, C);
+  if (st != MOE_OK) return st;
+  if (T > moe::kFewMaxT)
+    return fail(MOE_ERR_UNSUPPORTED, "T=%lld > %d tokens", static_cast<long long>(T), moe::kFewMaxT);
+  if (E > moe::kFewMaxE) return fail(MOE_ERR_UNSUPPORTED, "E=%d > %d", E, moe::kFewMaxE);
+  if (q4 && (d % 8 || d_ff % 8))
+    return fail(MOE_ERR_UNSUPPORTED, "4-bit weights need d and d_ff that are multiples of 8");
+  const int64_t act = std::min<int64_t>(E, T * k);
+  if (act * (moe::ceil_div(d_ff, 16) + moe::ceil_div(d, 16)) >= (int64_t{1} << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "too many weight tiles");
+  return MOE_OK;
+}
+
+int layer_few(const void* x, const void* W_router, const float* router_bias, const moe::FewWeights& wt, int64_t T,
+              int64_t d, int64_t d_ff, int32_t E, int32_t k, int64_t C, int32_t P, int32_t max_ranks,
+              moe_dtype_t dtype, void* out, const moe_stats_t* stats, void* workspace, size_t workspace_bytes,
+              void* stream) {
+  const int st = check_rank_limit(E, k, P, max_ranks);
+  if (st != MOE_OK) return st;
+  if (!x || !W_router || !out) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(x) || !aligned16(W_router) || !aligned16(out))
+    return fail(MOE_ERR_INVALID_ARG, "x, W_router and out must be 16-byte aligned");
+  const int eb = elem_bytes(dtype);
+  if (overlaps(x, static_cast<size_t>(T * d * eb), out, static_cast<size_t>(T * d * eb)))
+    return fail(MOE_ERR_INVALID_ARG, "out overlaps x");
+  moe_stats_t S;
+  std::memset(&S, 0, sizeof(S));
+  if (stats) S = *stats;
+  if (S.src || S.buckets || S.instance || S.g || S.u || S.h)
+    return fail(MOE_ERR_INVALID_ARG, "the few-token layer builds no src, buckets, instance, g, u or h");
+  if (T == 0) return MOE_OK;
+  const bool q4 = wt.kind >= 0;
+  const FewPlan p = plan_few(workspace, T, d, d_ff, E, k, eb, q4);
+  if (!workspace || workspace_bytes < p.bytes || reinterpret_cast<uintptr_t>(workspace) % kAlign)
+    return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned", p.bytes);
+  moe::FewLayer L;
+  L.x = x;
+  L.wr = W_router;
+  L.bias = router_bias;
+  L.wt = wt;
+  L.T = static_cast<int>(T);
+  L.E = E;
+  L.k = k;
+  L.P = P;
+  L.M = max_ranks;
+  L.d = d;
+  L.f = d_ff;
+  L.C = C;
+  L.bf16 = dtype == MOE_DTYPE_BF16;
+  L.out = out;
+  L.idx = pick(S.topk_idx, p.idx);
+  L.w = pick(S.topk_w, p.w);
+  L.slot = S.slot;
+  L.routed = S.routed_count;
+  L.kept = S.kept_count;
+  L.send = S.send_count;
+  L.totals = S.totals;
+  L.part = p.part;
+  L.xparts = p.xparts;
+  L.ls = {p.n_act, p.act_e, p.act_off, p.token, p.pos};
+  L.h = p.h;
+  L.y = p.y;
+  MOE_HIP_TRY(moe::launch_few_layer(L, static_cast<hipStream_t>(stream)), "few-token layer");
+  return MOE_OK;
+}
+
+}  // namespace
+
+int moe_q4_size(int32_t E, int64_t N, int64_t K, int32_t group, size_t* codes_bytes, size_t* scale_bytes,
+                size_t* zero_bytes) {
+  const int st = check_q4_shape(E, N, K, group);
+  if (st != MOE_OK) return st;
+  const size_t tiles = static_cast<size_t>(E) * moe::ceil_div(N, 16) * moe::ceil_div(K, 128);
+  const size_t groups = tiles * (128 / group) * 16;
+  if (codes_bytes) *codes_bytes = tiles * 1024;
+  if (scale_bytes) *scale_bytes = groups * 2;
+  if (zero_bytes) *zero_bytes = groups;
+  return MOE_OK;
+}
+
+int moe_q4_quantize(const void* W, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, const moe_q4_t* q,
+                    void* stream) {
+  if (!valid_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  int st = check_q4(q, "q");
+  if (st != MOE_OK || (st = check_q4_shape(E, N, K, q->group)) != MOE_OK) return st;
+  if (!W || !aligned16(W)) return fail(MOE_ERR_INVALID_ARG, "W is NULL or not 16-byte aligned");
+  MOE_HIP_TRY(moe::launch_q4_quantize(W, dtype == MOE_DTYPE_BF16, E, N, K, q->kind, q->group, q->codes,
+                                      static_cast<moe::bf16_t*>(q->scale), static_cast<uint8_t*>(q->zero),
+                                      static_cast<hipStream_t>(stream)),
+              "quantize");
+  return MOE_OK;
+}
+
+int moe_q4_dequantize(const moe_q4_t* q, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, void* W, void* stream) {
+  if (!valid_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  int st = check_q4(q, "q");
+  if (st != MOE_OK || (st = check_q4_shape(E, N, K, q->group)) != MOE_OK) return st;
+  if (!W || !aligned16(W)) return fail(MOE_ERR_INVALID_ARG, "W is NULL or not 16-byte aligned");
+  MOE_HIP_TRY(moe::launch_q4_dequantize(q->codes, static_cast<const moe::bf16_t*>(q->scale),
+                                        static_cast<const uint8_t*>(q->zero), E, N, K, q->kind, q->group,
+                                        dtype == MOE_DTYPE_BF16, W, static_cast<hipStream_t>(stream)),
+              "dequantize");
+  return MOE_OK;
+}
+
+int moe_q4_matvec_workspace_size(int32_t R, int64_t K, moe_dtype_t dtype, size_t* bytes) {
+  if (!bytes || R < 0 || K < 1) return fail(MOE_ERR_INVALID_ARG, "need bytes, R >= 0, K >= 1");
+  if (!valid_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  *bytes = dtype == MOE_DTYPE_BF16 ? 0 : align_up(static_cast<size_t>(R) * K * 6);
+  return MOE_OK;
+}
+
+int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32_t R, int32_t E, int64_t N, int64_t K,
+                  moe_dtype_t dtype, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (R < 0) return fail(MOE_ERR_INVALID_ARG, "R=%d < 0", R);
+  int st = check_q4(W, "W");
+  if (st != MOE_OK || (st = check_q4_shape(E, N, K, W->group)) != MOE_OK) return st;
+  if (R > moe::kFewMaxT) return fail(MOE_ERR_UNSUPPORTED, "R=%d > %d rows", R, moe::kFewMaxT);
+  if (std::min(E, std::max(R, 1)) * moe::ceil_div(N, 16) >= (int64_t{1} << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "too many weight tiles");
+  if (!x || !out) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(x) || !aligned16(out)) return fail(MOE_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
+  const size_t eb = elem_bytes(dtype);
+  if (overlaps(x, R * K * eb, out, R * N * eb)) return fail(MOE_ERR_INVALID_ARG, "out overlaps x");
+  if (R == 0) return MOE_OK;
+  size_t need;
+  moe_q4_matvec_workspace_size(R, K, dtype, &need);
+  if (need && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % kAlign))
+    return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned", need);
+  const moe::FewWeights w = {W->kind, W->group, {W->codes, nullptr, nullptr}, {W->scale, nullptr, nullptr},
+                             {W->zero, nullptr, nullptr}};
+  MOE_HIP_TRY(moe::launch_q4_matvec(x, dtype == MOE_DTYPE_BF16, expert, w, R, E, N, K,
+                                    static_cast<moe::bf16_t*>(workspace), out, static_cast<hipStream_t>(stream)),
+              "matvec");
+  return MOE_OK;
+}
+
+int moe_few_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P,
+                           moe_dtype_t dtype, int32_t q4, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  int64_t C;
+  const int st = check_few_shape(T, d, d_ff, E, k, cf, P, dtype, q4 != 0, &C);
+  if (st != MOE_OK) return st;
+  *bytes = plan_few(nullptr, T, d, d_ff, E, k, elem_bytes(dtype), q4 != 0).bytes;
+  return MOE_OK;
+}
+
+int moe_layer_forward_few(const void* x, const void* W_router, const float* router_bias, const void* W_gate,
+                          const void* W_up, const void* W_down, int64_t T, int64_t d, int64_t d_ff, int32_t E,
+                          int32_t k, float cf, int32_t P, int32_t max_ranks, moe_dtype_t dtype, void* out,
+                          moe_stats_t* stats, void* workspace, size_t workspace_bytes, void* stream) {
+  int64_t C;
+  const int st = check_few_shape(T, d, d_ff, E, k, cf, P, dtype, false, &C);
+  if (st != MOE_OK) return st;
+  if (!W_gate || !W_up || !W_down) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(W_gate) || !aligned16(W_up) || !aligned16(W_down))
+    return fail(MOE_ERR_INVALID_ARG, "the weights must be 16-byte aligned");
+  const moe::FewWeights w = {-1, 0, {W_gate, W_up, W_down}, {nullptr, nullptr, nullptr}, {nullptr, nullptr, nullptr}};
+  return layer_few(x, W_router, router_bias, w, T, d, d_ff, E, k, C, P, max_ranks, dtype, out, stats, workspace,
+                   workspace_bytes, stream);
+}
+
+int moe_layer_forward_few_q4(const void* x, const void* W_router, const float* router_bias, const moe_q4_t* W_gate,
+                             const moe_q4_t* W_up, const moe_q4_t* W_down, int64_t T, int64_t d, int64_t d_ff,
+                             int32_t E, int32_t k, float cf, int32_t P, int32_t max_ranks, moe_dtype_t dtype,
+                             void* out, moe_stats_t* stats, void* workspace, size_t workspace_bytes, void* stream) {
+  int64_t C;
+  int st = check_few_shape(T, d, d_ff, E, k, cf, P, dtype, true, &C);
+  if (st != MOE_OK) return st;
+  if ((st = check_q4(W_gate, "W_gate")) != MOE_OK || (st = check_q4(W_up, "W_up")) != MOE_OK ||
+      (st = check_q4(W_down, "W_down")) != MOE_OK)
+    return st;
+  for (const moe_q4_t* q : {W_up, W_down})
+    if (q->kind != W_gate->kind || q->group != W_gate->group || !q->zero != !W_gate->zero)
+      return fail(MOE_ERR_INVALID_ARG, "W_gate, W_up and W_down must agree in kind, group and the use of zero");
+  if ((st = check_q4_shape(E, d_ff, d, W_gate->group)) != MOE_OK ||
+      (st = check_q4_shape(E, d, d_ff, W_gate->group)) != MOE_OK)
+    return st;
+  const moe::FewWeights w = {W_gate->kind, W_gate->group, {W_gate->codes, W_up->codes, W_down->codes},
+                             {W_gate->scale, W_up->scale, W_down->scale}, {W_gate->zero, W_up->zero, W_down->zero}};
+  return layer_few(x, W_router, router_bias, w, T, d, d_ff, E, k, C, P, max_ranks, dtype, out, stats, workspace,
+                   workspace_bytes, stream);
+}
+
 }  // extern "C"
