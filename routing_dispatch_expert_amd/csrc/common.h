@@ -313,6 +313,7 @@ hipError_t launch_combine(const void* x, const void* y, const int32_t* idx, cons
 
 // ---- few tokens and 4-bit weights (few.hip, q4.hip) ----
 constexpr int kFewMaxT = 64, kFewMaxE = 1024, kFewMaxCopies = kFewMaxT * 32;
+constexpr int64_t kFewMaxWidth = 1 << 23;  // of d, d_ff and K
 enum { kQ4U4 = 0, kQ4E2m1 = 1 };  // MOE_Q4_U4, MOE_Q4_E2M1
 // Expert weights: kind < 0 dense (bf16 or fp32 rows), else 4-bit (q4.h).
 struct FewWeights {
@@ -320,10 +321,10 @@ struct FewWeights {
   const void *w[3], *scale[3], *zero[3];
 };
 // The kept copies by expert: experts with copies act_e[n_act], copies
-// act_off[i] .. act_off[i + 1] - 1 of the i-th, each copy's token [T k], and
-// each copy's position pos [T, k] (-1: dropped).
+// act_off[i] .. act_off[i + 1] - 1 of the i-th, and each copy's token and gate.
 struct FewLists {
-  int32_t *n_act, *act_e, *act_off, *token, *pos;
+  int32_t *n_act, *act_e, *act_off, *token;
+  float* gate;
 };
 struct FewLayer {
   const void *x, *wr;
@@ -341,12 +342,10 @@ struct FewLayer {
   bf16_t* xparts;   // [3][T][d]: fp32 x beside 4-bit weights, else NULL
   FewLists ls;
   void* h;          // [parts][T k][few_ld_h(f)], bf16 (fp32 beside fp32 weights)
-  float* y;         // [T k][few_ld_y(d)]
 };
 int few_router_splits(int64_t T, int64_t d, int E);
-// Row lengths of h and y: whole 128-byte lines, so that no two rows share one.
+// Row length of h: whole 128-byte lines.
 inline int64_t few_ld_h(int64_t f) { return ceil_div(f, 64) * 64; }
-inline int64_t few_ld_y(int64_t d) { return ceil_div(d, 32) * 32; }
 hipError_t launch_few_layer(const FewLayer& L, hipStream_t s);
 // out[r] = W[expert[r]] x[r] for R <= 64 rows, W (w.w[0]) 4-bit [E, N, K];
 // expert NULL: matrix 0; a row whose expert is outside [0, E) is left as it

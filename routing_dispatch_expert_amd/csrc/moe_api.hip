@@ -1047,8 +1047,8 @@ int check_q4(const moe_q4_t* q, const char* name) {
 
 // Workspace of the few-token layer.
 struct FewPlan {
-  int32_t *idx, *n_act, *act_e, *act_off, *token, *pos;
-  float *w, *y;
+  int32_t *idx, *n_act, *act_e, *act_off, *token;
+  float *w, *gate;
   double* part;
   moe::bf16_t* xparts;
   void* h;
@@ -1066,11 +1066,10 @@ FewPlan plan_few(void* ws, int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_
   p.act_e = c.take<int32_t>(E);
   p.act_off = c.take<int32_t>(static_cast<size_t>(E) + 1);
   p.token = c.take<int32_t>(n);
-  p.pos = c.take<int32_t>(n);
+  p.gate = c.take<float>(n);
   p.part = c.take<double>(static_cast<size_t>(moe::few_router_splits(T, d, E)) * T * E);
   p.xparts = c.take<moe::bf16_t>(split ? 3 * static_cast<size_t>(T) * d : 0);
   p.h = c.take<char>(n * moe::few_ld_h(d_ff) * (split ? 6 : eb));
-  p.y = c.take<float>(n * moe::few_ld_y(d));
   p.bytes = align_up(c.off);
   if (!split) p.xparts = nullptr;
   return p;
@@ -1085,6 +1084,8 @@ int check_few_shape(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, fl
   if (E > moe::kFewMaxE) return fail(MOE_ERR_UNSUPPORTED, "E=%d > %d", E, moe::kFewMaxE);
   if (q4 && (d % 8 || d_ff % 8))
     return fail(MOE_ERR_UNSUPPORTED, "4-bit weights need d and d_ff that are multiples of 8");
+  if (std::max(d, d_ff) > moe::kFewMaxWidth)  // rows are addressed with 32-bit byte offsets
+    return fail(MOE_ERR_UNSUPPORTED, "d and d_ff must be at most %lld", static_cast<long long>(moe::kFewMaxWidth));
   const int64_t act = std::min<int64_t>(E, T * k);
   if (act * (moe::ceil_div(d_ff, 16) + moe::ceil_div(d, 16)) >= (int64_t{1} << 30))
     return fail(MOE_ERR_UNSUPPORTED, "too many weight tiles");
@@ -1137,9 +1138,8 @@ int layer_few(const void* x, const void* W_router, const float* router_bias, con
   L.totals = S.totals;
   L.part = p.part;
   L.xparts = p.xparts;
-  L.ls = {p.n_act, p.act_e, p.act_off, p.token, p.pos};
+  L.ls = {p.n_act, p.act_e, p.act_off, p.token, p.gate};
   L.h = p.h;
-  L.y = p.y;
   MOE_HIP_TRY(moe::launch_few_layer(L, static_cast<hipStream_t>(stream)), "few-token layer");
   return MOE_OK;
 }
@@ -1197,6 +1197,8 @@ int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32
   int st = check_q4(W, "W");
   if (st != MOE_OK || (st = check_q4_shape(E, N, K, W->group)) != MOE_OK) return st;
   if (R > moe::kFewMaxT) return fail(MOE_ERR_UNSUPPORTED, "R=%d > %d rows", R, moe::kFewMaxT);
+  if (K > moe::kFewMaxWidth)
+    return fail(MOE_ERR_UNSUPPORTED, "K must be at most %lld", static_cast<long long>(moe::kFewMaxWidth));
   if (std::min(E, std::max(R, 1)) * moe::ceil_div(N, 16) >= (int64_t{1} << 31))
     return fail(MOE_ERR_UNSUPPORTED, "too many weight tiles");
   if (!x || !out) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
