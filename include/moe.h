@@ -341,7 +341,7 @@ int moe_q4_size(int32_t E, int64_t N, int64_t K, int32_t group, size_t* codes_by
 int moe_q4_quantize(const void* W, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, const moe_q4_t* q, void* stream);
 int moe_q4_dequantize(const moe_q4_t* q, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, void* W, void* stream);
 
-/* out[r] = W[expert[r]] x[r] for R <= 64 rows, K <= 2^23: x [R, K], out [R, N] (dtype, out
+/* out[r] = W[expert[r]] x[r] for R <= 64 rows, K <= 2^22: x [R, K], out [R, N] (dtype, out
  * must not overlap x), W [E, N, K] 4-bit, expert [R] int32 or NULL (matrix 0
  * for every row). A row whose expert is outside [0, E) is left as it was.
  * Products are exact and summed in fp32, out is rounded once. R == 0 returns
@@ -351,7 +351,7 @@ int moe_q4_matvec_workspace_size(int32_t R, int64_t K, moe_dtype_t dtype, size_t
 int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32_t R, int32_t E, int64_t N, int64_t K,
                   moe_dtype_t dtype, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
-/* The layer for few tokens, T <= 64, E <= 1024, d and d_ff <= 2^23 (else
+/* The layer for few tokens, T <= 64, E <= 1024, d and d_ff <= 2^22 (else
  * MOE_ERR_UNSUPPORTED):
  * the formula, arguments and checks of moe_layer_forward, computed by reading
  * each chosen expert's weights once instead of through capacity-padded

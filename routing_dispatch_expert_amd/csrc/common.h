@@ -313,7 +313,8 @@ hipError_t launch_combine(const void* x, const void* y, const int32_t* idx, cons
 
 // ---- few tokens and 4-bit weights (few.hip, q4.hip) ----
 constexpr int kFewMaxT = 64, kFewMaxE = 1024, kFewMaxCopies = kFewMaxT * 32;
-constexpr int64_t kFewMaxWidth = 1 << 23;  // of d, d_ff and K
+constexpr int kFewMaxSplits = 8;  // slices of d of the router scores
+constexpr int64_t kFewMaxWidth = 1 << 22;  // of d, d_ff and K
 enum { kQ4U4 = 0, kQ4E2m1 = 1 };  // MOE_Q4_U4, MOE_Q4_E2M1
 // Expert weights: kind < 0 dense (bf16 or fp32 rows), else 4-bit (q4.h).
 struct FewWeights {

@@ -18,12 +18,12 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 namespace moe {
 namespace {
 
-constexpr int kWaves = 4;            // waves of an expert work-group
-constexpr int kThreads = kWaves * 64;
+constexpr int kRouterWaves = 4, kRouterThreads = 64 * kRouterWaves;
 
 enum WKind { kDenseBf16, kDenseF32, kU4, kE2m1 };
 
@@ -34,41 +34,48 @@ enum WKind { kDenseBf16, kDenseF32, kU4, kE2m1 };
 // below fp32's rounding: sums of different order pick the same experts.
 // ---------------------------------------------------------------------------
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void few_router_kernel(const void* xv, const void* wv, int T, int E, int64_t d,
+__global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void* xv, const void* wv, int T, int E, int64_t d,
                                                               int S, double* __restrict__ part,
-                                                              bf16_t* __restrict__ parts, int32_t* __restrict__ clear,
-                                                              int n_clear) {
-  __shared__ double red[kWaves][64][4];
+                                                              bf16_t* __restrict__ parts) {
+  __shared__ double red[kRouterWaves][64][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
   const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16, s = blockIdx.z;
   const int64_t block = (static_cast<int64_t>(s) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-  const int64_t nthreads = static_cast<int64_t>(gridDim.x) * gridDim.y * gridDim.z * kThreads;
-  for (int64_t i = block * kThreads + threadIdx.x; i < n_clear; i += nthreads) clear[i] = 0;
-  if (!BF16 && parts) split_rows(static_cast<const float*>(xv), T * d, parts, block * kThreads + threadIdx.x, nthreads);
+  const int64_t nthreads = static_cast<int64_t>(gridDim.x) * gridDim.y * gridDim.z * kRouterThreads;
+  if (!BF16 && parts) split_rows(static_cast<const float*>(xv), T * d, parts, block * kRouterThreads + threadIdx.x, nthreads);
   constexpr int kStep = BF16 ? 32 : 16, kVec = BF16 ? 8 : 4;
   const int64_t steps = ceil_div(d, kStep);
-  const int64_t j0 = steps * (s * kWaves + wave) / (S * kWaves), j1 = steps * (s * kWaves + wave + 1) / (S * kWaves);
+  const int64_t j0 = steps * (s * kRouterWaves + wave) / (S * kRouterWaves), j1 = steps * (s * kRouterWaves + wave + 1) / (S * kRouterWaves);
   const int64_t er = std::min(e0 + col, E - 1), tr = std::min(t0 + col, T - 1);
+  const char* wr = static_cast<const char*>(wv) + er * d * (16 / kVec);
+  const char* xr = static_cast<const char*>(xv) + tr * d * (16 / kVec);
   double acc[4] = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int64_t j = j0; j < j1; ++j) {
-    const int64_t c = j * kStep + kVec * quad;
-    f32x4 p = {0, 0, 0, 0};
-    uint4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-    if (c < d) {  // d is a multiple of kVec
-      a = *reinterpret_cast<const uint4*>(static_cast<const char*>(wv) + (er * d + c) * (16 / kVec));
-      b = *reinterpret_cast<const uint4*>(static_cast<const char*>(xv) + (tr * d + c) * (16 / kVec));
-    }
-    if constexpr (BF16) {
-      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), p, 0,
-                                                  0, 0);
-    } else {
-      const f32x4 av = __builtin_bit_cast(f32x4, a), bv = __builtin_bit_cast(f32x4, b);
+  constexpr int U = 8;  // steps whose loads are in flight together
+  for (int64_t j = j0; j < j1; j += U) {
+    uint4 a[U], b[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[i], p, 0, 0, 0);
+    for (int u = 0; u < U; ++u) {
+      // past the end the last piece again, and 0 for x (d is a multiple of kVec)
+      const int64_t c = (j + u) * kStep + kVec * quad;
+      const int64_t at = std::min(c, d - kVec) * (16 / kVec);
+      a[u] = *reinterpret_cast<const uint4*>(wr + at);
+      b[u] = *reinterpret_cast<const uint4*>(xr + at);
+      if (j + u >= j1 || c >= d) a[u] = b[u] = uint4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += static_cast<double>(p[i]);
+    for (int u = 0; u < U; ++u) {
+      f32x4 p = {0, 0, 0, 0};
+      if constexpr (BF16) {
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[u]), __builtin_bit_cast(bf16x8, b[u]),
+                                                    p, 0, 0, 0);
+      } else {
+        const f32x4 av = __builtin_bit_cast(f32x4, a[u]), bv = __builtin_bit_cast(f32x4, b[u]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[i], p, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += static_cast<double>(p[i]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) red[wave][lane][i] = acc[i];
@@ -77,7 +84,7 @@ __global__ __launch_bounds__(kThreads) void few_router_kernel(const void* xv, co
   const int l = threadIdx.x >> 2, i = threadIdx.x & 3;
   double v = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) v += red[w][l][i];
+  for (int w = 0; w < kRouterWaves; ++w) v += red[w][l][i];
   const int e = e0 + 4 * (l >> 4) + i, t = t0 + (l & 15);
   if (e < E && t < T) part[(static_cast<int64_t>(s) * T + t) * E + e] = v;
 }
@@ -86,13 +93,51 @@ __global__ __launch_bounds__(kThreads) void few_router_kernel(const void* xv, co
 // Top-k, gates, slots and the experts' token lists: one work-group.
 // ---------------------------------------------------------------------------
 
-// Monotone map of a double to uint64; NaN sorts below every number (its
-// choice is unspecified, but stays a distinct expert), and 0 is below NaN.
+// Monotone map of a double to uint64 and back; NaN sorts below every number
+// (its choice is unspecified, but stays a distinct expert), and 0 is below NaN.
 __device__ inline uint64_t order_key(double v) {
   if (v != v) return 1;
   v += 0.0;  // -0.0 -> +0.0
   const uint64_t u = __double_as_longlong(v);
   return (u >> 63) ? ~u : (u | (uint64_t{1} << 63));
+}
+__device__ inline double key_value(uint64_t k) {
+  return __longlong_as_double((k >> 63) ? (k & ~(uint64_t{1} << 63)) : ~k);
+}
+
+// The largest of a wave's 64 values, in every lane: partial maxima move up the
+// lanes by register shifts (within 16, then across rows), without LDS.
+__device__ inline uint32_t wave_max(uint32_t v) {
+  v = std::max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true)));  // by 1
+  v = std::max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true)));  // by 2
+  v = std::max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true)));  // by 4
+  v = std::max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true)));  // by 8
+  v = std::max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x142, 0xf, 0xf, true)));  // lane 15 on
+  v = std::max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x143, 0xf, 0xf, true)));  // lane 31 on
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// The best (key, then lowest expert) of a wave's candidates, one a lane; *win is
+// the lane that holds it. Two candidates seldom share the key's upper half.
+__device__ inline void wave_best(uint64_t key, int e, uint64_t* best_key, int* best_e, int* win) {
+  const uint32_t hi = key >> 32, lo = static_cast<uint32_t>(key);
+  const uint32_t mh = wave_max(hi);
+  unsigned long long c = __ballot(hi == mh);
+  uint32_t ml;
+  if (__popcll(c) == 1) {
+    ml = __builtin_amdgcn_readlane(lo, __ffsll(c) - 1);
+  } else {
+    ml = wave_max(hi == mh ? lo : 0u);
+    c = __ballot(hi == mh && lo == ml);
+    if (__popcll(c) > 1) {
+      const bool mine = hi == mh && lo == ml;
+      const uint32_t first = ~wave_max(mine ? ~static_cast<uint32_t>(e) : 0u);
+      c = __ballot(mine && static_cast<uint32_t>(e) == first);
+    }
+  }
+  *win = __ffsll(c) - 1;
+  *best_e = __builtin_amdgcn_readlane(e, *win);
+  *best_key = (static_cast<uint64_t>(mh) << 32) | ml;
 }
 
 struct RouteOut {
@@ -119,17 +164,27 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const double* __restric
   if (tid == 0) dropped_tokens = 0;
 
   for (int t = wave; t < T; t += 16) {
-    double v[NE];
     uint64_t key[NE];
+    constexpr int G = NE < 4 ? NE : 4;  // experts a lane whose partial scores are fetched together
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = lane + 64 * i;
-      v[i] = 0;
-      key[i] = 0;
-      if (e < E) {
-        for (int s = 0; s < S; ++s) v[i] += part[(static_cast<int64_t>(s) * T + t) * E + e];
-        if (bias) v[i] += static_cast<double>(bias[e]);
-        key[i] = order_key(v[i]);
+    for (int i0 = 0; i0 < NE; i0 += G) {
+      double v[kFewMaxSplits][G];
+#pragma unroll
+      for (int s = 0; s < kFewMaxSplits; ++s)
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const int e = lane + 64 * (i0 + i);
+          v[s][i] = 0;
+          if (s < S && e < E) v[s][i] = part[(static_cast<int64_t>(s) * T + t) * E + e];
+        }
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int e = lane + 64 * (i0 + i);
+        double sum = v[0][i];
+#pragma unroll
+        for (int s = 1; s < kFewMaxSplits; ++s) sum += v[s][i];
+        if (bias && e < E) sum += static_cast<double>(bias[e]);
+        key[i0 + i] = e < E ? order_key(sum) : 0;
       }
     }
     if (limit) {  // P <= 64: lane p holds rank p's best score
@@ -149,40 +204,28 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const double* __restric
       for (int i = 0; i < NE; ++i)
         if (lane + 64 * i < E && !((allowed >> ((lane + 64 * i) / per)) & 1)) key[i] = 0;
     }
-    double sel = 0, top = 0;
+    uint64_t sel = 0, top = 0;
     int sel_e = 0;
     for (int r = 0; r < k; ++r) {
-      uint64_t bk = key[0];
-      int be = lane;
-      double bv = v[0];
+      uint64_t mine = key[0], best;
+      int me = lane, e, win;
 #pragma unroll
       for (int i = 1; i < NE; ++i)
-        if (key[i] > bk) {
-          bk = key[i];
-          be = lane + 64 * i;
-          bv = v[i];
+        if (key[i] > mine) {
+          mine = key[i];
+          me = lane + 64 * i;
         }
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) {
-        const uint64_t ok = __shfl_xor(static_cast<unsigned long long>(bk), off);
-        const int oe = __shfl_xor(be, off);
-        const double ov = __shfl_xor(bv, off);
-        if (ok > bk || (ok == bk && oe < be)) {
-          bk = ok;
-          be = oe;
-          bv = ov;
-        }
-      }
-      if (r == 0) top = bv;
+      wave_best(mine, me, &best, &e, &win);
+      if (r == 0) top = best;
       if (lane == r) {
-        sel = bv;
-        sel_e = be;
+        sel = best;
+        sel_e = e;
       }
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (be == lane + 64 * i) key[i] = 0;
+        if (e == lane + 64 * i) key[i] = 0;
     }
-    const double z = lane < k ? exp(sel - top) : 0.0;
+    const double z = lane < k ? exp(key_value(sel) - key_value(top)) : 0.0;
     double sum = z;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
@@ -290,21 +333,22 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const double* __restric
 
 constexpr bool is_dense(WKind k) { return k == kDenseBf16 || k == kDenseF32; }
 
-// Waves a SIMD that the registers are cut for; LDS allows no more where x takes
-// three parts or, beside 4-bit weights, two token tiles.
-constexpr int waves_per_simd(WKind k, int parts, bool wide) { return parts == 3 ? 2 : wide && !is_dense(k) ? 3 : 4; }
+// Waves a SIMD that the registers are cut for: as many as fit without spills,
+// whose own loads and stores would make every wait one for all loads in flight.
+constexpr int waves_per_simd(WKind k, int parts, bool wide) { return parts == 3 ? 2 : wide ? 3 : 4; }
 
 template <WKind KIND>
 using XType = std::conditional_t<KIND == kDenseF32, float, bf16_t>;
 
 // Units of a contraction of K columns.
 template <WKind KIND>
-__device__ inline int64_t units_of(int64_t K) {
-  return KIND == kDenseBf16 ? ceil_div(K, 64) : KIND == kDenseF32 ? ceil_div(K, 32) : ceil_div(K, 128);
+__device__ inline int units_of(int64_t K) {
+  return static_cast<int>(KIND == kDenseBf16 ? ceil_div(K, 64) : KIND == kDenseF32 ? ceil_div(K, 32) : ceil_div(K, 128));
 }
 
 // One matrix stack [E, N, K] as the kernels take it.
 struct WMat {
+  int64_t E;            // matrices
   const void* w;        // dense rows, or code tiles
   const bf16_t* scale;  // 4-bit only
   const uint8_t* zero;  // u4 only; NULL: 8
@@ -326,24 +370,58 @@ __device__ inline int lane_here() {
   return lane;
 }
 
-// One strip: where it begins (the same for all lanes, so that loads take a
-// scalar base), and each lane's offsets from there. Dense: of its pieces of the
-// strip's rows 0 - 7 and 8 - 15.
+// Memory from `base` on, `bytes` long, for loads at a common base (in scalar
+// registers) plus a lane's 32-bit offset. A lane past the end gets 0 and touches
+// nothing, which also stands in for loads under a condition.
+struct Span {
+  const char* base;
+  uint32_t bytes;
+
+  __device__ inline uint32_t load4(uint32_t lane_off, uint32_t off) const {
+    const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), static_cast<short>(0),
+                                                     static_cast<int>(bytes), 0x00020000);
+    return __builtin_amdgcn_raw_buffer_load_b32(r, static_cast<int>(lane_off), static_cast<int>(off), 0);
+  }
+  template <bool ONCE>  // read once: not to be kept in the caches
+  __device__ inline auto load16(uint32_t lane_off, uint32_t off) const {
+    const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), static_cast<short>(0),
+                                                     static_cast<int>(bytes), 0x00020000);
+    return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(lane_off), static_cast<int>(off), ONCE ? 2 : 0);
+  }
+};
+__device__ inline Span span(const void* base, int64_t bytes) {
+  return Span{static_cast<const char*>(base), static_cast<uint32_t>(std::min<int64_t>(bytes, 0x7ffffff0ll))};
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every span
+
+// One strip: its weights from their first line or tile to the end of the
+// matrices, and each lane's offset there (dense: of its pieces of rows 0 - 7
+// and, `hi` further, of rows 8 - 15); the scales and zero points of its groups.
 template <WKind KIND>
 struct Strip {
-  const char* base;      // first line, or first tile
-  const bf16_t* scale;   // first group's rows
-  const uint8_t* zero;   // u4: first group's zero points, and the bytes to the next group's
-  int zstep;
+  Span w, scale, zero;
+  int zstep;             // bytes from one group's zero points to the next group's
   uint32_t lo, hi;
 };
 
-// n rows of x (at most 64): a common base, and in lane c row c's offset.
+// n rows of x (at most 64), and in lane c row c's offset.
 struct Rows {
-  const char* base;
+  Span first;
+  int64_t part;  // bytes from one bf16 part of fp32 rows to the next
   uint32_t off;
   int n;
-  int64_t part;  // bytes from one bf16 part of fp32 rows to the next
+  __device__ inline Span of_part(int p) const { return Span{first.base + p * part, first.bytes}; }
+};
+
+// n rows of `stride` bytes in x, row `row` in lane c for c < n. The rows'
+// numbers may still be on their way when the weights are asked for.
+struct RowList {
+  Span x;
+  int64_t stride, part;
+  int n, row;
+  __device__ inline Rows rows() const {
+    return Rows{x, part, static_cast<uint32_t>(row) * static_cast<uint32_t>(stride), n};
+  }
 };
 
 // Dense strips are read in whole 128-byte lines, eight rows an instruction:
@@ -354,37 +432,41 @@ struct Rows {
 // operands of two steps, up to a rotation by eight lanes (operands()).
 __device__ inline int piece_of(int lane) { return (lane >> 4) + 4 * ((lane >> 3) & 1); }
 
-// Rows r0 .. r0 + 15 of matrix e (both the same for all lanes).
+// Rows r0 .. r0 + 15 of matrix e (both the same for all lanes). What lies past
+// the matrix is not stored, whatever is read there: the next matrix or, past
+// the last one, 0.
 template <WKind KIND, int GPT>
 __device__ inline Strip<KIND> strip_of(const WMat& m, int64_t e, int64_t r0, int64_t N, int64_t K) {
   const int lane = threadIdx.x & 63;
   Strip<KIND> s = {};
   if constexpr (is_dense(KIND)) {
-    const uint32_t row = static_cast<uint32_t>(K * sizeof(XType<KIND>));
-    s.base = static_cast<const char*>(m.w) + (e * N + r0) * row;
-    // rows past the matrix repeat its last one; their results are not stored
-    const int last = static_cast<int>(std::min<int64_t>(15, N - 1 - r0));
-    s.lo = std::min(lane & 7, last) * row + piece_of(lane) * 16;
-    s.hi = std::min(8 + (lane & 7), last) * row + piece_of(lane) * 16;
+    const int64_t row = K * sizeof(XType<KIND>), at = (e * N + r0) * row;
+    s.w = span(static_cast<const char*>(m.w) + at, m.E * N * row - at);
+    s.lo = (lane & 7) * static_cast<uint32_t>(row) + piece_of(lane) * 16;
+    s.hi = 8 * static_cast<uint32_t>(row);
   } else {
-    const int64_t nt = ceil_div(N, 16), kt = ceil_div(K, 128);
-    const int64_t t = (e * nt + r0 / 16) * kt;
-    s.base = static_cast<const char*>(m.w) + t * 1024;
+    const int64_t nt = ceil_div(N, 16), kt = ceil_div(K, 128), t = (e * nt + r0 / 16) * kt;
+    s.w = span(static_cast<const char*>(m.w) + t * 1024, kt * 1024);
     s.lo = lane * 16;
-    s.scale = m.scale + t * GPT * 16;
-    s.zero = m.zero ? m.zero + t * GPT * 16 : kEights;
+    s.scale = span(m.scale + t * GPT * 16, kt * GPT * 32);
     s.zstep = m.zero ? 16 : 0;
+    s.zero = span(m.zero ? m.zero + t * GPT * 16 : kEights, m.zero ? kt * GPT * 16 : 16);
   }
   return s;
 }
 
+// Groups of a tile between two marks of multiply().
+template <WKind KIND, int NS>
+constexpr int kMarkEvery = NS == 1 ? (KIND == kU4 ? 2 : 4) : 1;
+
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ inline u32x4 load_once(const char* p, uint32_t off) {
-  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + off));
+__device__ inline u32x4 load_once(const Span& s, uint32_t lane_off, uint32_t off) {
+  return __builtin_bit_cast(u32x4, s.load16<true>(lane_off, off));
 }
-
-__device__ inline u32x4 load_kept(const char* p, uint32_t off) { return *reinterpret_cast<const u32x4*>(p + off); }
+__device__ inline u32x4 load_kept(const Span& s, uint32_t lane_off, uint32_t off = 0) {
+  return __builtin_bit_cast(u32x4, s.load16<false>(lane_off, off));
+}
 
 // The A operands of a line's two steps from the loads of rows 0 - 7 and 8 - 15:
 // step 0 wants piece l / 16 of row l % 16, so lanes 8 - 15 of every 16 take
@@ -418,25 +500,22 @@ __device__ inline f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // and not larger because the difference loses as many bits as it exceeds q.
 // PARTS = 3: fp32 x as the exact sum of three bf16 arrays.
 
-// One unit's weights, as loaded. In the last unit of a row that ends inside it
-// (dense) the lanes past the end repeat the row's last piece: x is 0 there.
+// One unit's weights, as loaded. In the last unit of a dense row that ends
+// inside it the lanes past the end get what follows: x is 0 there.
 template <WKind KIND, int NS>
 struct UnitW {
   u32x4 w[NS][is_dense(KIND) ? 2 : 1];
 };
 
 template <WKind KIND, int NS>
-__device__ inline void load_weights(const Strip<KIND> (&a)[NS], int64_t K, int64_t j, UnitW<KIND, NS>& u) {
+__device__ inline void load_weights(const Strip<KIND> (&a)[NS], int j, UnitW<KIND, NS>& u) {
 #pragma unroll
   for (int r = 0; r < NS; ++r)
     if constexpr (is_dense(KIND)) {
-      const int piece = piece_of(threadIdx.x & 63) * 16;
-      const int64_t left = K * static_cast<int64_t>(sizeof(XType<KIND>)) - j * 128;
-      const uint32_t over = left < 128 ? std::max(0, piece + 16 - static_cast<int>(left)) : 0;
-      u.w[r][0] = load_once(a[r].base + j * 128, a[r].lo - over);
-      u.w[r][1] = load_once(a[r].base + j * 128, a[r].hi - over);
+      u.w[r][0] = load_once(a[r].w, a[r].lo, j * 128);
+      u.w[r][1] = load_once(a[r].w, a[r].lo, j * 128 + a[r].hi);
     } else {
-      u.w[r][0] = load_once(a[r].base + j * 1024, a[r].lo);
+      u.w[r][0] = load_once(a[r].w, a[r].lo, j * 1024);
     }
 }
 
@@ -445,117 +524,143 @@ __device__ inline void load_weights(const Strip<KIND> (&a)[NS], int64_t K, int64
 // registers that the 4-bit codes it meets do, so it cannot be asked for as far
 // ahead, and a load takes about 1 us when all of them wait for memory). The
 // next run's loads wait in registers while this one is multiplied.
-// LDS of a wave: x [PARTS][n rows][run bytes + 16] (the 16 bytes shift each row's
-// banks), then scale [NS][units][GPT][16] bf16 and zero [NS][units][GPT][16] bytes.
-template <WKind KIND, int GPT, int PARTS, int NS, int NT>
+// LDS of a wave: x [PARTS][rows][run bytes + 16] (the 16 bytes shift each row's
+// banks), then fp32 scales [NS][units][GPT][16] and, for u4, -(16 + z) alike:
+// converted here once, not by each of the 16 token columns.
+//
+// A run is up to 4 KiB of x (a part), for ROWS = 1, 4, 16 or (NT = 2) 32 rows: 16,
+// 4 or 1 tiles, 32, 8, 2 or 1 lines; one tile (8 KiB) of 32 rows.
+// Nothing here is loaded under a condition (lanes past the rows, the units and
+// the groups load from nowhere): a load that some path leaves out makes the
+// wait for any older one a wait for all of them.
+template <WKind KIND, int GPT, int PARTS, int NS, int NT, int ROWS>
 struct Stage {
   static constexpr bool kDense = is_dense(KIND);
-  static constexpr int kUnitBytes = kDense ? 128 : 256;  // of a row of x (a part)
-  static constexpr int kLoads = kDense ? 2 * NT + (NT == 1 ? 2 : 0) : 4 * NT;  // 1 KiB each, a part
-  static constexpr int kMaxUnits = kDense ? 32 : GPT == 4 ? 8 : 16;
-  static constexpr int kXBytes = PARTS * (kLoads * 1024 + 16 * NT * 16);
-  static constexpr int kGroupsBytes = kDense ? 0 : NS * kMaxUnits * GPT * 48;
-  static constexpr int kBytes = kXBytes + kGroupsBytes;
+  static constexpr int kUnitBytes = kDense ? 128 : 256;       // of a row of x (a part)
+  static constexpr int kRows = ROWS;
+  // no more groups in a run than the lanes hold zero points of
+  static constexpr int kUnits = kDense ? 32 / ROWS : std::max(1, std::min(16 / GPT, 16 / ROWS));
+  static constexpr int kLoads = (kUnits * kUnitBytes * ROWS + 1023) / 1024;  // 1 KiB each, a part
+  static constexpr int kRow = kUnits * kUnitBytes;            // bytes of a row in a run
+  static constexpr int kStride = kRow + 16;
+  static constexpr int kXBytes = PARTS * kRows * kStride;
+  static constexpr int kScale = kUnits * GPT * 64;            // bytes of a strip's scales
+  static constexpr int kOff = NS * kScale;
+  static constexpr int kBytes = kXBytes + (kDense ? 0 : KIND == kU4 ? 2 * kOff : kOff);
+  // words of a strip's scales (two each) and zero points (four each) in a run, a lane
+  static constexpr int kScaleWords = (kUnits * GPT * 8 + 63) / 64;
+  static_assert(kDense || kUnits * GPT * 4 <= 64, "a lane for each four zero points of a run");
 
   char* lds;
-  int shift, units, stride;     // log2 of a row's 16-byte pieces, units of a run, bytes of a row
+  uint32_t from[kLoads];  // where this lane's pieces of x are in the first run
   u32x4 x[PARTS][kLoads];
-  u32x4 scale[kDense ? 1 : NS], zero[kDense ? 1 : NS];
-  uint32_t at[NT];              // this lane's rows (and piece) in the staged x
+  uint32_t scale[kDense ? 1 : NS][kScaleWords], zero[kDense ? 1 : NS];
+  uint32_t at[NT];        // this lane's rows (and piece) in the staged x
+
+  static __device__ inline int row_of(int lane, int u) { return (u * 64 + lane) / (kRow / 16); }
+  static __device__ inline int piece(int lane, int u) { return (u * 64 + lane) % (kRow / 16) * 16; }
 
   __device__ inline void init(char* wave_lds, const Rows& r) {
     const int lane = threadIdx.x & 63;
     lds = wave_lds;
-    // as many units, a power of two, as the rows leave room for
-    const int log_n = r.n > 1 ? 32 - __clz(r.n - 1) : 0;
-    constexpr int kLogRoom = 31 - __builtin_clz(kLoads * 1024 / kUnitBytes), kLogMost = 31 - __builtin_clz(kMaxUnits);
-    const int log_units = uniform(std::min(kLogMost, kLogRoom - log_n));
-    units = 1 << log_units;
-    shift = log_units + (kDense ? 3 : 4);
-    stride = (16 << shift) + 16;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)  // columns past n repeat the last row; their results are not stored
-      at[t] = std::min(t * 16 + (lane & 15), r.n - 1) * stride + (lane >> 4) * 16;
-  }
-
-  // Asks for units j .. j + units - 1 (up to j1).
-  __device__ inline void ask(const Strip<KIND> (&a)[NS], const Rows& r, int64_t K, int64_t j, int64_t j1) {
-    const int lane = lane_here();
-    const int n_units = static_cast<int>(std::min<int64_t>(units, j1 - j));
-    const int64_t left = K * static_cast<int64_t>(sizeof(XType<KIND>)) - j * kUnitBytes;
-    const int bytes = static_cast<int>(std::min<int64_t>(left, n_units * kUnitBytes));
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      const int i = u * 64 + lane, row = i >> shift, c = (i & ((1 << shift) - 1)) * 16;
-      const uint32_t off = __shfl(r.off, row & 63) + c;
+      const uint32_t row = __shfl(r.off, row_of(lane, u) & 63);
+      from[u] = row_of(lane, u) < r.n ? row + piece(lane, u) : kNowhere;
+    }
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
-        x[p][u] = u32x4{0, 0, 0, 0};  // also past the end of the contraction
-        if (row < r.n && c < bytes) x[p][u] = load_kept(r.base + p * r.part + j * kUnitBytes, off);
-      }
+    for (int t = 0; t < NT; ++t)  // columns past n repeat the last row; their results are not stored
+      at[t] = std::min(t * 16 + (lane & 15), r.n - 1) * kStride + (lane >> 4) * 16;
+  }
+
+  // Asks for units j .. j + kUnits - 1; x and the scales are 0 from unit j1 and
+  // from the end of the contraction on.
+  __device__ inline void ask(const Strip<KIND> (&a)[NS], const Rows& r, int64_t K, int j, int j1) {
+    const int lane = lane_here();
+    const int jj = std::min(j, j1 - 1);  // offsets stay inside, also where nothing is wanted
+    const int64_t left = K * static_cast<int64_t>(sizeof(XType<KIND>)) - static_cast<int64_t>(j) * kUnitBytes;
+    const int bytes = static_cast<int>(std::min<int64_t>(left, static_cast<int64_t>(j1 - j) * kUnitBytes));
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const uint32_t off = piece(lane, u) < bytes ? from[u] : kNowhere;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) x[p][u] = load_kept(r.of_part(p), off, jj * kUnitBytes);
     }
     if constexpr (!kDense) {
       // groups that begin past the end are padding: 0, whatever the arrays hold
-      const int64_t groups = std::min<int64_t>(n_units * GPT, ceil_div(K, 128 / GPT) - j * GPT);
+      const int groups = static_cast<int>(
+          std::min<int64_t>(static_cast<int64_t>(j1 - j) * GPT, ceil_div(K, 128 / GPT) - static_cast<int64_t>(j) * GPT));
 #pragma unroll
       for (int r2 = 0; r2 < NS; ++r2) {
-        scale[r2] = zero[r2] = u32x4{0, 0, 0, 0};
-        if (lane < 2 * groups)
-          scale[r2] = load_kept(reinterpret_cast<const char*>(a[r2].scale + j * GPT * 16), lane * 16);
-        if (KIND == kU4 && lane < groups)
-          zero[r2] = load_kept(reinterpret_cast<const char*>(a[r2].zero) + j * GPT * a[r2].zstep, lane * a[r2].zstep);
+#pragma unroll
+        for (int k = 0; k < kScaleWords; ++k)
+          scale[r2][k] = a[r2].scale.load4(lane + 64 * k < 8 * groups ? (lane + 64 * k) * 4 : kNowhere, jj * GPT * 32);
+        if constexpr (KIND == kU4)
+          zero[r2] = a[r2].zero.load4(lane < 4 * groups ? (lane & 3) * 4 + (lane >> 2) * a[r2].zstep : kNowhere,
+                                      jj * GPT * a[r2].zstep);
       }
     }
   }
 
   // Puts what was asked for into LDS; the wave's reads of the run before are
   // done (a wave's LDS accesses keep their order).
-  __device__ inline void put(int n) {
+  __device__ inline void put() {
     const int lane = lane_here();
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const int i = u * 64 + lane, row = i >> shift, c = (i & ((1 << shift) - 1)) * 16;
+    for (int u = 0; u < kLoads; ++u)
 #pragma unroll
       for (int p = 0; p < PARTS; ++p)
-        if (row < n) *reinterpret_cast<u32x4*>(lds + (p * n + row) * stride + c) = x[p][u];
-    }
+        *reinterpret_cast<u32x4*>(lds + (p * kRows + row_of(lane, u)) * kStride + piece(lane, u)) = x[p][u];
     if constexpr (!kDense) {
-      constexpr int kScale = kMaxUnits * GPT * 32, kZero = kMaxUnits * GPT * 16;
-      char* s = lds + kXBytes;
 #pragma unroll
       for (int r2 = 0; r2 < NS; ++r2) {
-        if (lane < units * GPT * 2) *reinterpret_cast<u32x4*>(s + r2 * kScale + lane * 16) = scale[r2];
-        if (KIND == kU4 && lane < units * GPT)
-          *reinterpret_cast<u32x4*>(s + NS * kScale + r2 * kZero + lane * 16) = zero[r2];
+        float2* s = reinterpret_cast<float2*>(lds + kXBytes + r2 * kScale) + lane;
+#pragma unroll
+        for (int k = 0; k < kScaleWords; ++k)
+          if (lane + 64 * k < kUnits * GPT * 8)
+            s[64 * k] = float2{__uint_as_float(scale[r2][k] << 16), __uint_as_float(scale[r2][k] & 0xffff0000u)};
+        if (KIND == kU4 && lane < kUnits * GPT * 4) {
+          f32x4 z;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) z[c] = -16.f - static_cast<float>((zero[r2] >> (8 * c)) & 0xffu);
+          reinterpret_cast<f32x4*>(lds + kXBytes + kOff + r2 * kScale)[lane] = z;
+        }
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
   }
 
-  // 64 bytes' worth (step q) of unit i of the run, token tile t, part p.
-  __device__ inline u32x4 get(int i, int t, int p, int q, int n) const {
-    return *reinterpret_cast<const u32x4*>(lds + p * n * stride + at[t] + i * kUnitBytes + q * 64);
+  // 64 bytes' worth (step q) of unit i of the run, part p, of the row at `at`.
+  __device__ inline u32x4 get(int i, uint32_t at, int p, int q) const {
+    return *reinterpret_cast<const u32x4*>(lds + p * kRows * kStride + at + i * kUnitBytes + q * 64);
   }
-  __device__ inline uint2 get_scale(int i, int r, int g) const {
-    return reinterpret_cast<const uint2*>(lds + kXBytes + ((r * kMaxUnits + i) * GPT + g) * 32)[(threadIdx.x & 63) >> 4];
+  // Scales, and -(16 + z), of rows 4 quad .. 4 quad + 3 in group g of unit i, strip r.
+  __device__ inline f32x4 get_scale(int i, int r, int g, int quad) const {
+    return reinterpret_cast<const f32x4*>(lds + kXBytes + r * kScale + (i * GPT + g) * 64)[quad];
   }
-  __device__ inline uint32_t get_zero(int i, int r, int g) const {
-    return reinterpret_cast<const uint32_t*>(lds + kXBytes + NS * kMaxUnits * GPT * 32 +
-                                             ((r * kMaxUnits + i) * GPT + g) * 16)[(threadIdx.x & 63) >> 4];
+  __device__ inline f32x4 get_off(int i, int r, int g, int quad) const {
+    return reinterpret_cast<const f32x4*>(lds + kXBytes + kOff + r * kScale + (i * GPT + g) * 64)[quad];
   }
 };
 
+// LDS bytes of a wave: the larger of its kinds of run.
+template <WKind KIND, int GPT, int PARTS, int NS, bool WIDE>
+constexpr int kWaveLds =
+    std::max({Stage<KIND, GPT, PARTS, NS, 1, 1>::kBytes, Stage<KIND, GPT, PARTS, NS, 1, 4>::kBytes,
+              Stage<KIND, GPT, PARTS, NS, 1, 8>::kBytes,               Stage<KIND, GPT, PARTS, NS, 1, 16>::kBytes,
+              WIDE ? Stage<KIND, GPT, PARTS, NS, 2, 32>::kBytes : 0});
+
 // acc += unit i of the staged run times its weights.
-template <WKind KIND, int GPT, int PARTS, int NS, int NT>
-__device__ inline void multiply(const UnitW<KIND, NS>& u, const Stage<KIND, GPT, PARTS, NS, NT>& in, int i, int n,
+template <WKind KIND, int GPT, int PARTS, int NS, int NT, int ROWS>
+__device__ inline void multiply(const UnitW<KIND, NS>& u, const Stage<KIND, GPT, PARTS, NS, NT, ROWS>& in, int i,
                                 f32x4 (&acc)[NS][NT]) {
   if constexpr (is_dense(KIND)) {
     u32x4 x[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) x[t][q] = in.get(i, t, 0, q, n);
+      for (int q = 0; q < 2; ++q) x[t][q] = in.get(i, in.at[t], 0, q);
 #pragma unroll
     for (int r = 0; r < NS; ++r) {
       u32x4 a0, a1;
@@ -574,6 +679,15 @@ __device__ inline void multiply(const UnitW<KIND, NS>& u, const Stage<KIND, GPT,
     for (int c = 0; c < 8; ++c) ones[c] = static_cast<__bf16>(1.0f);
 #pragma unroll
     for (int g = 0; g < GPT; ++g) {
+      // One group after the other: with these marks neither its LDS reads nor its
+      // sums move past its neighbours', which would keep all groups' in registers.
+      uint32_t at[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        at[t] = in.at[t];
+        if (g % kMarkEvery<KIND, NS> == 0) asm volatile("" : "+v"(at[t]));
+      }
+      const int quad = g % kMarkEvery<KIND, NS> == 0 ? lane_here() >> 4 : (threadIdx.x & 63) >> 4;
       f32x4 sum[NS][NT] = {}, sx[NT] = {};
 #pragma unroll
       for (int st = g * kSteps; st < (g + 1) * kSteps; ++st) {
@@ -584,7 +698,7 @@ __device__ inline void multiply(const UnitW<KIND, NS>& u, const Stage<KIND, GPT,
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
-            const bf16x8 xv = __builtin_bit_cast(bf16x8, in.get(i, t, p, st, n));
+            const bf16x8 xv = __builtin_bit_cast(bf16x8, in.get(i, at[t], p, st));
 #pragma unroll
             for (int r = 0; r < NS; ++r)
               sum[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[r], xv, sum[r][t], 0, 0, 0);
@@ -593,22 +707,19 @@ __device__ inline void multiply(const UnitW<KIND, NS>& u, const Stage<KIND, GPT,
       }
 #pragma unroll
       for (int r = 0; r < NS; ++r) {
-        const uint2 sv = in.get_scale(i, r, g);
-        const float s[4] = {__uint_as_float(sv.x << 16), __uint_as_float(sv.x & 0xffff0000u),
-                            __uint_as_float(sv.y << 16), __uint_as_float(sv.y & 0xffff0000u)};
-        float off[4];
-        if constexpr (kU) {
-          const uint32_t z = in.get_zero(i, r, g);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) off[c] = 16.f + static_cast<float>((z >> (8 * c)) & 0xffu);
-        }
+        const f32x4 s = in.get_scale(i, r, g, quad);
+        f32x4 off = {};
+        if constexpr (kU) off = in.get_off(i, r, g, quad);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float v = kU ? fmaf(-off[c], sx[t][c], sum[r][t][c]) : sum[r][t][c];
+            const float v = kU ? fmaf(off[c], sx[t][c], sum[r][t][c]) : sum[r][t][c];
             acc[r][t][c] = fmaf(s[c], v, acc[r][t][c]);
           }
+        if ((g + 1) % kMarkEvery<KIND, NS> == 0)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(acc[r][t]));
       }
     }
   }
@@ -617,81 +728,95 @@ __device__ inline void multiply(const UnitW<KIND, NS>& u, const Stage<KIND, GPT,
 // Units j0 .. j1 - 1 of the strips. 8 KiB of weights a wave are in flight all
 // the time: each place of the ring is asked for again as soon as its unit is
 // multiplied (past the range the last unit, from the cache).
-template <WKind KIND, int GPT, int PARTS, int NS, int NT>
-__device__ inline void mac(const Strip<KIND> (&a)[NS], const Rows& x, int64_t K, int64_t j0, int64_t j1, char* lds,
-                           f32x4 (&acc)[NS][NT]) {
-  if (j0 >= j1) return;
-  constexpr int U = (is_dense(KIND) ? 4 : 8) / NS;
+template <WKind KIND, int GPT, int PARTS, int NS, int NT, int ROWS>
+__device__ inline void mac_run(const Strip<KIND> (&a)[NS], const RowList& list, int64_t K, int j0, int j1, char* lds,
+                               f32x4 (&acc)[NS][NT]) {
+  using Run = Stage<KIND, GPT, PARTS, NS, NT, ROWS>;
+  constexpr int U = 4 / NS, kUnits = Run::kUnits;
   UnitW<KIND, NS> w[U];
-  Stage<KIND, GPT, PARTS, NS, NT> in;
+#pragma unroll
+  for (int u = 0; u < U; ++u) load_weights(a, std::min(j0 + u, j1 - 1), w[u]);
+  Run in;
+  const Rows x = list.rows();
   in.init(lds, x);
   in.ask(a, x, K, j0, j1);
-#pragma unroll
-  for (int u = 0; u < U; ++u) load_weights(a, K, std::min(j0 + u, j1 - 1), w[u]);
-  int i = in.units;  // unit of the staged run
-  for (int64_t j = j0; j < j1; j += U) {
+  int i = 0;  // unit of the staged run, where a run has several rounds of the ring
+  for (int j = j0; j < j1; j += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (j + u < j1) {
-        if (i == in.units) {
-          in.put(x.n);
-          in.ask(a, x, K, std::min(j + u + in.units, j1), j1);
-          i = 0;
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        multiply<KIND, GPT, PARTS>(w[u], in, i, x.n, acc);
-        ++i;
-        __builtin_amdgcn_sched_barrier(0);
-        load_weights(a, K, std::min(j + u + U, j1 - 1), w[u]);
+      if (kUnits >= U ? u == 0 && i == 0 : u % kUnits == 0) {
+        in.put();
+        in.ask(a, x, K, j + u + kUnits, j1);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if (j + u < j1) multiply<KIND, GPT, PARTS>(w[u], in, kUnits >= U ? i + u : u % kUnits, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      load_weights(a, std::min(j + u + U, j1 - 1), w[u]);
     }
+    if (kUnits > U) i = (i + U) % kUnits;
   }
 }
 
-// The waves' sums of both strips, joined in wave order: thread tid gets element
-// i = tid % 4 of lane tid / 4 (feature 4 (l / 16) + i, token l % 16).
-template <int NT>
-__device__ inline void join(f32x4 (&acc)[2][NT], float (&out)[2][NT], f32x4* red) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __syncthreads();  // every wave is done with its staged x
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) red[((wave * 2 + r) * NT + t) * 64 + lane] = acc[r][t];
-  __syncthreads();
-  const float* f = reinterpret_cast<const float*>(red);
-#pragma unroll
-  for (int r = 0; r < 2; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float v = 0;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += f[((w * 2 + r) * NT + t) * 256 + threadIdx.x];
-      out[r][t] = v;
+template <WKind KIND, int GPT, int PARTS, int NS, int NT>
+__device__ inline void mac(const Strip<KIND> (&a)[NS], const RowList& list, int64_t K, int j0, int j1, char* lds,
+                           f32x4 (&acc)[NS][NT]) {
+  if (j0 >= j1) return;
+  if constexpr (NT == 1) {
+    if (list.n > (is_dense(KIND) ? 4 : 8))
+      mac_run<KIND, GPT, PARTS, NS, NT, 16>(a, list, K, j0, j1, lds, acc);
+    else if constexpr (is_dense(KIND))
+      mac_run<KIND, GPT, PARTS, NS, NT, 4>(a, list, K, j0, j1, lds, acc);
+    else {
+      if (list.n == 1)
+        mac_run<KIND, GPT, PARTS, NS, NT, 1>(a, list, K, j0, j1, lds, acc);
+      else if (list.n <= 4)
+        mac_run<KIND, GPT, PARTS, NS, NT, 4>(a, list, K, j0, j1, lds, acc);
+      else
+        mac_run<KIND, GPT, PARTS, NS, NT, 8>(a, list, K, j0, j1, lds, acc);
     }
-  __syncthreads();  // the LDS may be staged into again
+  } else {
+    mac_run<KIND, GPT, PARTS, NS, NT, 32>(a, list, K, j0, j1, lds, acc);
+  }
 }
 
-// out[r][t] of two strips: rows r0 of matrix m0 and r1 of m1 (expert e), for
-// the x rows given per lane, K the contraction length; its waves split K.
-template <WKind KIND, int GPT, int PARTS, int NT>
-__device__ inline void strip_pair(const WMat& m0, const WMat& m1, int64_t e, int64_t r0, int64_t r1, int64_t N,
-                                  int64_t K, const Rows& x, float (&out)[2][NT], char* lds) {
-  const int wave = uniform(threadIdx.x >> 6);
-  f32x4 acc[2][NT] = {};
-  const int64_t units = units_of<KIND>(K);
+// The W waves' sums of both strips, joined in wave order in the first wave's
+// registers; true for that wave.
+template <int W, int NT>
+__device__ inline bool join(f32x4 (&acc)[2][NT], f32x4* red) {
+  if constexpr (W > 1) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();  // every wave is done with its staged x
+    if (wave > 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) red[((wave * 2 + r) * NT + t) * 64 + lane] = acc[r][t];
+    }
+    __syncthreads();
+    if (wave > 0) return false;
+#pragma unroll
+    for (int w = 1; w < W; ++w)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] += red[((w * 2 + r) * NT + t) * 64 + lane];
+  }
+  return true;
+}
+
+// Two strips, rows r0 of matrix m0 and r1 of m1 (expert e), times the x rows
+// given over the whole contraction, K long, which the work-group's W waves
+// split. True for the wave that gets the sums.
+template <WKind KIND, int GPT, int PARTS, int W, int NT>
+__device__ inline bool strip_pair(const WMat& m0, const WMat& m1, int64_t e, int64_t r0, int64_t r1, int64_t N,
+                                  int64_t K, const RowList& x, f32x4 (&acc)[2][NT], char* lds) {
+  const int wave = W > 1 ? uniform(threadIdx.x >> 6) : 0;
+  const int units = units_of<KIND>(K);
   const Strip<KIND> a[2] = {strip_of<KIND, GPT>(m0, e, r0, N, K), strip_of<KIND, GPT>(m1, e, r1, N, K)};
-  mac<KIND, GPT, PARTS>(a, x, K, units * wave / kWaves, units * (wave + 1) / kWaves,
-                        lds + wave * Stage<KIND, GPT, PARTS, 2, NT>::kBytes, acc);
-  join<NT>(acc, out, reinterpret_cast<f32x4*>(lds));
-}
-
-// Rows row(c), c = 0 .. n - 1, of `stride` bytes each from base.
-template <typename F>
-__device__ inline Rows rows_of(const void* base, int64_t stride, int64_t part, int n, F&& row) {
-  const int lane = threadIdx.x & 63;
-  return Rows{static_cast<const char*>(base),
-              static_cast<uint32_t>(row(std::min(lane, n - 1))) * static_cast<uint32_t>(stride), n, part};
+  if constexpr (W > 1) __syncthreads();  // the sums of the pass before have been read
+  mac<KIND, GPT, PARTS>(a, x, K, units * wave / W, units * (wave + 1) / W,
+                        lds + wave * kWaveLds<KIND, GPT, PARTS, 2, (NT > 1)>, acc);
+  return join<W, NT>(acc, reinterpret_cast<f32x4*>(lds));
 }
 
 struct FewArgs {
@@ -707,31 +832,43 @@ struct FewArgs {
 };
 
 // h = silu(g) u of 16 features for an expert's tokens.
-template <WKind KIND, int GPT, int PARTS, int NT>
+template <WKind KIND, int GPT, int PARTS, int W, int NT>
 __device__ inline void gate_up_tile(const FewArgs& a, int64_t e, int p0, int n, int64_t f0, char* lds) {
   constexpr int kElem = sizeof(XType<KIND>);
-  const Rows x = rows_of(a.x, a.d * kElem, a.T * a.d * kElem, n, [&](int c) { return a.ls.token[p0 + c]; });
-  float v[2][NT];
-  strip_pair<KIND, GPT, PARTS, NT>(a.gate, a.up, e, f0, f0, a.f, a.d, x, v, lds);
-  const int l = threadIdx.x >> 2;
-  const int64_t feat = f0 + 4 * (l >> 4) + (threadIdx.x & 3);
+  const int lane = threadIdx.x & 63;
+  const RowList x = {span(a.x, a.T * a.d * kElem), a.d * kElem, a.T * a.d * kElem, n,
+                     a.ls.token[p0 + std::min(lane, n - 1)]};
+  f32x4 v[2][NT] = {};
+  if (!strip_pair<KIND, GPT, PARTS, W, NT>(a.gate, a.up, e, f0, f0, a.f, a.d, x, v, lds)) return;
+  const int64_t feat = f0 + 4 * (lane >> 4);  // of this lane's four; d_ff is a multiple of 4
+  if (feat >= a.f) return;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int c = t * 16 + (l & 15);
-    if (c >= n || feat >= a.f) continue;
-    const float g = v[0][t], u = v[1][t];
-    const float h = g / (1.f + expf(-g)) * u;
+    const int c = t * 16 + (lane & 15);
+    if (c >= n) continue;
+    f32x4 h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float g = v[0][t][i];
+      h[i] = g / (1.f + expf(-g)) * v[1][t][i];
+    }
     const int64_t at = (p0 + c) * a.ldh + feat;
     if constexpr (KIND == kDenseF32) {
-      static_cast<float*>(a.h)[at] = h;
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.h) + at) = h;
     } else if constexpr (PARTS == 1) {
-      static_cast<bf16_t*>(a.h)[at] = f32_to_bf16(h);  // as the layer rounds h between its two products
+      uint2 b;  // rounded as the layer rounds h between its two products
+      b.x = f32_to_bf16(h[0]) | static_cast<uint32_t>(f32_to_bf16(h[1])) << 16;
+      b.y = f32_to_bf16(h[2]) | static_cast<uint32_t>(f32_to_bf16(h[3])) << 16;
+      *reinterpret_cast<uint2*>(static_cast<bf16_t*>(a.h) + at) = b;
     } else {
       const int64_t part = static_cast<int64_t>(a.T) * a.k * a.ldh;
-      bf16_t q[3];
-      split3(h, q);
+      bf16_t q[4][3];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) static_cast<bf16_t*>(a.h)[i * part + at] = q[i];
+      for (int i = 0; i < 4; ++i) split3(h[i], q[i]);
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        *reinterpret_cast<uint2*>(static_cast<bf16_t*>(a.h) + j * part + at) =
+            uint2{q[0][j] | static_cast<uint32_t>(q[1][j]) << 16, q[2][j] | static_cast<uint32_t>(q[3][j]) << 16};
     }
   }
 }
@@ -753,20 +890,20 @@ __device__ inline void gate_up_tile(const FewArgs& a, int64_t e, int p0, int n, 
     }                                                                            \
   } while (0)
 
-// LDS bytes of a work-group that works on pairs of strips.
-template <WKind KIND, int GPT, int PARTS, bool WIDE>
-constexpr int kPairLds = kWaves * Stage<KIND, GPT, PARTS, 2, WIDE ? 2 : 1>::kBytes;
+// LDS words of a work-group of W waves that works on a pair of strips.
+template <WKind KIND, int GPT, int PARTS, bool WIDE, int W>
+constexpr int kPairLds = W * kWaveLds<KIND, GPT, PARTS, 2, WIDE> / 16;
 
-template <WKind KIND, int GPT, int PARTS, bool WIDE>
-__global__ __launch_bounds__(kThreads, waves_per_simd(KIND, PARTS, WIDE)) void few_gate_up_kernel(FewArgs a) {
-  __shared__ f32x4 lds[kPairLds<KIND, GPT, PARTS, WIDE> / 16];
+template <WKind KIND, int GPT, int PARTS, bool WIDE, int W>
+__global__ __launch_bounds__(W * 64, waves_per_simd(KIND, PARTS, WIDE)) void few_gate_up_kernel(FewArgs a) {
+  __shared__ f32x4 lds[kPairLds<KIND, GPT, PARTS, WIDE, W>];
   const int64_t ft = ceil_div(a.f, 16);
   const int64_t i = blockIdx.x / ft;
   const int n_act = *a.ls.n_act;  // the four loads together: past n_act the lists hold anything
   const int e = uniform(a.ls.act_e[i]), p0 = uniform(a.ls.act_off[i]), p1 = uniform(a.ls.act_off[i + 1]);
   if (i >= n_act) return;
-  MOE_BY_TOKENS(p0, p1 - p0,
-                (gate_up_tile<KIND, GPT, PARTS, NT>(a, e, p, n, (blockIdx.x % ft) * 16, reinterpret_cast<char*>(lds))));
+  MOE_BY_TOKENS(p0, p1 - p0, (gate_up_tile<KIND, GPT, PARTS, W, NT>(a, e, p, n, (blockIdx.x % ft) * 16,
+                                                                    reinterpret_cast<char*>(lds))));
 }
 
 // out for 16 of its columns: x plus the gate-weighted sums of all experts'
@@ -776,41 +913,62 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(KIND, PARTS, WIDE)) void f
 // gates, to its own sums of the T tokens in LDS, and these are joined in wave
 // order: no y goes to memory, nothing waits for another work-group.
 template <WKind KIND, int GPT, int PARTS, int NT>
-__device__ inline void down_run(const FewArgs& a, int64_t e, int p0, int n, int64_t c0, int64_t j0, int64_t j1,
-                                char* lds, float* sums) {
+__device__ inline void down_run(const FewArgs& a, int64_t e, int p0, int n, int64_t c0, int j0, int j1, char* lds,
+                                float* sums) {
   const int lane = threadIdx.x & 63;
   const int64_t row = a.ldh * sizeof(XType<KIND>);
-  const Rows x = rows_of(static_cast<const char*>(a.h) + p0 * row, row, a.T * a.k * row, n, [](int c) { return c; });
+  const RowList x = {span(static_cast<const char*>(a.h) + p0 * row, n * row), row, a.T * a.k * row, n,
+                     std::min(lane, n - 1)};
+  int token[NT];
+  float gate[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {  // on their way while the products are taken
+    const int c = p0 + std::min(t * 16 + (lane & 15), n - 1);
+    token[t] = a.ls.token[c];
+    gate[t] = a.ls.gate[c];
+  }
   f32x4 acc[1][NT] = {};
   const Strip<KIND> s[1] = {strip_of<KIND, GPT>(a.down, e, c0, a.d, a.f)};
   mac<KIND, GPT, PARTS>(s, x, a.f, j0, j1, lds, acc);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int c = t * 16 + (lane & 15);
-    if (c >= n) continue;
-    const float w = a.ls.gate[p0 + c];
-    f32x4* o = reinterpret_cast<f32x4*>(sums + a.ls.token[p0 + c] * 16) + (lane >> 4);
-    *o += w * acc[0][t];
-  }
+  for (int t = 0; t < NT; ++t)
+    if (t * 16 + (lane & 15) < n) {
+      f32x4* o = reinterpret_cast<f32x4*>(sums + token[t] * 16) + (lane >> 4);
+      *o += gate[t] * acc[0][t];
+    }
 }
 
 template <WKind KIND, int GPT, int PARTS, bool WIDE, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, is_dense(KIND) || !(WIDE || PARTS == 3) ? 4 : 2) void few_down_kernel(FewArgs a) {
-  constexpr int kStage = Stage<KIND, GPT, PARTS, 1, WIDE ? 2 : 1>::kBytes;
+__global__ __launch_bounds__(WAVES * 64, waves_per_simd(KIND, PARTS, WIDE)) void few_down_kernel(
+    FewArgs a) {
+  constexpr int kStage = kWaveLds<KIND, GPT, PARTS, 1, WIDE>;
   __shared__ f32x4 staged[WAVES * kStage / 16];
   extern __shared__ f32x4 all_sums_[];  // [WAVES][T][16] floats
   float* all_sums = reinterpret_cast<float*>(all_sums_);
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   float* sums = all_sums + wave * a.T * 16;
   char* lds = reinterpret_cast<char*>(staged) + wave * kStage;
+  // the first 64 experts of the list, on their way together with its length
+  const int first_e = a.ls.act_e[std::min(lane, a.E - 1)], first_p = a.ls.act_off[std::min(lane, a.E)];
+  const int after_p = a.ls.act_off[std::min(lane + 1, a.E)];
   for (int i = lane; i < a.T * 16; i += 64) sums[i] = 0.f;
   const int64_t c0 = blockIdx.x * 16ll;
-  const int64_t units = units_of<KIND>(a.f), total = units * uniform(*a.ls.n_act);
-  const int64_t end = total * (wave + 1) / WAVES;
-  for (int64_t u = total * wave / WAVES; u < end;) {
-    const int64_t i = u / units, j0 = u % units, j1 = std::min(units, j0 + end - u);
-    const int e = uniform(a.ls.act_e[i]), p0 = uniform(a.ls.act_off[i]);
-    MOE_BY_TOKENS(p0, uniform(a.ls.act_off[i + 1]) - p0, (down_run<KIND, GPT, PARTS, NT>(a, e, p, n, c0, j0, j1, lds, sums)));
+  const int units = units_of<KIND>(a.f);
+  const int64_t total = static_cast<int64_t>(units) * uniform(*a.ls.n_act);  // below 2^31: 2^18 units of 1024 experts
+  const int end = static_cast<int>(total * (wave + 1) / WAVES);
+  for (int u = static_cast<int>(total * wave / WAVES); u < end;) {
+    const int i = u / units, j0 = u % units, j1 = std::min(units, j0 + end - u);
+    int e, p0, p1;
+    if (i < 64) {
+      e = __builtin_amdgcn_readlane(first_e, i);
+      p0 = __builtin_amdgcn_readlane(first_p, i);
+      p1 = __builtin_amdgcn_readlane(after_p, i);
+    } else {
+      e = uniform(a.ls.act_e[i]);
+      p0 = uniform(a.ls.act_off[i]);
+      p1 = uniform(a.ls.act_off[i + 1]);
+    }
+    MOE_BY_TOKENS(p0, p1 - p0, (down_run<KIND, GPT, PARTS, NT>(a, e, p, n, c0, j0, j1, lds, sums)));
     u += j1 - j0;
   }
   __syncthreads();
@@ -884,43 +1042,46 @@ __device__ inline void group_rows(const int32_t* expert, int R, int E, RowGroups
   __syncthreads();
 }
 
-template <WKind KIND, int GPT, int PARTS, int NT>
-__device__ inline void matvec_tile(const MatvecArgs& a, const RowGroups& g, int i, int p0, int n, int64_t n0,
+template <WKind KIND, int GPT, int PARTS, int W, int NT>
+__device__ inline void matvec_tile(const MatvecArgs& a, const RowGroups& g, int e, int p0, int n, int64_t n0,
                                    char* lds) {
-  const Rows x = rows_of(a.x, a.K * 2, a.R * a.K * 2, n, [&](int c) { return g.row[p0 + c]; });
-  float v[2][NT];
+  const int lane = threadIdx.x & 63;
+  const RowList x = {span(a.x, a.R * a.K * 2), a.K * 2, a.R * a.K * 2, n, g.row[p0 + std::min(lane, n - 1)]};
   // the last 16 rows of a matrix may have no 16 after them: they are read twice
   const int64_t n1 = n0 + 16 < a.N ? n0 + 16 : n0;
-  strip_pair<KIND, GPT, PARTS, NT>(a.w, a.w, uniform(g.e[i]), n0, n1, a.N, a.K, x, v, lds);
-  const int l = threadIdx.x >> 2;
+  f32x4 v[2][NT] = {};
+  if (!strip_pair<KIND, GPT, PARTS, W, NT>(a.w, a.w, e, n0, n1, a.N, a.K, x, v, lds)) return;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int c = t * 16 + (l & 15);
+    const int c = t * 16 + (lane & 15);
     if (c >= n) continue;
+    const int64_t row = g.row[p0 + c] * a.N;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t col = n0 + 16 * r + 4 * (l >> 4) + (threadIdx.x & 3);
-      if (col >= a.N) continue;
-      const int64_t at = g.row[p0 + c] * a.N + col;
-      if constexpr (PARTS == 1)
-        static_cast<bf16_t*>(a.out)[at] = f32_to_bf16(v[r][t]);
-      else
-        static_cast<float*>(a.out)[at] = v[r][t];
-    }
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t col = n0 + 16 * r + 4 * (lane >> 4) + i;
+        if (col >= a.N) continue;
+        if constexpr (PARTS == 1)
+          static_cast<bf16_t*>(a.out)[row + col] = f32_to_bf16(v[r][t][i]);
+        else
+          static_cast<float*>(a.out)[row + col] = v[r][t][i];
+      }
   }
 }
 
-template <WKind KIND, int GPT, int PARTS, bool WIDE>
-__global__ __launch_bounds__(kThreads, waves_per_simd(KIND, PARTS, WIDE)) void matvec_kernel(MatvecArgs a) {
-  __shared__ f32x4 lds[kPairLds<KIND, GPT, PARTS, WIDE> / 16];
+template <WKind KIND, int GPT, int PARTS, bool WIDE, int W>
+__global__ __launch_bounds__(W * 64, waves_per_simd(KIND, PARTS, WIDE)) void matvec_kernel(MatvecArgs a) {
+  __shared__ f32x4 lds[kPairLds<KIND, GPT, PARTS, WIDE, W>];
   __shared__ RowGroups g;
   group_rows(a.expert, a.R, a.E, g);
   const int64_t nt = ceil_div(a.N, 32);
   const int i = static_cast<int>(blockIdx.x / nt);
   if (i >= g.n) return;
-  const int p0 = uniform(g.off[i]);
+  const int e = uniform(g.e[i]), p0 = uniform(g.off[i]);
   MOE_BY_TOKENS(p0, uniform(g.off[i + 1]) - p0,
-                (matvec_tile<KIND, GPT, PARTS, NT>(a, g, i, p, n, (blockIdx.x % nt) * 32, reinterpret_cast<char*>(lds))));
+                (matvec_tile<KIND, GPT, PARTS, W, NT>(a, g, e, p, n, (blockIdx.x % nt) * 32,
+                                                      reinterpret_cast<char*>(lds))));
 }
 
 __global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t n, bf16_t* parts) {
@@ -957,12 +1118,32 @@ hipError_t by_weights(const FewWeights& w, bool bf16, bool wide, F&& g) {
 
 }  // namespace
 
+// Experts that T tokens with k of E each hit, if each choice were as likely.
+double expected_distinct(int E, int k, int T) { return E * (1 - std::pow(1 - static_cast<double>(k) / E, T)); }
+
+// f(waves of a work-group) for about `items` pairs of strips. The chip holds
+// 4096 waves: with few items more waves share one, so that the memory has
+// enough to do. With very many, one wave alone spares the joining; between, its
+// long items would leave the last round's waves alone with the memory (1.2
+// rounds of single waves: 254 us instead of 219 with four).
+template <int PARTS, typename F>
+void by_waves(double items, F&& f) {
+  if (PARTS == 1 && items <= 512)
+    f(std::integral_constant<int, 8>{});
+  else if (items > 1024 && items <= 2048)
+    f(std::integral_constant<int, 2>{});
+  else if (items <= 16384)
+    f(std::integral_constant<int, 4>{});
+  else
+    f(std::integral_constant<int, 1>{});
+}
+
 // Slices of d for the router scores: enough work-groups to spread W_router
 // over the chip, slices of 512 columns at least, and few enough partial scores
 // to add up.
 int few_router_splits(int64_t T, int64_t d, int E) {
   const int64_t tiles = std::max<int64_t>(1, ceil_div(E, 16) * ceil_div(T, 16));
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, d / 512, 256 / tiles})));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kFewMaxSplits, d / 512, 256 / tiles})));
 }
 
 hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
@@ -970,9 +1151,9 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
   const int S = few_router_splits(L.T, L.d, L.E);
   const dim3 rgrid(static_cast<unsigned>(ceil_div(L.E, 16)), static_cast<unsigned>(ceil_div(L.T, 16)), S);
   if (bf16)
-    few_router_kernel<true><<<rgrid, dim3(kThreads), 0, s>>>(L.x, L.wr, L.T, L.E, L.d, S, L.part, nullptr, nullptr, 0);
+    few_router_kernel<true><<<rgrid, dim3(kRouterThreads), 0, s>>>(L.x, L.wr, L.T, L.E, L.d, S, L.part, nullptr);
   else
-    few_router_kernel<false><<<rgrid, dim3(kThreads), 0, s>>>(L.x, L.wr, L.T, L.E, L.d, S, L.part, L.xparts, nullptr, 0);
+    few_router_kernel<false><<<rgrid, dim3(kRouterThreads), 0, s>>>(L.x, L.wr, L.T, L.E, L.d, S, L.part, L.xparts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const RouteOut ro{L.idx, L.w, L.slot, L.routed, L.kept, L.send, L.totals};
@@ -992,9 +1173,9 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
   a.f = L.f;
   a.x = L.xparts ? static_cast<const void*>(L.xparts) : L.x;
   a.x_res = L.x;
-  a.gate = {L.wt.w[0], static_cast<const bf16_t*>(L.wt.scale[0]), static_cast<const uint8_t*>(L.wt.zero[0])};
-  a.up = {L.wt.w[1], static_cast<const bf16_t*>(L.wt.scale[1]), static_cast<const uint8_t*>(L.wt.zero[1])};
-  a.down = {L.wt.w[2], static_cast<const bf16_t*>(L.wt.scale[2]), static_cast<const uint8_t*>(L.wt.zero[2])};
+  a.gate = {L.E, L.wt.w[0], static_cast<const bf16_t*>(L.wt.scale[0]), static_cast<const uint8_t*>(L.wt.zero[0])};
+  a.up = {L.E, L.wt.w[1], static_cast<const bf16_t*>(L.wt.scale[1]), static_cast<const uint8_t*>(L.wt.zero[1])};
+  a.down = {L.E, L.wt.w[2], static_cast<const bf16_t*>(L.wt.scale[2]), static_cast<const uint8_t*>(L.wt.zero[2])};
   a.ls = L.ls;
   a.h = L.h;
   a.ldh = few_ld_h(L.f);
@@ -1007,13 +1188,17 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
     constexpr WKind kKind = decltype(kind)::value;
     constexpr int kGpt = decltype(gpt)::value, kParts = decltype(parts)::value;
     constexpr bool kWide = decltype(two)::value;
-    few_gate_up_kernel<kKind, kGpt, kParts, kWide>
-        <<<dim3(static_cast<unsigned>(act * ceil_div(L.f, 16))), dim3(kThreads), 0, s>>>(a);
-    constexpr int kMany = kParts == 1 && !kWide ? 16 : 8;
-    // enough waves to cover the memory's latency with few columns too
-    if (strips > 256)
-      few_down_kernel<kKind, kGpt, kParts, kWide, 8>
-          <<<dim3(static_cast<unsigned>(strips)), dim3(512), 8 * L.T * 64, s>>>(a);
+    const int64_t ft = ceil_div(L.f, 16);
+    by_waves<kParts>(expected_distinct(L.E, L.k, L.T) * ft, [&](auto waves) {
+      constexpr int W = decltype(waves)::value;
+      few_gate_up_kernel<kKind, kGpt, kParts, kWide, W>
+          <<<dim3(static_cast<unsigned>(act * ft)), dim3(W * 64), 0, s>>>(a);
+    });
+    // two work-groups a CU; with few strips one of twice the waves, where their sums of the tokens fit the LDS
+    constexpr int kSome = 2 * waves_per_simd(kKind, kParts, kWide), kMany = kParts == 1 ? 2 * kSome : kSome;
+    if (strips > 256 || L.T > 32)
+      few_down_kernel<kKind, kGpt, kParts, kWide, kSome>
+          <<<dim3(static_cast<unsigned>(strips)), dim3(kSome * 64), kSome * L.T * 64, s>>>(a);
     else
       few_down_kernel<kKind, kGpt, kParts, kWide, kMany>
           <<<dim3(static_cast<unsigned>(strips)), dim3(kMany * 64), kMany * L.T * 64, s>>>(a);
@@ -1036,14 +1221,20 @@ hipError_t launch_q4_matvec(const void* x, bool bf16, const int32_t* expert, con
   a.K = K;
   a.x = bf16 ? static_cast<const bf16_t*>(x) : parts;
   a.expert = expert;
-  a.w = {w.w[0], static_cast<const bf16_t*>(w.scale[0]), static_cast<const uint8_t*>(w.zero[0])};
+  a.w = {E, w.w[0], static_cast<const bf16_t*>(w.scale[0]), static_cast<const uint8_t*>(w.zero[0])};
   a.out = out;
   const int64_t groups = expert ? std::min(E, R) : 1;
   return by_weights(w, bf16, R > 8 * groups, [&](auto kind, auto gpt, auto parts_, auto two) {
     constexpr WKind kKind = decltype(kind)::value;
     if constexpr (kKind == kU4 || kKind == kE2m1) {
-      matvec_kernel<kKind, decltype(gpt)::value, decltype(parts_)::value, decltype(two)::value>
-          <<<dim3(static_cast<unsigned>(groups * ceil_div(N, 32))), dim3(kThreads), 0, s>>>(a);
+      constexpr int kGpt = decltype(gpt)::value, kParts = decltype(parts_)::value;
+      constexpr bool kWide = decltype(two)::value;
+      const int64_t nt = ceil_div(N, 32);
+      by_waves<kParts>((expert ? expected_distinct(E, 1, R) : 1) * nt, [&](auto waves) {
+        constexpr int W = decltype(waves)::value;
+        matvec_kernel<kKind, kGpt, kParts, kWide, W>
+            <<<dim3(static_cast<unsigned>(groups * nt)), dim3(W * 64), 0, s>>>(a);
+      });
       return hipGetLastError();
     } else {
       return hipErrorInvalidValue;

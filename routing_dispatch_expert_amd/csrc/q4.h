@@ -23,9 +23,14 @@ template <bool U4>
 __device__ inline bf16x8 q4_decode(uint32_t w) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   if constexpr (U4) {
-    constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u;
-    const u32x4 v = {((w << 3) & kMask) | kSixteen, ((w >> 1) & kMask) | kSixteen, ((w >> 5) & kMask) | kSixteen,
-                     ((w >> 9) & kMask) | kSixteen};
+    // and-or by hand: the compiler splits it in two, as both constants are literals
+    const uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+    u32x4 v;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t shifted = p == 0 ? w << 3 : w >> (4 * p - 3);
+      asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(v[p]) : "v"(shifted), "s"(mask), "v"(sixteen));
+    }
     return __builtin_bit_cast(bf16x8, v);
   } else {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

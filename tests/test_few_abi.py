@@ -44,8 +44,8 @@ LAYER = [
     (dict(E=8, k=4, P=4, max_ranks=1), INVALID), (dict(E=256, k=8, P=128, max_ranks=4), UNSUPPORTED),
     (dict(T=65), UNSUPPORTED), (dict(T=1 << 40), UNSUPPORTED), (dict(E=1025), UNSUPPORTED),
     (dict(E=64, k=33), UNSUPPORTED), (dict(d=12), UNSUPPORTED), (dict(d_ff=100), UNSUPPORTED),
-    (dict(d=1 << 20, d_ff=1 << 20), UNSUPPORTED), (dict(d=(1 << 23) + 8, d_ff=8), UNSUPPORTED),
-    (dict(d_ff=(1 << 23) + 8, d=8), UNSUPPORTED), (dict(workspace=None), WORKSPACE),
+    (dict(d=1 << 20, d_ff=1 << 20), UNSUPPORTED), (dict(d=(1 << 22) + 8, d_ff=8), UNSUPPORTED),
+    (dict(d_ff=(1 << 22) + 8, d=8), UNSUPPORTED), (dict(workspace=None), WORKSPACE),
     (dict(workspace_bytes=100), WORKSPACE), (dict(workspace=FAKE * 3 + 8), WORKSPACE),
     (dict(stats=dict(STATS, buckets=FAKE)), INVALID), (dict(stats=dict(STATS, src=FAKE)), INVALID),
     (dict(stats=dict(STATS, instance=FAKE)), INVALID), (dict(stats=dict(STATS, g=FAKE, u=FAKE, h=FAKE)), INVALID),
@@ -143,7 +143,7 @@ def test_q4_argument_refusals():
     refused(INVALID, lambda: mv(FAKE, None, q4(), -1, 2, 32, 128, "bf16", FAKE * 2, None, 0))
     refused(INVALID, lambda: mv(FAKE, None, q4(), 4, 2, 32, 128, "bf16", FAKE + 64, None, 0))
     refused(INVALID, lambda: mv(FAKE + 2, None, q4(), 4, 2, 32, 128, "bf16", FAKE * 2, None, 0))
-    refused(UNSUPPORTED, lambda: mv(FAKE, None, q4(), 4, 1, 8, (1 << 23) + 8, "bf16", FAKE << 10, None, 0))
+    refused(UNSUPPORTED, lambda: mv(FAKE, None, q4(), 4, 1, 8, (1 << 22) + 8, "bf16", FAKE << 10, None, 0))
     refused(UNSUPPORTED, lambda: mv(FAKE, None, q4(), 65, 2, 32, 128, "bf16", FAKE * 2, None, 0))
     refused(WORKSPACE, lambda: mv(FAKE, None, q4(), 4, 2, 32, 128, "f32", FAKE * 2, None, 0))
     refused(WORKSPACE, lambda: mv(FAKE, None, q4(), 4, 2, 32, 128, "f32", FAKE * 2, FAKE * 3 + 16, 1 << 30))
