@@ -150,89 +150,107 @@ struct RouteOut {
   int64_t* totals;  // or NULL
 };
 
+struct Scores {
+  const double* part;  // [S][T][E]
+  int S;
+  const float* bias;
+  int T, E, k, P, M;
+};
+
+// Token t's experts and gates, by one wave: lane j < k gets the j-th best
+// expert and its gate. rbest: the wave's LDS for 64 ranks' best scores.
 template <int NE>  // scores a lane holds: E <= 64 NE
-__global__ __launch_bounds__(1024) void few_route_kernel(const double* __restrict__ part, int S,
-                                                         const float* __restrict__ bias, int T, int E, int k, int P,
-                                                         int M, int64_t C, int64_t row_bytes, RouteOut o, FewLists ls) {
+__device__ inline void choose(const Scores& a, int t, unsigned long long* rbest, int* expert, float* gate) {
+  const int lane = threadIdx.x & 63, T = a.T, E = a.E, k = a.k, P = a.P, M = a.M, S = a.S, per = E / P;
+  const double* __restrict__ part = a.part;
+  const float* __restrict__ bias = a.bias;
+  uint64_t key[NE];
+  constexpr int G = NE < 4 ? NE : 4;  // experts a lane whose partial scores are fetched together
+#pragma unroll
+  for (int i0 = 0; i0 < NE; i0 += G) {
+    double v[kFewMaxSplits][G];
+#pragma unroll
+    for (int s = 0; s < kFewMaxSplits; ++s)
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int e = lane + 64 * (i0 + i);
+        v[s][i] = 0;
+        if (s < S && e < E) v[s][i] = part[(static_cast<int64_t>(s) * T + t) * E + e];
+      }
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int e = lane + 64 * (i0 + i);
+      double sum = v[0][i];
+#pragma unroll
+      for (int s = 1; s < kFewMaxSplits; ++s) sum += v[s][i];
+      if (bias && e < E) sum += static_cast<double>(bias[e]);
+      key[i0 + i] = e < E ? order_key(sum) : 0;
+    }
+  }
+  if (M > 0 && M < P) {  // P <= 64: lane p holds rank p's best score
+    rbest[lane] = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (lane + 64 * i < E) atomicMax(&rbest[(lane + 64 * i) / per], static_cast<unsigned long long>(key[i]));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    const uint64_t mine = rbest[lane];
+    int ahead = 0;  // ranks ahead of mine: better score, or equal score and lower index
+    for (int p = 0; p < P; ++p) {
+      const uint64_t q = rbest[p];
+      ahead += (q > mine || (q == mine && p < lane)) ? 1 : 0;
+    }
+    const uint64_t allowed = __ballot(lane < P && ahead < M);
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (lane + 64 * i < E && !((allowed >> ((lane + 64 * i) / per)) & 1)) key[i] = 0;
+  }
+  uint64_t sel = 0, top = 0;
+  int sel_e = 0;
+  for (int r = 0; r < k; ++r) {
+    uint64_t mine = key[0], best;
+    int me = lane, e, win;
+#pragma unroll
+    for (int i = 1; i < NE; ++i)
+      if (key[i] > mine) {
+        mine = key[i];
+        me = lane + 64 * i;
+      }
+    wave_best(mine, me, &best, &e, &win);
+    if (r == 0) top = best;
+    if (lane == r) {
+      sel = best;
+      sel_e = e;
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (e == lane + 64 * i) key[i] = 0;
+  }
+  const double z = lane < k ? exp(key_value(sel) - key_value(top)) : 0.0;
+  double sum = z;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+  *expert = sel_e;
+  *gate = static_cast<float>(z / sum);
+}
+
+template <int NE>
+__global__ __launch_bounds__(1024) void few_route_kernel(Scores sc, int64_t C, int64_t row_bytes, RouteOut o,
+                                                         FewLists ls) {
   __shared__ int cnt[kFewMaxE], ecp[kFewMaxCopies], rank[kFewMaxCopies], scratch[kRankChunkInts];
   __shared__ unsigned long long rbest[16][64];
   __shared__ int wsum[17], send_s[64], dropped_tokens;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = E / P;
-  const bool limit = M > 0 && M < P;
+  const int T = sc.T, E = sc.E, k = sc.k, P = sc.P, per = E / P;
   for (int e = tid; e < E; e += 1024) cnt[e] = 0;
   if (tid == 0) dropped_tokens = 0;
-
   for (int t = wave; t < T; t += 16) {
-    uint64_t key[NE];
-    constexpr int G = NE < 4 ? NE : 4;  // experts a lane whose partial scores are fetched together
-#pragma unroll
-    for (int i0 = 0; i0 < NE; i0 += G) {
-      double v[kFewMaxSplits][G];
-#pragma unroll
-      for (int s = 0; s < kFewMaxSplits; ++s)
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          const int e = lane + 64 * (i0 + i);
-          v[s][i] = 0;
-          if (s < S && e < E) v[s][i] = part[(static_cast<int64_t>(s) * T + t) * E + e];
-        }
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const int e = lane + 64 * (i0 + i);
-        double sum = v[0][i];
-#pragma unroll
-        for (int s = 1; s < kFewMaxSplits; ++s) sum += v[s][i];
-        if (bias && e < E) sum += static_cast<double>(bias[e]);
-        key[i0 + i] = e < E ? order_key(sum) : 0;
-      }
-    }
-    if (limit) {  // P <= 64: lane p holds rank p's best score
-      rbest[wave][lane] = 0;
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (lane + 64 * i < E) atomicMax(&rbest[wave][(lane + 64 * i) / per], static_cast<unsigned long long>(key[i]));
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-      const uint64_t mine = rbest[wave][lane];
-      int ahead = 0;  // ranks ahead of mine: better score, or equal score and lower index
-      for (int p = 0; p < P; ++p) {
-        const uint64_t q = rbest[wave][p];
-        ahead += (q > mine || (q == mine && p < lane)) ? 1 : 0;
-      }
-      const uint64_t allowed = __ballot(lane < P && ahead < M);
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (lane + 64 * i < E && !((allowed >> ((lane + 64 * i) / per)) & 1)) key[i] = 0;
-    }
-    uint64_t sel = 0, top = 0;
-    int sel_e = 0;
-    for (int r = 0; r < k; ++r) {
-      uint64_t mine = key[0], best;
-      int me = lane, e, win;
-#pragma unroll
-      for (int i = 1; i < NE; ++i)
-        if (key[i] > mine) {
-          mine = key[i];
-          me = lane + 64 * i;
-        }
-      wave_best(mine, me, &best, &e, &win);
-      if (r == 0) top = best;
-      if (lane == r) {
-        sel = best;
-        sel_e = e;
-      }
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (e == lane + 64 * i) key[i] = 0;
-    }
-    const double z = lane < k ? exp(key_value(sel) - key_value(top)) : 0.0;
-    double sum = z;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    int e;
+    float w;
+    choose<NE>(sc, t, rbest[wave], &e, &w);
     if (lane < k) {
-      o.idx[t * k + lane] = sel_e;
-      o.w[t * k + lane] = static_cast<float>(z / sum);
-      ecp[t * k + lane] = sel_e;
+      o.idx[t * k + lane] = e;
+      o.w[t * k + lane] = w;
+      ecp[t * k + lane] = e;
     }
   }
   __syncthreads();
@@ -323,6 +341,82 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const double* __restric
   }
 }
 
+// The same for at most 64 copies (T k <= 64) and 64 ranks: one wave holds all
+// copies and takes an expert's copies at a time, by a ballot, in place of the
+// larger kernel's scans and their barriers.
+template <int NE>
+__global__ __launch_bounds__(1024) void few_route_small_kernel(Scores sc, int64_t C, int64_t row_bytes, RouteOut o,
+                                                               FewLists ls) {
+  __shared__ int ecp[64], send_s[64];
+  __shared__ float gate[64];
+  __shared__ unsigned long long rbest[16][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int T = sc.T, E = sc.E, k = sc.k, P = sc.P, n = T * k;
+  for (int e = tid; e < E; e += blockDim.x) {
+    if (o.routed) o.routed[e] = 0;
+    if (o.kept) o.kept[e] = 0;
+  }
+  if (tid < 64) send_s[tid] = 0;
+  for (int t = wave; t < T; t += waves) {
+    int e;
+    float w;
+    choose<NE>(sc, t, rbest[wave], &e, &w);
+    if (lane < k) {
+      o.idx[t * k + lane] = e;
+      o.w[t * k + lane] = w;
+      ecp[t * k + lane] = e;
+      gate[t * k + lane] = w;
+    }
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  const bool in = lane < n;
+  const int e = in ? ecp[lane] : -1;
+  const unsigned long long below = (1ull << lane) - 1ull;
+  int experts = 0, total = 0;  // experts listed so far (by their first copies), and their kept copies
+  for (unsigned long long left = __ballot(in); left;) {
+    const int its = __builtin_amdgcn_readlane(e, __ffsll(left) - 1);
+    const unsigned long long mine = __ballot(e == its);
+    const int rank = __popcll(mine & below), copies = __popcll(mine);
+    const int kept = static_cast<int>(std::min<int64_t>(copies, C));  // C >= 1: an expert with copies keeps its first
+    if (e == its) {
+      if (rank < kept) {
+        ls.token[total + rank] = lane / k;
+        ls.gate[total + rank] = gate[lane];
+      }
+      if (o.slot) o.slot[lane] = rank < kept ? rank : -1;
+      if (rank >= kept) ecp[lane] = -1;  // dropped
+      if (rank == 0) {
+        ls.act_e[experts] = e;
+        ls.act_off[experts] = total;
+        if (o.routed) o.routed[e] = copies;
+        if (o.kept) o.kept[e] = kept;
+        atomicAdd(&send_s[e / (E / P)], kept);  // order-free
+      }
+    }
+    ++experts;
+    total += kept;
+    left &= ~mine;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  if (o.send && lane < P) o.send[lane] = send_s[lane];
+  // tokens none of whose k copies is kept
+  bool lost = lane < T;
+  if (lost)
+    for (int j = 0; j < k; ++j) lost &= ecp[lane * k + j] < 0;
+  const int lost_tokens = __popcll(__ballot(lost));
+  if (lane == 0) {
+    *ls.n_act = experts;
+    ls.act_off[experts] = total;
+    if (o.totals) {
+      o.totals[0] = n - total;
+      o.totals[1] = lost_tokens;
+      o.totals[2] = E * C - total;
+      o.totals[3] = static_cast<int64_t>(total - send_s[0]) * row_bytes;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Products of NS strips of 16 weight rows with NT tiles of 16 rows of x over a
 // range of the contraction: acc[r][t] += W_r x_t^T, one 16 x 16 tile in the
@@ -335,7 +429,7 @@ constexpr bool is_dense(WKind k) { return k == kDenseBf16 || k == kDenseF32; }
 
 // Waves a SIMD that the registers are cut for: as many as fit without spills,
 // whose own loads and stores would make every wait one for all loads in flight.
-constexpr int waves_per_simd(WKind k, int parts, bool wide) { return parts == 3 ? 2 : wide ? 3 : 4; }
+constexpr int waves_per_simd(WKind, int parts, bool wide) { return parts == 3 ? 2 : wide ? 3 : 4; }
 
 template <WKind KIND>
 using XType = std::conditional_t<KIND == kDenseF32, float, bf16_t>;
@@ -459,25 +553,11 @@ __device__ inline Strip<KIND> strip_of(const WMat& m, int64_t e, int64_t r0, int
 template <WKind KIND, int NS>
 constexpr int kMarkEvery = NS == 1 ? (KIND == kU4 ? 2 : 4) : 1;
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 __device__ inline u32x4 load_once(const Span& s, uint32_t lane_off, uint32_t off) {
   return __builtin_bit_cast(u32x4, s.load16<true>(lane_off, off));
 }
 __device__ inline u32x4 load_kept(const Span& s, uint32_t lane_off, uint32_t off = 0) {
   return __builtin_bit_cast(u32x4, s.load16<false>(lane_off, off));
-}
-
-// The A operands of a line's two steps from the loads of rows 0 - 7 and 8 - 15:
-// step 0 wants piece l / 16 of row l % 16, so lanes 8 - 15 of every 16 take
-// the other load's lanes 0 - 7; step 1 the other way round.
-__device__ inline void operands(u32x4 lo, u32x4 hi, u32x4& a0, u32x4& a1) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    constexpr int kRotate8 = 0x128;
-    a0[i] = __builtin_amdgcn_update_dpp(lo[i], hi[i], kRotate8, 0xf, 0xc, false);
-    a1[i] = __builtin_amdgcn_update_dpp(hi[i], lo[i], kRotate8, 0xf, 0x3, false);
-  }
 }
 
 template <WKind KIND>
@@ -725,8 +805,8 @@ __device__ inline void multiply(const UnitW<KIND, NS>& u, const Stage<KIND, GPT,
   }
 }
 
-// Units j0 .. j1 - 1 of the strips. 8 KiB of weights a wave are in flight all
-// the time: each place of the ring is asked for again as soon as its unit is
+// Units j0 .. j1 - 1 of the strips. 4 KiB (4-bit) or 8 KiB (dense) of weights a
+// wave are in flight all the time: each place of the ring is asked for again as soon as its unit is
 // multiplied (past the range the last unit, from the cache).
 template <WKind KIND, int GPT, int PARTS, int NS, int NT, int ROWS>
 __device__ inline void mac_run(const Strip<KIND> (&a)[NS], const RowList& list, int64_t K, int j0, int j1, char* lds,
@@ -1158,12 +1238,21 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
   if (e != hipSuccess) return e;
   const RouteOut ro{L.idx, L.w, L.slot, L.routed, L.kept, L.send, L.totals};
   const int64_t row = L.d * (bf16 ? 2 : 4);
+  const Scores sc{L.part, S, L.bias, L.T, L.E, L.k, L.P, L.M};
+  const bool small = L.T * L.k <= 64 && L.P <= 64;
+  auto route = [&](auto ne) {
+    constexpr int NE = decltype(ne)::value;
+    if (small)
+      few_route_small_kernel<NE><<<dim3(1), dim3(64 * std::min(L.T, 16)), 0, s>>>(sc, L.C, row, ro, L.ls);
+    else
+      few_route_kernel<NE><<<dim3(1), dim3(1024), 0, s>>>(sc, L.C, row, ro, L.ls);
+  };
   if (L.E <= 64)
-    few_route_kernel<1><<<dim3(1), dim3(1024), 0, s>>>(L.part, S, L.bias, L.T, L.E, L.k, L.P, L.M, L.C, row, ro, L.ls);
+    route(std::integral_constant<int, 1>{});
   else if (L.E <= 256)
-    few_route_kernel<4><<<dim3(1), dim3(1024), 0, s>>>(L.part, S, L.bias, L.T, L.E, L.k, L.P, L.M, L.C, row, ro, L.ls);
+    route(std::integral_constant<int, 4>{});
   else
-    few_route_kernel<16><<<dim3(1), dim3(1024), 0, s>>>(L.part, S, L.bias, L.T, L.E, L.k, L.P, L.M, L.C, row, ro, L.ls);
+    route(std::integral_constant<int, 16>{});
   if ((e = hipGetLastError()) != hipSuccess) return e;
   FewArgs a;
   a.T = L.T;

@@ -6,6 +6,20 @@
 
 namespace moe {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The A operands of a line's two steps from the loads of rows 0 - 7 and 8 - 15:
+// step 0 wants piece l / 16 of row l % 16, so lanes 8 - 15 of every 16 take
+// the other load's lanes 0 - 7; step 1 the other way round.
+__device__ inline void operands(u32x4 lo, u32x4 hi, u32x4& a0, u32x4& a1) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    constexpr int kRotate8 = 0x128;
+    a0[i] = __builtin_amdgcn_update_dpp(lo[i], hi[i], kRotate8, 0xf, 0xc, false);
+    a1[i] = __builtin_amdgcn_update_dpp(hi[i], lo[i], kRotate8, 0xf, 0x3, false);
+  }
+}
+
 // A matrix stack [E, N, K] in 4 bits (the layout of moe_q4_t in moe.h): tiles
 // of 16 rows by 128 columns, 1024 bytes each, [E][ceil(N/16)][ceil(K/128)].
 // Lane l of a wave owns 16 bytes of a tile, row l % 16 and, in word s, the
@@ -21,7 +35,6 @@ namespace moe {
 // time, two neighbouring columns.
 template <bool U4>
 __device__ inline bf16x8 q4_decode(uint32_t w) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   if constexpr (U4) {
     // and-or by hand: the compiler splits it in two, as both constants are literals
     const uint32_t mask = 0x00780078u, sixteen = 0x41804180u;

@@ -1,8 +1,8 @@
 // Making 4-bit weights and reading them back (layout: q4.h). Both are one pass
 // over memory: a wave takes a tile of 16 rows by 128 columns, a lane the 32
 // columns of one row that its 16 bytes of codes hold, so codes are written and
-// read as 1 KiB in a row and the rows in pieces of 64 bytes (bf16) a load. The
-// four lanes of a row join their extremes by shuffles.
+// read as 1 KiB in a row and the rows in whole 128-byte lines. The four lanes of
+// a row join their extremes by shuffles.
 #include "common.h"
 #include "q4.h"
 
@@ -11,32 +11,120 @@
 namespace moe {
 namespace {
 
-// The lane's eight columns c .. c + 7 of row `row`, 0 past the matrix (K is a
-// multiple of 8, so all eight are inside or none).
+// A tile's 16 rows in whole 128-byte lines: lane l has 16-byte piece
+// piece_at(l) of row l % 8, and of row 8 + l % 8, of a line; operands() turns
+// these into two pieces of row l % 16 and back. Two lines of bf16 (four of fp32)
+// make a tile; whole lines can stream past the caches.
 template <typename T>
-__device__ inline void load_cols(const T* row, int64_t c, bool in, float (&v)[8]) {
-  if (!in) {
+struct Lines {
+  static constexpr int kPer = 16 / sizeof(T), kLines = sizeof(T) == 2 ? 2 : 4;  // elements of a piece; lines of a tile
+  static __device__ inline int piece_at(int lane) {
+    const int quad = lane >> 4, half = (lane >> 3) & 1;
+    // bf16: pieces quad and quad + 4, eight columns each, of steps 2 line and
+    // 2 line + 1; fp32: 2 quad and 2 quad + 1, the eight columns of step `line`
+    return sizeof(T) == 2 ? quad + 4 * half : 2 * quad + half;
+  }
+};
+
+// The lane's columns of the tile at row n0 and column c0 of matrix W [N, K]: v[s]
+// are the columns c0 + 32 s + 8 (l / 16) .. + 7 of row n0 + l % 16, 0 past the
+// matrix (K is a multiple of 8).
+template <typename T>
+__device__ inline void load_tile(const T* W, int64_t n0, int64_t c0, int64_t N, int64_t K, float (&v)[4][8]) {
+  using L = Lines<T>;
+  const int lane = threadIdx.x & 63, r = lane & 7;
+  u32x4 lo[L::kLines], hi[L::kLines];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  } else if constexpr (sizeof(T) == 2) {
-    const bf16x8 b = *reinterpret_cast<const bf16x8*>(row + c);
+  for (int i = 0; i < L::kLines; ++i) {
+    const int64_t c = c0 + i * 8 * L::kPer + L::piece_at(lane) * L::kPer;
+    lo[i] = hi[i] = u32x4{0, 0, 0, 0};
+    if (c < K && n0 + r < N) lo[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(W + (n0 + r) * K + c));
+    if (c < K && n0 + 8 + r < N)
+      hi[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(W + (n0 + 8 + r) * K + c));
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(b[i]);
-  } else {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(row + c), b = *reinterpret_cast<const f32x4*>(row + c + 4);
+  for (int i = 0; i < L::kLines; ++i) {
+    u32x4 a0, a1;
+    operands(lo[i], hi[i], a0, a1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
-    }
+    for (int q = 0; q < 4; ++q)
+      if constexpr (sizeof(T) == 2) {
+        v[2 * i][2 * q] = __uint_as_float(a0[q] << 16);
+        v[2 * i][2 * q + 1] = __uint_as_float(a0[q] & 0xffff0000u);
+        v[2 * i + 1][2 * q] = __uint_as_float(a1[q] << 16);
+        v[2 * i + 1][2 * q + 1] = __uint_as_float(a1[q] & 0xffff0000u);
+      } else {
+        v[i][q] = __uint_as_float(a0[q]);
+        v[i][4 + q] = __uint_as_float(a1[q]);
+      }
   }
 }
 
-// Code of the E2M1 value nearest to r (ties to the even code, 6 for more).
-__device__ inline uint32_t e2m1_code(float r) {
-  const float a = fabsf(r);
-  const uint32_t m = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.f);
-  return m | (r < 0.f ? 8u : 0u);
+// The other way: v rounded to T, into the tile.
+template <typename T>
+__device__ inline void store_tile(T* W, int64_t n0, int64_t c0, int64_t N, int64_t K, const float (&v)[4][8]) {
+  using L = Lines<T>;
+  const int lane = threadIdx.x & 63, r = lane & 7;
+#pragma unroll
+  for (int i = 0; i < L::kLines; ++i) {
+    u32x4 a0, a1, lo, hi;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if constexpr (sizeof(T) == 2) {
+        a0[q] = f32_to_bf16(v[2 * i][2 * q]) | static_cast<uint32_t>(f32_to_bf16(v[2 * i][2 * q + 1])) << 16;
+        a1[q] = f32_to_bf16(v[2 * i + 1][2 * q]) | static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1][2 * q + 1])) << 16;
+      } else {
+        a0[q] = __float_as_uint(v[i][q]);
+        a1[q] = __float_as_uint(v[i][4 + q]);
+      }
+    operands(a0, a1, lo, hi);
+    const int64_t c = c0 + i * 8 * L::kPer + L::piece_at(lane) * L::kPer;
+    if (c < K && n0 + r < N) __builtin_nontemporal_store(lo, reinterpret_cast<u32x4*>(W + (n0 + r) * K + c));
+    if (c < K && n0 + 8 + r < N) __builtin_nontemporal_store(hi, reinterpret_cast<u32x4*>(W + (n0 + 8 + r) * K + c));
+  }
+}
+
+// v / sc, rounded as the division rounds it, without a division for each v: inv
+// is the rounded 1 / sc, and the product's remainder, exact in an fma, corrects
+// it to v / sc (1 + 2^-46) before the last rounding. That rounds the same way, as
+// no quotient of a 24-bit by an 8-bit number lies nearer than 2^-33 of its value
+// to a midpoint of two floats. Below 1/4, where every code is the nearest one,
+// the remainder may underflow. Scales that are tiny, 0 or infinite divide.
+struct Quotient {
+  float sc, inv;
+  bool ordinary;
+  __device__ explicit Quotient(float s) : sc(s), ordinary(s >= 0x1p-100f && s < 0x1p127f) {
+    inv = 1.f / (ordinary ? s : 1.f);
+  }
+  __device__ float fast(float v) const {
+    const float r = v * inv;
+    return fmaf(fmaf(-r, sc, v), inv, r);
+  }
+  __device__ float operator()(float v) const { return ordinary ? fast(v) : sc > 0.f ? v / sc : 0.f; }
+};
+
+// The eight codes of v / sc as a word.
+template <bool U4>
+__device__ inline uint32_t codes_of(const float (&v)[8], const Quotient& by, float z) {
+  float r[8];
+  if (by.ordinary) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = by.fast(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = by(v[i]);
+  }
+  uint32_t w = 0;
+  if constexpr (U4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= static_cast<uint32_t>(__builtin_amdgcn_fmed3f(rintf(r[i]) + z, 0.f, 15.f)) << q4_shift(true, i);
+  } else {  // the conversion rounds ties to the even code and takes 6 for more
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[0], r[1], 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[2], r[3], 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[4], r[5], 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[6], r[7], 1.0f, 3);
+  }
+  return w;
 }
 
 template <typename T, bool U4>
@@ -47,13 +135,11 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ W, 
   const int64_t nt = ceil_div(N, 16), kt = ceil_div(K, 128);
   const int64_t tile = blockIdx.x * 4ll + (threadIdx.x >> 6);
   if (tile >= tiles) return;
-  const int64_t strip = tile / kt, j = tile % kt, e = strip / nt, n = (strip % nt) * 16 + (lane & 15);
-  const T* row = W + (e * N + n) * K;
+  const int64_t strip = tile / kt, j = tile % kt, e = strip / nt;
   float v[4][8], lo[4], hi[4];
+  load_tile(W + e * N * K, (strip % nt) * 16, j * 128, N, K, v);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const int64_t c = j * 128 + 32 * s + 8 * quad;
-    load_cols(row, c, n < N && c < K, v[s]);
     lo[s] = 0.f;
     hi[s] = 0.f;
 #pragma unroll
@@ -86,24 +172,16 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ W, 
     // times the constants' fp32 reciprocals, as moe.h defines the scales
     const float span = !U4 ? big * (1.f / 6.f) : zero ? (hi[s] - lo[s]) * (1.f / 15.f) : big * (1.f / 7.f);
     const bf16_t sb = f32_to_bf16(span);
-    const float sc = bf16_to_f32(sb);
-    float z = zero ? 0.f : 8.f;
-    if (U4 && zero && sc > 0.f) z = fminf(fmaxf(rintf(-lo[s] / sc), 0.f), 15.f);
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float r = sc > 0.f ? v[s][i] / sc : 0.f;
-      const uint32_t q = U4 ? static_cast<uint32_t>(fminf(fmaxf(rintf(r) + z, 0.f), 15.f)) : e2m1_code(r);
-      w |= q << q4_shift(U4, i);
-    }
-    word[s] = w;
+    const Quotient by(bf16_to_f32(sb));
+    const float z = U4 && zero ? fminf(fmaxf(rintf(by(-lo[s])), 0.f), 15.f) : 8.f;
+    word[s] = codes_of<U4>(v[s], by, z);
     if (quad == 0 && s % gs == 0) {
       const int64_t at = (tile * (4 / gs) + s / gs) * 16 + lane;
       scale[at] = sb;
       if (U4 && zero) zero[at] = static_cast<uint8_t>(z);
     }
   }
-  codes[tile * 64 + lane] = uint4{word[0], word[1], word[2], word[3]};
+  __builtin_nontemporal_store(u32x4{word[0], word[1], word[2], word[3]}, reinterpret_cast<u32x4*>(codes + tile * 64 + lane));
 }
 
 template <typename T, bool U4>
@@ -111,37 +189,24 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint4* __restrict
                                                          const bf16_t* __restrict__ scale,
                                                          const uint8_t* __restrict__ zero, int64_t tiles, int64_t N,
                                                          int64_t K, int group, T* __restrict__ W) {
-  const int lane = threadIdx.x & 63, quad = lane >> 4;
+  const int lane = threadIdx.x & 63;
   const int64_t nt = ceil_div(N, 16), kt = ceil_div(K, 128);
   const int64_t tile = blockIdx.x * 4ll + (threadIdx.x >> 6);
   if (tile >= tiles) return;
-  const int64_t strip = tile / kt, j = tile % kt, e = strip / nt, n = (strip % nt) * 16 + (lane & 15);
-  if (n >= N) return;
-  const uint4 cw = codes[tile * 64 + lane];
-  const uint32_t word[4] = {cw.x, cw.y, cw.z, cw.w};
-  T* row = W + (e * N + n) * K;
+  const int64_t strip = tile / kt, j = tile % kt, e = strip / nt;
+  const u32x4 word = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + tile * 64 + lane));
+  float v[4][8];
   const int gs = group / 32;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const int64_t c = j * 128 + 32 * s + 8 * quad;
-    if (c >= K) break;
     const int64_t at = (tile * (4 / gs) + s / gs) * 16 + (lane & 15);
     const float sc = bf16_to_f32(scale[at]);
     const float z = U4 ? (zero ? static_cast<float>(zero[at]) : 8.f) + 16.f : 0.f;
     const bf16x8 q = q4_decode<U4>(word[s]);
-    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (static_cast<float>(q[i]) - z) * sc;  // exact: 5 bits times 8
-    if constexpr (sizeof(T) == 2) {
-      bf16x8 o;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = static_cast<__bf16>(v[i]);
-      *reinterpret_cast<bf16x8*>(row + c) = o;
-    } else {
-      *reinterpret_cast<f32x4*>(row + c) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(row + c + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    }
+    for (int i = 0; i < 8; ++i) v[s][i] = (static_cast<float>(q[i]) - z) * sc;  // exact: 5 bits times 8
   }
+  store_tile(W + e * N * K, (strip % nt) * 16, j * 128, N, K, v);
 }
 
 // f(element type, is U4) with compile-time arguments.
