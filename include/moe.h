@@ -302,7 +302,8 @@ int moe_combine(const void* x, const void* y, const int32_t* topk_idx, const flo
  *   MOE_Q4_E2M1: W = scale * v, v = 0, .5, 1, 1.5, 2, 3, 4, 6 by q's low three
  *                bits and negative where the fourth is set; `zero` must be NULL
  * group is 32, 64 or 128 (the last group of a row may be shorter), K a
- * multiple of 8. Layout (device memory, 16-byte aligned):
+ * multiple of 8, and a stack has fewer than 2^26 tiles (64 GiB of codes; else
+ * MOE_ERR_UNSUPPORTED). Layout (device memory, 16-byte aligned):
  *   codes [E][ceil(N/16)][ceil(K/128)][1024 bytes]: tiles of 16 rows by 128
  *     columns. Little-endian 32-bit word s (0 .. 3) of 16-byte piece l (0 .. 63)
  *     holds row l % 16 and the columns 32 s + 8 (l / 16) + i, i = 0 .. 7 of the
@@ -344,8 +345,9 @@ int moe_q4_dequantize(const moe_q4_t* q, int32_t E, int64_t N, int64_t K, moe_dt
 /* out[r] = W[expert[r]] x[r] for R <= 64 rows, K <= 2^22: x [R, K], out [R, N] (dtype, out
  * must not overlap x), W [E, N, K] 4-bit, expert [R] int32 or NULL (matrix 0
  * for every row). A row whose expert is outside [0, E) is left as it was.
- * Products are exact and summed in fp32, out is rounded once. R == 0 returns
- * MOE_OK. workspace: moe_q4_matvec_workspace_size() bytes (0 for bf16),
+ * Products are exact and summed in fp32, out is rounded once. U4 sums are taken
+ * as scale * (sum (16 + q) x - (16 + zero) sum x): where a group's sum of |x|
+ * passes 2^123, or x is infinite, out is not finite. R == 0 returns MOE_OK. workspace: moe_q4_matvec_workspace_size() bytes (0 for bf16),
  * 256-byte aligned. */
 int moe_q4_matvec_workspace_size(int32_t R, int64_t K, moe_dtype_t dtype, size_t* bytes);
 int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32_t R, int32_t E, int64_t N, int64_t K,

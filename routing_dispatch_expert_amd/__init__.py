@@ -570,7 +570,9 @@ class _On:
             self.guard.__exit__(*exc)
 
     def empty(self, shape, dtype):
-        t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        return self.lent(self.torch.empty(shape, dtype=dtype, device=self.device))
+
+    def lent(self, t):
         if self.other is not None:
             t.record_stream(self.other)
         return t
@@ -635,9 +637,12 @@ def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
                     out.zero_()
         else:
             _require(out, "out", x.dtype, (R, N))
+            on.lent(out)
         nbytes = moe_q4_matvec_workspace_size(R, K, dt)
         if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
             workspace = on.empty(max(nbytes, 1), torch.uint8)
+        else:
+            on.lent(workspace)
         moe_q4_matvec(x, expert, W, R, E, N, K, dt, out, workspace, nbytes, on.stream)
     return {"out": out, "workspace": workspace}
 
@@ -688,6 +693,9 @@ def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None,
             res = out
             if not isinstance(res, FewResult) or res._bound[0] != key:
                 raise ValueError("out: need the result of a forward_few call with the same sizes, types and device")
+            for t in res._bound[2].values():
+                if isinstance(t, torch.Tensor):
+                    on.lent(t)
         _, nbytes, t = res._bound
         call = moe_layer_forward_few_q4 if q4 else moe_layer_forward_few
         call(x, W_router, router_bias, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, max_ranks, dtype, t["out"], t,

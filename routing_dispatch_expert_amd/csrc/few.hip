@@ -496,6 +496,8 @@ struct Strip {
   Span w, scale, zero;
   int zstep;             // bytes from one group's zero points to the next group's
   uint32_t lo, hi;
+  int last;              // dense: the row's last line,
+  bool past;             // and whether the lane's piece of that is past the row's end
 };
 
 // n rows of x (at most 64), and in lane c row c's offset.
@@ -537,7 +539,10 @@ __device__ inline Strip<KIND> strip_of(const WMat& m, int64_t e, int64_t r0, int
     const int64_t row = K * sizeof(XType<KIND>), at = (e * N + r0) * row;
     s.w = span(static_cast<const char*>(m.w) + at, m.E * N * row - at);
     s.lo = (lane & 7) * static_cast<uint32_t>(row) + piece_of(lane) * 16;
-    s.hi = 8 * static_cast<uint32_t>(row);
+    s.last = static_cast<int>(ceil_div(row, 128)) - 1;
+    s.past = s.last * 128 + piece_of(lane) * 16 >= row;
+    // without rows 8 - 15 rows 0 - 7 again: a common offset past the span's end is no test of its end
+    s.hi = r0 + 8 < N ? 8 * static_cast<uint32_t>(row) : 0;
   } else {
     const int64_t nt = ceil_div(N, 16), kt = ceil_div(K, 128), t = (e * nt + r0 / 16) * kt;
     s.w = span(static_cast<const char*>(m.w) + t * 1024, kt * 1024);
@@ -580,8 +585,8 @@ __device__ inline f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // and not larger because the difference loses as many bits as it exceeds q.
 // PARTS = 3: fp32 x as the exact sum of three bf16 arrays.
 
-// One unit's weights, as loaded. In the last unit of a dense row that ends
-// inside it the lanes past the end get what follows: x is 0 there.
+// One unit's weights, as loaded. Past the end of a dense row that ends inside
+// its last line they are 0, as x is: what follows in memory may be NaN.
 template <WKind KIND, int NS>
 struct UnitW {
   u32x4 w[NS][is_dense(KIND) ? 2 : 1];
@@ -592,8 +597,9 @@ __device__ inline void load_weights(const Strip<KIND> (&a)[NS], int j, UnitW<KIN
 #pragma unroll
   for (int r = 0; r < NS; ++r)
     if constexpr (is_dense(KIND)) {
-      u.w[r][0] = load_once(a[r].w, a[r].lo, j * 128);
-      u.w[r][1] = load_once(a[r].w, a[r].lo, j * 128 + a[r].hi);
+      const uint32_t lo = j == a[r].last && a[r].past ? kNowhere : a[r].lo;
+      u.w[r][0] = load_once(a[r].w, lo, j * 128);
+      u.w[r][1] = load_once(a[r].w, lo, j * 128 + a[r].hi);
     } else {
       u.w[r][0] = load_once(a[r].w, a[r].lo, j * 1024);
     }
@@ -728,7 +734,7 @@ struct Stage {
 template <WKind KIND, int GPT, int PARTS, int NS, bool WIDE>
 constexpr int kWaveLds =
     std::max({Stage<KIND, GPT, PARTS, NS, 1, 1>::kBytes, Stage<KIND, GPT, PARTS, NS, 1, 4>::kBytes,
-              Stage<KIND, GPT, PARTS, NS, 1, 8>::kBytes,               Stage<KIND, GPT, PARTS, NS, 1, 16>::kBytes,
+              Stage<KIND, GPT, PARTS, NS, 1, 8>::kBytes, Stage<KIND, GPT, PARTS, NS, 1, 16>::kBytes,
               WIDE ? Stage<KIND, GPT, PARTS, NS, 2, 32>::kBytes : 0});
 
 // acc += unit i of the staged run times its weights.
@@ -1022,6 +1028,8 @@ template <WKind KIND, int GPT, int PARTS, bool WIDE, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, waves_per_simd(KIND, PARTS, WIDE)) void few_down_kernel(
     FewArgs a) {
   constexpr int kStage = kWaveLds<KIND, GPT, PARTS, 1, WIDE>;
+  static_assert(WAVES * (kStage + (WAVES > 2 * waves_per_simd(KIND, PARTS, WIDE) ? 32 : kFewMaxT) * 64) <= 160 * 1024,
+                "a CU's LDS");
   __shared__ f32x4 staged[WAVES * kStage / 16];
   extern __shared__ f32x4 all_sums_[];  // [WAVES][T][16] floats
   float* all_sums = reinterpret_cast<float*>(all_sums_);

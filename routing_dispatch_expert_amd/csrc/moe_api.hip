@@ -1028,9 +1028,10 @@ int check_q4_shape(int32_t E, int64_t N, int64_t K, int32_t group) {
   if (group != 32 && group != 64 && group != 128)
     return fail(MOE_ERR_INVALID_ARG, "group=%d must be 32, 64 or 128", group);
   if (K % 8) return fail(MOE_ERR_UNSUPPORTED, "K=%lld must be a multiple of 8", static_cast<long long>(K));
-  const int64_t lim = int64_t{1} << 31;
-  if (N >= lim || K >= lim || moe::ceil_div(N, 16) * moe::ceil_div(K, 128) >= lim / E)
-    return fail(MOE_ERR_UNSUPPORTED, "the weights must have fewer than 2^31 tiles");
+  // a launch has fewer than 2^32 threads, 64 for a tile
+  const int64_t lim = int64_t{1} << 31, most = int64_t{1} << 26;
+  if (N >= lim || K >= lim || moe::ceil_div(N, 16) * moe::ceil_div(K, 128) >= moe::ceil_div(most, E))
+    return fail(MOE_ERR_UNSUPPORTED, "the weights must have fewer than 2^26 tiles");
   return MOE_OK;
 }
 
@@ -1087,7 +1088,7 @@ int check_few_shape(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, fl
   if (std::max(d, d_ff) > moe::kFewMaxWidth)  // rows are addressed with 32-bit byte offsets
     return fail(MOE_ERR_UNSUPPORTED, "d and d_ff must be at most %lld", static_cast<long long>(moe::kFewMaxWidth));
   const int64_t act = std::min<int64_t>(E, T * k);
-  if (act * (moe::ceil_div(d_ff, 16) + moe::ceil_div(d, 16)) >= (int64_t{1} << 30))
+  if (act * moe::ceil_div(d_ff, 16) >= (int64_t{1} << 26))  // a launch has fewer than 2^32 threads
     return fail(MOE_ERR_UNSUPPORTED, "too many weight tiles");
   return MOE_OK;
 }
@@ -1199,8 +1200,6 @@ int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32
   if (R > moe::kFewMaxT) return fail(MOE_ERR_UNSUPPORTED, "R=%d > %d rows", R, moe::kFewMaxT);
   if (K > moe::kFewMaxWidth)
     return fail(MOE_ERR_UNSUPPORTED, "K must be at most %lld", static_cast<long long>(moe::kFewMaxWidth));
-  if (std::min(E, std::max(R, 1)) * moe::ceil_div(N, 16) >= (int64_t{1} << 31))
-    return fail(MOE_ERR_UNSUPPORTED, "too many weight tiles");
   if (!x || !out) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned16(x) || !aligned16(out)) return fail(MOE_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
   const size_t eb = elem_bytes(dtype);

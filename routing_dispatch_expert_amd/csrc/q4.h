@@ -59,13 +59,14 @@ __device__ inline bf16x8 q4_decode(uint32_t w) {
 __device__ inline int q4_shift(bool u4, int i) { return u4 ? ((i & 1) ? 16 + 2 * (i - 1) : 2 * i) : 4 * i; }
 
 // v as the exact sum of three bf16 numbers: each takes the leading 8 of the
-// bits that are left (24 in all), by cutting off the rest.
+// bits that are left (24 in all), by cutting off the rest. An infinity is the
+// first of them alone.
 __device__ inline void split3(float v, bf16_t (&q)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     const uint32_t top = __float_as_uint(v) & 0xffff0000u;
     q[i] = static_cast<bf16_t>(top >> 16);
-    v -= __uint_as_float(top);
+    v = v == __uint_as_float(top) ? 0.f : v - __uint_as_float(top);
   }
 }
 

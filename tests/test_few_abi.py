@@ -46,7 +46,7 @@ LAYER = [
     (dict(E=64, k=33), UNSUPPORTED), (dict(d=12), UNSUPPORTED), (dict(d_ff=100), UNSUPPORTED),
     (dict(d=1 << 20, d_ff=1 << 20), UNSUPPORTED), (dict(d=(1 << 22) + 8, d_ff=8), UNSUPPORTED),
     (dict(d_ff=(1 << 22) + 8, d=8), UNSUPPORTED), (dict(workspace=None), WORKSPACE),
-    (dict(workspace_bytes=100), WORKSPACE), (dict(workspace=FAKE * 3 + 8), WORKSPACE),
+    (dict(E=1024, k=4, T=64, d=8, d_ff=1 << 22), UNSUPPORTED), (dict(workspace_bytes=100), WORKSPACE), (dict(workspace=FAKE * 3 + 8), WORKSPACE),
     (dict(stats=dict(STATS, buckets=FAKE)), INVALID), (dict(stats=dict(STATS, src=FAKE)), INVALID),
     (dict(stats=dict(STATS, instance=FAKE)), INVALID), (dict(stats=dict(STATS, g=FAKE, u=FAKE, h=FAKE)), INVALID),
 ]
@@ -109,7 +109,8 @@ def test_q4_size(E, N, K, group):
 
 
 SHAPES = [(dict(E=0), INVALID), (dict(N=0), INVALID), (dict(K=-8), INVALID), (dict(K=12), UNSUPPORTED),
-          (dict(N=1 << 40), UNSUPPORTED), (dict(E=1 << 16, N=1 << 16, K=1 << 12), UNSUPPORTED)]
+          (dict(N=1 << 40), UNSUPPORTED), (dict(E=1 << 16, N=1 << 16, K=1 << 12), UNSUPPORTED),
+          (dict(E=1 << 12, N=1 << 14, K=1 << 11), UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("kw,status", SHAPES)
@@ -128,6 +129,10 @@ def test_q4_weight_refusals(bad):
     refused(INVALID, lambda: moe.moe_q4_quantize(FAKE, 2, 32, 128, "bf16", q4(**bad)))
     refused(INVALID, lambda: moe.moe_q4_dequantize(q4(**bad), 2, 32, 128, "bf16", FAKE))
     refused(INVALID, lambda: moe.moe_q4_matvec(FAKE, None, q4(**bad), 4, 2, 32, 128, "bf16", FAKE * 2, None, 0))
+
+
+def test_largest_q4_sizes():
+    assert moe.moe_q4_size((1 << 12) - 1, 1 << 14, 1 << 11, 64)[0] == ((1 << 12) - 1) << 24
 
 
 def test_q4_argument_refusals():

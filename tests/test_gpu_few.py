@@ -125,6 +125,20 @@ CASES = [
 ]
 
 
+# what the sizes above do not reach: many feature strips a work-group of 4, 2 and 1 waves each; contractions of several
+# staged runs a wave; more than 256 strips of out; both sides of 64 copies and of 64 ranks
+LONG = [
+    dict(T=64, d=136, E=64, k=8, d_ff=200, cf=2.0),
+    dict(T=64, d=264, E=64, k=8, d_ff=392, cf=1.0, P=2),
+    dict(T=3, d=72, E=1, k=1, d_ff=262168, cf=1.0),
+    dict(T=3, d=4360, E=4, k=2, d_ff=136, cf=2.0),
+    dict(T=40, d=4360, E=4, k=2, d_ff=72, cf=2.0),
+    dict(T=16, d=136, E=16, k=4, d_ff=136, cf=1.0),
+    dict(T=13, d=136, E=16, k=5, d_ff=136, cf=1.0),
+    dict(T=2, d=136, E=1024, k=4, d_ff=16, cf=2.0, P=128),
+]
+
+
 def _id(c):
     return "-".join(f"{k}{v}" for k, v in c.items())
 
@@ -149,6 +163,52 @@ def test_few_layer_q4(case, q4, dtype):
     wl = wl_of(dtype=dtype, **case)
     dev, view = weights_of(wl, q4)
     check(wl, run_few(wl, dev), view)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", LONG, ids=_id)
+def test_few_layer_many_strips_and_long_rows(case, dtype):
+    say(f"few layer {dtype} {case}")
+    wl = wl_of(dtype=dtype, **case)
+    dev, view = weights_of(wl)
+    check(wl, run_few(wl, dev), view)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q4", [dict(U4, group=64), dict(kind="e2m1", group=32, zero_points=False)], ids=_id)
+@pytest.mark.parametrize("case", [LONG[i] for i in (0, 1, 3, 4)] + [
+    dict(T=1, d=16520, E=2, k=1, d_ff=40, cf=2.0),
+    dict(T=6, d=40, E=2, k=2, d_ff=16520, cf=2.0),
+    dict(T=3, d=24, E=1, k=1, d_ff=262168, cf=1.0),
+], ids=_id)
+def test_few_layer_q4_many_strips_and_long_rows(case, q4, dtype):
+    say(f"few layer {dtype} {q4} {case}")
+    wl = wl_of(dtype=dtype, **case)
+    dev, view = weights_of(wl, q4)
+    check(wl, run_few(wl, dev), view)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,f", [(136, 72), (8, 24), (392, 200), (1032, 40)])
+def test_weights_not_chosen_may_hold_anything(d, f, dtype):
+    """NaN and infinities in the matrices of experts without copies change nothing (rows end inside a cache line that
+    the next expert's first row shares), and in one row of W_down only that column of out."""
+    wl = wl_of(T=9, d=d, E=3, k=1, d_ff=f, cf=3.0, dtype=dtype)
+    x, wr = to_dev(wl.x, dtype), to_dev(wl.wr, dtype)
+    bias = torch.tensor([0.0, 1e4, 0.0], device="cuda")
+    dev, _ = weights_of(wl)
+    want = moe.forward_few(x, wr, *dev, k=1, cf=3.0, router_bias=bias)["out"].clone()
+    assert torch.isfinite(want).all()
+    for bad in (float("nan"), float("inf")):
+        spoilt = [w.clone() for w in dev]
+        for w in spoilt:
+            w[0] = w[2] = bad
+        got = moe.forward_few(x, wr, *spoilt, k=1, cf=3.0, router_bias=bias)["out"]
+        assert torch.equal(got, want)
+        spoilt[2][1, 5] = bad
+        got = moe.forward_few(x, wr, *spoilt, k=1, cf=3.0, router_bias=bias)["out"]
+        rest = [c for c in range(d) if c != 5]
+        assert torch.equal(got[:, rest], want[:, rest]) and not torch.isfinite(got[:, 5]).any()
 
 
 def test_without_stats():
@@ -279,6 +339,27 @@ def test_current_stream_is_the_default():
         got = r["out"].clone()
     torch.cuda.synchronize()
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+def test_lent_buffers_on_another_stream():
+    """Buffers lent to a call on a given stream stay its own until it is done, also when dropped at once."""
+    wl = wl_of(T=8, d=512, E=16, k=4, d_ff=512, cf=4.0, dtype="bf16")
+    dev, _ = weights_of(wl)
+    x, wr = to_dev(wl.x, "bf16"), to_dev(wl.wr, "bf16")
+    want = moe.forward_few(x, wr, *dev, k=4, cf=4.0)["out"].clone()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        r = moe.forward_few(x, wr, *dev, k=4, cf=4.0)
+        s.wait_stream(torch.cuda.current_stream())
+        r = moe.forward_few(x, wr, *dev, k=4, cf=4.0, stream=s, out=r)
+        with torch.cuda.stream(s):
+            got = r["out"].clone()
+        n = r["workspace"].numel()
+        del r
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x7f)
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
 def test_results_lend_their_buffers():

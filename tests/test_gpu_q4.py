@@ -71,6 +71,42 @@ def test_quantize_and_back(shape, group, kind, zero, dtype):
     assert np.array_equal(got, rounded), "values"
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind,zero", KINDS)
+def test_quantize_at_the_edges_between_codes(kind, zero, dtype):
+    """Quotients on, and one unit beside, every edge between two codes, at scales from subnormal to the largest."""
+    rng = np.random.default_rng(17)
+    edges = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5, 6] if kind == "e2m1" else np.arange(.5, 15, 1), np.float32)
+    top = np.float32(6 if kind == "e2m1" else 15 if zero else 7)
+    rows = []
+    for exp in (-140, -126, -120, -101, -100, -99, -60, -1, 0, 1, 60, 122, 124):
+        for _ in range(4):
+            s = np.float32(1 + rng.integers(0, 128) / 128) * np.float32(2.0) ** exp
+            e = rng.choice(edges, 32) * (1 if kind == "u4" and zero else rng.choice([-1, 1], 32))
+            v = (e.astype(np.float64) * np.float64(s)).astype(np.float32)
+            v = np.nextafter(v, rng.choice([-np.inf, np.inf], 32).astype(np.float32), where=rng.random(32) < .5, out=v)
+            v = np.clip(v, -top * s, top * s)
+            v[3] = top * s
+            rows.append(v)
+    w = np.array(rows, np.float32)[None]
+    host = moe_inputs.to_bf16_bits(w) if dtype == "bf16" else w
+    q = moe.quantize_q4(to_dev(host, dtype), group=32, kind=kind, zero_points=zero)
+    torch.cuda.synchronize()
+    # 15 2^124 passes fp32's range: rows with infinities, which weights must not hold, are only quantised, not compared
+    finite = np.isfinite(bits_to_f64(host, dtype)).all(-1)[0]
+    assert finite[:48].all()
+    want = ref.q4_quantize(bits_to_f64(host, dtype).astype(np.float32), 32, kind, zero)
+    s64 = moe_inputs.bits_to_f64(to_host(q.scale, "bf16"), "bf16")
+    row = np.pad(finite, (0, -len(finite) % 16)).reshape(1, -1, 1, 16) & np.ones(s64.shape, bool)
+    assert np.array_equal(s64[row], want[1][row]), "scale"
+    z = None if q.zero is None else q.zero.cpu().numpy()
+    assert z is None or np.array_equal(z[row], want[2][row]), "zero"
+    with np.errstate(invalid="ignore"):
+        have, _ = ref.q4_decode(q.codes.cpu().numpy(), s64, z, w.shape, 32, kind)
+        should, _ = ref.q4_decode(want[0], want[1].astype(np.float64), want[2], w.shape, 32, kind)
+    assert np.array_equal(have[0, finite], should[0, finite]), "codes"
+
+
 def test_quantizing_codes_values_again_keeps_them():
     """Values that 4 bits hold exactly come back unchanged."""
     rng = np.random.default_rng(3)
@@ -126,6 +162,49 @@ def test_matvec(R, N, K, E, group, kind, zero, dtype):
         valid = [r for r in range(R) if expert[r] == 0]
         again = moe.matvec_q4(x, q)["out"]
         assert torch.equal(again[valid], out[valid])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,N,K,E", [(3, 20000, 136, 1), (9, 40016, 136, 1), (64, 12944, 264, 64), (1, 48, 16520, 1),
+                                     (4, 48, 8328, 1), (24, 32, 4232, 2)])
+def test_matvec_many_strips_and_long_rows(R, N, K, E, dtype):
+    """Work-groups of one, two and four waves, and several staged runs a wave."""
+    say(f"matvec {dtype} R={R} N={N} K={K} E={E}")
+    rng = np.random.default_rng(R + N)
+    for group, kind, zero in ((64, "u4", True), (32, "e2m1", False)):
+        codes, scale, z = ref.random_q4(rng, E, N, K, group, kind, zero)
+        host = rng.standard_normal((R, K)).astype(np.float32)
+        host = moe_inputs.to_bf16_bits(host) if dtype == "bf16" else host
+        expert = rng.integers(0, E, R).astype(np.int32)
+        q = moe.Q4Weights(torch.from_numpy(codes).cuda(), to_dev(scale, "bf16"),
+                          None if z is None else torch.from_numpy(z).cuda(), (E, N, K), group, kind)
+        out = moe.matvec_q4(to_dev(host, dtype), q, expert=torch.from_numpy(expert).cuda())["out"]
+        torch.cuda.synchronize()
+        got, x64 = bits_to_f64(to_host(out, dtype), dtype), bits_to_f64(host, dtype)
+        s64 = moe_inputs.bits_to_f64(scale, "bf16")
+        for e in np.unique(expert)[:3]:
+            W, A = ref.q4_decode(codes[e:e + 1], s64[e:e + 1], None if z is None else z[e:e + 1], (1, N, K), group, kind)
+            r = np.nonzero(expert == e)[0]
+            want = x64[r] @ W[0].T
+            bound = ref.STEP[dtype] * np.abs(want) + 1.01 * (K + 8) * ref.ACC * (np.abs(x64[r]) @ A[0].T)
+            assert (np.abs(got[r] - want) <= bound + 1e-30).all(), e
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_infinite_inputs(dtype):
+    """E2M1: an infinity times a weight is infinite, of its sign, and NaN where the weight is 0; U4: not finite.
+    Other rows stay as they are."""
+    w = torch.tensor([0.0, 1.0, -2.0, 6.0, -0.5, 3.0, 4.0, -1.5], device="cuda")[:, None].repeat(1, 40)[None].contiguous()
+    x = torch.ones(3, 40, device="cuda", dtype=dtype)
+    x[1, 37] = float("inf")
+    got = moe.matvec_q4(x, moe.quantize_q4(w, group=32, kind="e2m1"))["out"].double()
+    want = x.double() @ w[0].double().T
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.isnan(got[1, 0])
+    assert torch.equal(torch.isinf(got), torch.isinf(want))
+    assert torch.equal(got[1, 1:].sign(), want[1, 1:].sign())
+    u4 = moe.quantize_q4(w, group=32, zero_points=False)
+    a, b = moe.matvec_q4(x, u4)["out"], moe.matvec_q4(torch.ones_like(x), u4)["out"]
+    assert not torch.isfinite(a[1]).any() and torch.equal(a[[0, 2]], b[[0, 2]])
 
 
 def test_padding_is_not_looked_at():
