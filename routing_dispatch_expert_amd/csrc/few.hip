@@ -1085,65 +1085,52 @@ struct MatvecArgs {
   void* out;        // [R, N] bf16 (PARTS = 1) or fp32
 };
 
-// Rows with the same expert, grouped by the first wave: groups in the order of
-// their first row, rows in order. Rows with an expert outside [0, E) are left out.
-struct RowGroups {
-  int n, e[64], off[65], row[64];
+// The rows of one expert: rows with the same expert are a group, in the order of
+// their first rows; row c of this one in lane c < n. Rows with an expert outside
+// [0, E) are in none.
+struct RowGroup {
+  int e, n, row;  // n = 0: there are not so many groups
 };
 
-__device__ inline void group_rows(const int32_t* expert, int R, int E, RowGroups& g) {
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    int e = -1;
-    if (lane < R) e = expert ? expert[lane] : 0;
-    const bool valid = lane < R && e >= 0 && e < E;
-    bool leads = valid;
-    unsigned long long mates = 0;
-    for (int r = 0; r < R; ++r) {
-      const int o = __shfl(valid ? e : -1, r);
-      if (valid && o == e) {
-        mates |= 1ull << r;
-        if (r < lane) leads = false;
-      }
-    }
-    const unsigned long long leaders = __ballot(leads), below = (1ull << lane) - 1ull;
-    const int size = leads ? __popcll(mates) : 0;
-    int off = size;  // exclusive sum of the sizes of the groups before
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(off, o);
-      if (lane >= o) off += up;
-    }
-    if (lane == 63) {
-      g.n = __popcll(leaders);
-      g.off[g.n] = off;
-    }
-    off -= size;
-    if (leads) {
-      const int at = __popcll(leaders & below);
-      g.e[at] = e;
-      g.off[at] = off;
-    }
-    const int first = __shfl(off, valid ? __ffsll(mates) - 1 : 0);  // of the group's leader
-    if (valid) g.row[first + __popcll(mates & below)] = lane;
+// Group i, by one wave in registers: lanes with the same expert find each other
+// by one ballot a bit of its number. (Every wave for itself: the weights' loads,
+// which only need the expert, then wait for no barrier.)
+__device__ inline RowGroup row_group(const int32_t* expert, int R, int E, int i) {
+  const int lane = threadIdx.x & 63;
+  int e = -1;
+  if (lane < R) e = expert ? expert[lane] : 0;
+  const bool valid = e >= 0 && e < E;
+  unsigned long long mates = __ballot(valid);
+  for (int bit = 0; (E - 1) >> bit; ++bit) {
+    const unsigned long long set = __ballot((e >> bit) & 1);
+    mates &= (e >> bit) & 1 ? set : ~set;
   }
-  __syncthreads();
+  const unsigned long long below = (1ull << lane) - 1ull;
+  const bool leads = valid && !(mates & below);
+  const unsigned long long leaders = __ballot(leads);
+  if (i >= __popcll(leaders)) return {0, 0, 0};
+  const int first = __ffsll(__ballot(leads && __popcll(leaders & below) == i)) - 1;
+  const int its = __builtin_amdgcn_readlane(e, first);
+  const unsigned long long mine = __ballot(e == its);
+  const int n = __popcll(mine);
+  // lane to lane: the group's rows first, then the others
+  const int to = e == its ? __popcll(mine & below) : n + __popcll(~mine & below);
+  return {its, n, __builtin_amdgcn_ds_permute(4 * to, lane)};
 }
 
 template <WKind KIND, int GPT, int PARTS, int W, int NT>
-__device__ inline void matvec_tile(const MatvecArgs& a, const RowGroups& g, int e, int p0, int n, int64_t n0,
-                                   char* lds) {
+__device__ inline void matvec_tile(const MatvecArgs& a, const RowGroup& g, int p, int n, int64_t n0, char* lds) {
   const int lane = threadIdx.x & 63;
-  const RowList x = {span(a.x, a.R * a.K * 2), a.K * 2, a.R * a.K * 2, n, g.row[p0 + std::min(lane, n - 1)]};
+  const RowList x = {span(a.x, a.R * a.K * 2), a.K * 2, a.R * a.K * 2, n, __shfl(g.row, p + std::min(lane, n - 1))};
   // the last 16 rows of a matrix may have no 16 after them: they are read twice
   const int64_t n1 = n0 + 16 < a.N ? n0 + 16 : n0;
   f32x4 v[2][NT] = {};
-  if (!strip_pair<KIND, GPT, PARTS, W, NT>(a.w, a.w, e, n0, n1, a.N, a.K, x, v, lds)) return;
+  if (!strip_pair<KIND, GPT, PARTS, W, NT>(a.w, a.w, g.e, n0, n1, a.N, a.K, x, v, lds)) return;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int c = t * 16 + (lane & 15);
+    const int64_t row = __shfl(g.row, (p + c) & 63) * a.N;
     if (c >= n) continue;
-    const int64_t row = g.row[p0 + c] * a.N;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -1161,15 +1148,10 @@ __device__ inline void matvec_tile(const MatvecArgs& a, const RowGroups& g, int 
 template <WKind KIND, int GPT, int PARTS, bool WIDE, int W>
 __global__ __launch_bounds__(W * 64, waves_per_simd(KIND, PARTS, WIDE)) void matvec_kernel(MatvecArgs a) {
   __shared__ f32x4 lds[kPairLds<KIND, GPT, PARTS, WIDE, W>];
-  __shared__ RowGroups g;
-  group_rows(a.expert, a.R, a.E, g);
   const int64_t nt = ceil_div(a.N, 32);
-  const int i = static_cast<int>(blockIdx.x / nt);
-  if (i >= g.n) return;
-  const int e = uniform(g.e[i]), p0 = uniform(g.off[i]);
-  MOE_BY_TOKENS(p0, uniform(g.off[i + 1]) - p0,
-                (matvec_tile<KIND, GPT, PARTS, W, NT>(a, g, e, p, n, (blockIdx.x % nt) * 32,
-                                                      reinterpret_cast<char*>(lds))));
+  const RowGroup g = row_group(a.expert, a.R, a.E, static_cast<int>(blockIdx.x / nt));
+  MOE_BY_TOKENS(0, g.n, (matvec_tile<KIND, GPT, PARTS, W, NT>(a, g, p, n, (blockIdx.x % nt) * 32,
+                                                              reinterpret_cast<char*>(lds))));
 }
 
 __global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t n, bf16_t* parts) {
