@@ -306,9 +306,9 @@ def moe_combine(x, y, topk_idx, topk_w, slot, T, d, E, k, C, dtype, out, stream=
 
 def moe_q4_size(E, N, K, group) -> tuple[int, int, int]:
     """Bytes of a 4-bit matrix stack's codes, scales and (where kept) zero points."""
-    n = [ctypes.c_size_t(0) for _ in range(3)]
-    _check(lib().moe_q4_size(E, N, K, group, *(ctypes.byref(v) for v in n)), "moe_q4_size")
-    return tuple(v.value for v in n)
+    a, b, c = ctypes.c_size_t(0), ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().moe_q4_size(E, N, K, group, ctypes.byref(a), ctypes.byref(b), ctypes.byref(c)), "moe_q4_size")
+    return a.value, b.value, c.value
 
 
 def _q4(q) -> "ctypes.POINTER(moe_q4_t) | None":
@@ -532,8 +532,10 @@ class Q4Weights:
         for t in (codes, scale, zero):
             if t is not None and t.device != codes.device:
                 raise ValueError("codes, scale and zero must be on one device")
-        self.codes, self.scale, self.zero = codes, scale, zero
-        self.shape, self.group, self.kind = (E, N, K), int(group), kind
+        self._set(codes, scale, zero, (E, N, K), int(group), kind)
+
+    def _set(self, codes, scale, zero, shape, group, kind):
+        self.codes, self.scale, self.zero, self.shape, self.group, self.kind = codes, scale, zero, shape, group, kind
         self._ref = ctypes.pointer(moe_q4_t(_ptr(codes), _ptr(scale), _ptr(zero), Q4_KINDS[kind], self.group))
 
     @property
@@ -596,12 +598,13 @@ def quantize_q4(W, group=128, kind="u4", zero_points=True, stream=None):
     dt = _dtype(W.dtype)
     if kind not in Q4_KINDS:
         raise ValueError(f"kind: need one of {sorted(Q4_KINDS)}, got {kind!r}")
-    moe_q4_size(E, N, K, group)
+    moe_q4_size(E, N, K, group)   # checks the sizes
     nt, kt = -(-N // 16), -(-K // 128)
     with _On(W.device, stream) as on:
         groups = (E, nt, kt * (128 // group), 16)
-        q = Q4Weights(on.empty((E, nt, kt, 1024), torch.uint8), on.empty(groups, torch.bfloat16),
-                      on.empty(groups, torch.uint8) if kind == "u4" and zero_points else None, (E, N, K), group, kind)
+        q = Q4Weights.__new__(Q4Weights)   # of tensors that need no checks
+        q._set(on.empty((E, nt, kt, 1024), torch.uint8), on.empty(groups, torch.bfloat16),
+               on.empty(groups, torch.uint8) if kind == "u4" and zero_points else None, (E, N, K), int(group), kind)
         moe_q4_quantize(W, E, N, K, dt, q, on.stream)
     return q
 

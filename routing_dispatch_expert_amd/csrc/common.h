@@ -314,6 +314,7 @@ hipError_t launch_combine(const void* x, const void* y, const int32_t* idx, cons
 // ---- few tokens and 4-bit weights (few.hip, q4.hip) ----
 constexpr int kFewMaxT = 64, kFewMaxE = 1024, kFewMaxCopies = kFewMaxT * 32;
 constexpr int kFewMaxSplits = 8;  // slices of d of the router scores
+constexpr int kFewMaxShares = 8;  // work-groups that share a strip of out
 constexpr int64_t kFewMaxWidth = 1 << 22;  // of d, d_ff and K
 enum { kQ4U4 = 0, kQ4E2m1 = 1 };  // MOE_Q4_U4, MOE_Q4_E2M1
 // Expert weights: kind < 0 dense (bf16 or fp32 rows), else 4-bit (q4.h).
@@ -323,9 +324,13 @@ struct FewWeights {
 };
 // The kept copies by expert: experts with copies act_e[n_act], copies
 // act_off[i] .. act_off[i + 1] - 1 of the i-th, and each copy's token and gate.
+// done [strips]: counters of the down kernel's work-groups, zeroed by the
+// routing kernel where the strips are split (n_done of them, else 0).
 struct FewLists {
   int32_t *n_act, *act_e, *act_off, *token;
   float* gate;
+  int32_t* done;
+  int n_done;
 };
 struct FewLayer {
   const void *x, *wr;
@@ -343,8 +348,13 @@ struct FewLayer {
   bf16_t* xparts;   // [3][T][d]: fp32 x beside 4-bit weights, else NULL
   FewLists ls;
   void* h;          // [parts][T k][few_ld_h(f)], bf16 (fp32 beside fp32 weights)
+  float* sums;      // [strips][splits][T][16] where the down strips are split
+  int splits;
 };
 int few_router_splits(int64_t T, int64_t d, int E);
+// Work-groups that share 16 columns of out; columns of W_down that one of its
+// units has (64 bf16, 32 fp32, 128 4-bit).
+int few_down_splits(int64_t T, int64_t d, int64_t f, int E, int k, int unit_cols);
 // Row length of h: whole 128-byte lines.
 inline int64_t few_ld_h(int64_t f) { return ceil_div(f, 64) * 64; }
 hipError_t launch_few_layer(const FewLayer& L, hipStream_t s);

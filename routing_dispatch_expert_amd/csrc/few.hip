@@ -243,6 +243,7 @@ __global__ __launch_bounds__(1024) void few_route_kernel(Scores sc, int64_t C, i
   const int T = sc.T, E = sc.E, k = sc.k, P = sc.P, per = E / P;
   for (int e = tid; e < E; e += 1024) cnt[e] = 0;
   if (tid == 0) dropped_tokens = 0;
+  for (int i = tid; i < ls.n_done; i += 1024) ls.done[i] = 0;
   for (int t = wave; t < T; t += 16) {
     int e;
     float w;
@@ -357,6 +358,7 @@ __global__ __launch_bounds__(1024) void few_route_small_kernel(Scores sc, int64_
     if (o.kept) o.kept[e] = 0;
   }
   if (tid < 64) send_s[tid] = 0;
+  for (int i = tid; i < ls.n_done; i += blockDim.x) ls.done[i] = 0;
   for (int t = wave; t < T; t += waves) {
     int e;
     float w;
@@ -914,6 +916,7 @@ struct FewArgs {
   FewLists ls;
   void* h;               // [PARTS][T k][ldh], by position in the lists
   int64_t ldh;
+  float* sums;           // [strips][shares][T][16]
   void* out;
 };
 
@@ -997,7 +1000,9 @@ __global__ __launch_bounds__(W * 64, waves_per_simd(KIND, PARTS, WIDE)) void few
 // copies; the units of all of them, expert after expert, are dealt to the
 // waves in equal runs. A wave adds each expert's part of its run, times the
 // gates, to its own sums of the T tokens in LDS, and these are joined in wave
-// order: no y goes to memory, nothing waits for another work-group.
+// order: no y goes to memory. With few strips several work-groups share one: each
+// leaves its sums in memory and counts itself, and the last to come adds them up
+// in their order. Nothing waits for another work-group.
 template <WKind KIND, int GPT, int PARTS, int NT>
 __device__ inline void down_run(const FewArgs& a, int64_t e, int p0, int n, int64_t c0, int j0, int j1, char* lds,
                                 float* sums) {
@@ -1024,7 +1029,20 @@ __device__ inline void down_run(const FewArgs& a, int64_t e, int p0, int n, int6
     }
 }
 
-template <WKind KIND, int GPT, int PARTS, bool WIDE, int WAVES>
+// Sums between work-groups, which may run on dies whose L2s do not see each
+// other's writes: stored and loaded past these, one by one. (A fence instead
+// would write back and drop a whole L2; with one in each wave the kernel took
+// 100 us, with one a work-group as long as without the split, 16 - 19 us.)
+__device__ inline void to_chip(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline float from_chip(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline void wait_for_stores() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// SHARED: gridDim.y > 1 work-groups a strip.
+template <WKind KIND, int GPT, int PARTS, bool WIDE, int WAVES, bool SHARED>
 __global__ __launch_bounds__(WAVES * 64, waves_per_simd(KIND, PARTS, WIDE)) void few_down_kernel(
     FewArgs a) {
   constexpr int kStage = kWaveLds<KIND, GPT, PARTS, 1, WIDE>;
@@ -1034,17 +1052,18 @@ __global__ __launch_bounds__(WAVES * 64, waves_per_simd(KIND, PARTS, WIDE)) void
   extern __shared__ f32x4 all_sums_[];  // [WAVES][T][16] floats
   float* all_sums = reinterpret_cast<float*>(all_sums_);
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int strip = blockIdx.x, share = SHARED ? blockIdx.y : 0, shares = SHARED ? gridDim.y : 1;
   float* sums = all_sums + wave * a.T * 16;
   char* lds = reinterpret_cast<char*>(staged) + wave * kStage;
   // the first 64 experts of the list, on their way together with its length
   const int first_e = a.ls.act_e[std::min(lane, a.E - 1)], first_p = a.ls.act_off[std::min(lane, a.E)];
   const int after_p = a.ls.act_off[std::min(lane + 1, a.E)];
   for (int i = lane; i < a.T * 16; i += 64) sums[i] = 0.f;
-  const int64_t c0 = blockIdx.x * 16ll;
-  const int units = units_of<KIND>(a.f);
+  const int64_t c0 = strip * 16ll;
+  const int units = units_of<KIND>(a.f), nth = share * WAVES + wave, of = shares * WAVES;
   const int64_t total = static_cast<int64_t>(units) * uniform(*a.ls.n_act);  // below 2^31: 2^18 units of 1024 experts
-  const int end = static_cast<int>(total * (wave + 1) / WAVES);
-  for (int u = static_cast<int>(total * wave / WAVES); u < end;) {
+  const int end = static_cast<int>(total * (nth + 1) / of);
+  for (int u = static_cast<int>(total * nth / of); u < end;) {
     const int i = u / units, j0 = u % units, j1 = std::min(units, j0 + end - u);
     int e, p0, p1;
     if (i < 64) {
@@ -1060,12 +1079,37 @@ __global__ __launch_bounds__(WAVES * 64, waves_per_simd(KIND, PARTS, WIDE)) void
     u += j1 - j0;
   }
   __syncthreads();
+  float* shared = a.sums + strip * static_cast<int64_t>(shares) * a.T * 16;
+  if constexpr (SHARED) {
+    for (int i = threadIdx.x; i < a.T * 16; i += WAVES * 64) {
+      float v = all_sums[i];
+      for (int w = 1; w < WAVES; ++w) v += all_sums[w * a.T * 16 + i];
+      to_chip(shared + share * a.T * 16 + i, v);
+    }
+    __shared__ int before;
+    wait_for_stores();  // this wave's sums are there before thread 0 counts the work-group
+    __syncthreads();
+    if (threadIdx.x == 0)
+      before = __hip_atomic_fetch_add(a.ls.done + strip, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (before + 1 < shares) return;
+  }
   constexpr bool kBf16 = KIND == kDenseBf16 || (!is_dense(KIND) && PARTS == 1);
   for (int i = threadIdx.x; i < a.T * 16; i += WAVES * 64) {
     const int64_t col = c0 + (i & 15), at = (i >> 4) * a.d + col;
     if (col >= a.d) continue;
-    float v = all_sums[i];
-    for (int w = 1; w < WAVES; ++w) v += all_sums[w * a.T * 16 + i];
+    float v;
+    if constexpr (!SHARED) {
+      v = all_sums[i];
+      for (int w = 1; w < WAVES; ++w) v += all_sums[w * a.T * 16 + i];
+    } else {
+      float part[kFewMaxShares];  // asked for together
+#pragma unroll
+      for (int w = 0; w < kFewMaxShares; ++w) part[w] = w < shares ? from_chip(shared + w * a.T * 16 + i) : 0.f;
+      v = part[0];
+#pragma unroll
+      for (int w = 1; w < kFewMaxShares; ++w) v += part[w];
+    }
     if constexpr (kBf16)
       static_cast<bf16_t*>(a.out)[at] = f32_to_bf16(bf16_to_f32(static_cast<const bf16_t*>(a.x_res)[at]) + v);
     else
@@ -1216,6 +1260,16 @@ int few_router_splits(int64_t T, int64_t d, int E) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kFewMaxSplits, d / 512, 256 / tiles})));
 }
 
+// Enough work-groups for the chip (a CU holds two of those for more than 32
+// tokens), but 16 waves' units in each. Down kernel, one work-group a strip and
+// shared: d = 500, fp32, 7 tokens (32 strips) 18.6 and 11.9 us; d = 2048, u4, 3
+// tokens (128 strips) 16.1 and 12.8 us.
+int few_down_splits(int64_t T, int64_t d, int64_t f, int E, int k, int unit_cols) {
+  const int64_t units = std::min<int64_t>(E, T * k) * ceil_div(f, unit_cols);
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({kFewMaxShares, (T > 32 ? 512 : 256) / ceil_div(d, 16), units / 16})));
+}
+
 hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
   const bool bf16 = L.bf16;
   const int S = few_router_splits(L.T, L.d, L.E);
@@ -1258,6 +1312,7 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
   a.ls = L.ls;
   a.h = L.h;
   a.ldh = few_ld_h(L.f);
+  a.sums = L.sums;
   a.out = L.out;
   const int64_t act = std::min<int64_t>(L.E, static_cast<int64_t>(L.T) * L.k);  // experts with copies, at most
   const int64_t strips = ceil_div(L.d, 16);
@@ -1275,12 +1330,21 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
     });
     // two work-groups a CU; with few strips one of twice the waves, where their sums of the tokens fit the LDS
     constexpr int kSome = 2 * waves_per_simd(kKind, kParts, kWide), kMany = kParts == 1 ? 2 * kSome : kSome;
-    if (strips > 256 || L.T > 32)
-      few_down_kernel<kKind, kGpt, kParts, kWide, kSome>
-          <<<dim3(static_cast<unsigned>(strips)), dim3(kSome * 64), kSome * L.T * 64, s>>>(a);
+    auto down = [&](auto waves, auto shared) {
+      constexpr int W = decltype(waves)::value;
+      few_down_kernel<kKind, kGpt, kParts, kWide, W, decltype(shared)::value>
+          <<<dim3(static_cast<unsigned>(strips), L.splits), dim3(W * 64), W * L.T * 64, s>>>(a);
+    };
+    auto down_by = [&](auto shared) {
+      if (strips > 256 || L.T > 32)
+        down(std::integral_constant<int, kSome>{}, shared);
+      else
+        down(std::integral_constant<int, kMany>{}, shared);
+    };
+    if (L.splits > 1)
+      down_by(std::true_type{});
     else
-      few_down_kernel<kKind, kGpt, kParts, kWide, kMany>
-          <<<dim3(static_cast<unsigned>(strips)), dim3(kMany * 64), kMany * L.T * 64, s>>>(a);
+      down_by(std::false_type{});
     return hipGetLastError();
   });
 }

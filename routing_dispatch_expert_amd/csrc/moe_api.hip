@@ -1048,11 +1048,12 @@ int check_q4(const moe_q4_t* q, const char* name) {
 
 // Workspace of the few-token layer.
 struct FewPlan {
-  int32_t *idx, *n_act, *act_e, *act_off, *token;
-  float *w, *gate;
+  int32_t *idx, *n_act, *act_e, *act_off, *token, *done;
+  float *w, *gate, *sums;
   double* part;
   moe::bf16_t* xparts;
   void* h;
+  int splits, strips;
   size_t bytes;
 };
 
@@ -1071,6 +1072,11 @@ FewPlan plan_few(void* ws, int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_
   p.part = c.take<double>(static_cast<size_t>(moe::few_router_splits(T, d, E)) * T * E);
   p.xparts = c.take<moe::bf16_t>(split ? 3 * static_cast<size_t>(T) * d : 0);
   p.h = c.take<char>(n * moe::few_ld_h(d_ff) * (split ? 6 : eb));
+  p.splits = moe::few_down_splits(T, d, d_ff, E, k, q4 ? 128 : 128 / eb);
+  p.strips = static_cast<int>(moe::ceil_div(d, 16));
+  const size_t shared = p.splits > 1 ? p.strips : 0;
+  p.sums = c.take<float>(shared * p.splits * T * 16);
+  p.done = c.take<int32_t>(shared);
   p.bytes = align_up(c.off);
   if (!split) p.xparts = nullptr;
   return p;
@@ -1139,8 +1145,10 @@ int layer_few(const void* x, const void* W_router, const float* router_bias, con
   L.totals = S.totals;
   L.part = p.part;
   L.xparts = p.xparts;
-  L.ls = {p.n_act, p.act_e, p.act_off, p.token, p.gate};
+  L.ls = {p.n_act, p.act_e, p.act_off, p.token, p.gate, p.done, p.splits > 1 ? p.strips : 0};
   L.h = p.h;
+  L.sums = p.sums;
+  L.splits = p.splits;
   MOE_HIP_TRY(moe::launch_few_layer(L, static_cast<hipStream_t>(stream)), "few-token layer");
   return MOE_OK;
 }
