@@ -341,6 +341,26 @@ def test_current_stream_is_the_default():
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dropped_tokens_pass_bit_for_bit(dtype):
+    """Zeros of either sign, infinities and NaN of tokens without a kept copy, as moe_layer_forward passes them."""
+    for d, q4 in ((136, None), (4360, None), (136, U4)):   # strips shared by work-groups, and not
+        wl = wl_of(T=12, d=d, E=4, k=1, d_ff=64, cf=1.0, dtype=dtype, bias="hot0", reject=False)
+        dev, _ = weights_of(wl, q4)
+        x, wr = to_dev(wl.x, dtype), to_dev(wl.wr, dtype)
+        bits = x.view(torch.int16 if dtype == "bf16" else torch.int32)
+        bits[5:, 1::4] = bits.new_tensor(-2 ** (15 if dtype == "bf16" else 31))   # -0.0
+        bits[5:, 2::4] = 0
+        few = moe.forward_few(x, torch.zeros_like(wr), *dev, k=1, cf=1.0, router_bias=torch.from_numpy(wl.bias_vec).cuda())
+        bits[7, 3], bits[8, 3], bits[9, 3] = (0x7f81, -0x80, 0x7f80) if dtype == "bf16" else (0x7f800001, -0x800000, 0x7f800000)
+        few = moe.forward_few(x, torch.zeros_like(wr), *dev, k=1, cf=1.0, router_bias=torch.from_numpy(wl.bias_vec).cuda())
+        torch.cuda.synchronize()
+        lost = (few["slot"] < 0).all(1)
+        # NaN scores choose what they like; the others' first C = 3 stay, and every later token is lost
+        assert lost[[5, 6, 10, 11]].all()
+        assert torch.equal(few["out"].view(bits.dtype)[lost], bits[lost])
+
+
 def test_lent_buffers_on_another_stream():
     """Buffers lent to a call on a given stream stay its own until it is done, also when dropped at once."""
     wl = wl_of(T=8, d=512, E=16, k=4, d_ff=512, cf=4.0, dtype="bf16")
