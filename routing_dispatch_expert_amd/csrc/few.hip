@@ -1045,7 +1045,7 @@ __device__ inline void down_run(const FewArgs& a, int64_t e, int p0, int n, int6
 // Sums between work-groups, which may run on dies whose L2s do not see each
 // other's writes: stored and loaded past these, one by one. (A fence instead
 // would write back and drop a whole L2; with one in each wave the kernel took
-// 100 us, with one a work-group as long as without the split, 16 - 19 us.)
+// 100 us, with one a work-group as long as with unshared strips, 16 - 19 us.)
 __device__ inline void to_chip(float* p, float v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -1059,8 +1059,7 @@ template <WKind KIND, int GPT, int PARTS, bool WIDE, int WAVES, bool SHARED>
 __global__ __launch_bounds__(WAVES * 64, waves_per_simd(KIND, PARTS, WIDE)) void few_down_kernel(
     FewArgs a) {
   constexpr int kStage = kWaveLds<KIND, GPT, PARTS, 1, WIDE>;
-  static_assert(WAVES * (kStage + (WAVES > 2 * waves_per_simd(KIND, PARTS, WIDE) ? 32 : kFewMaxT) * 64) <= 160 * 1024,
-                "a CU's LDS");
+  static_assert(WAVES * (kStage + kFewMaxT * 64) <= 160 * 1024, "a CU's LDS");
   __shared__ f32x4 staged[WAVES * kStage / 16];
   extern __shared__ f32x4 all_sums_[];  // [WAVES][T][16] floats
   float* all_sums = reinterpret_cast<float*>(all_sums_);
@@ -1254,9 +1253,13 @@ double expected_distinct(int E, int k, int T) { return E * (1 - std::pow(1 - sta
 
 // f(waves of a work-group) for about `items` pairs of strips. The chip holds
 // 4096 waves: with few items more waves share one, so that the memory has
-// enough to do. With very many, one wave alone spares the joining; between, its
-// long items would leave the last round's waves alone with the memory (1.2
-// rounds of single waves: 254 us instead of 219 with four).
+// enough to do (u4 row product, 128 items of 14336 columns: 13.8 us with eight
+// waves, 17.2 with four; 448 items of 4096: 12.0 and 11.6). Two waves instead of
+// four put 1024 - 2048 items on the chip at once (e2m1, 64 rows: 16.2 us, 19.0
+// with four). With very many, one wave alone spares the joining (64 tokens of
+// a DeepSeek-V3-shaped layer: bf16 3.03 ms, 3.24 with four; u4 1.07 and 1.10);
+// below, its long items would leave the last round's waves alone with the
+// memory (1.2 rounds of single waves: 254 us instead of 219 with four).
 template <int PARTS, typename F>
 void by_waves(double items, F&& f) {
   if (PARTS == 1 && items <= 512)
@@ -1277,14 +1280,14 @@ int few_router_splits(int64_t T, int64_t d, int E) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kFewMaxSplits, d / 512, 256 / tiles})));
 }
 
-// Enough work-groups for the chip (a CU holds two of those for more than 32
-// tokens), but 16 waves' units in each. Down kernel, one work-group a strip and
-// shared: d = 500, fp32, 7 tokens (32 strips) 18.6 and 11.9 us; d = 2048, u4, 3
-// tokens (128 strips) 16.1 and 12.8 us.
+// Enough work-groups for the chip (a CU holds two), but 16 units in each. The
+// layer without sharing and with it: fp32, 7 tokens, d = 500 (32 strips) 37.2 and
+// 28.6 us; u4, 3 tokens, d = 2048 (128 strips) 43.0 and 40.1 us; e2m1, 16 tokens,
+// d = 4096 (256 strips) 180 and 167 us.
 int few_down_splits(int64_t T, int64_t d, int64_t f, int E, int k, int unit_cols) {
   const int64_t units = std::min<int64_t>(E, T * k) * ceil_div(f, unit_cols);
   return static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>({kFewMaxShares, (T > 32 ? 512 : 256) / ceil_div(d, 16), units / 16})));
+      std::max<int64_t>(1, std::min<int64_t>({kFewMaxShares, 512 / ceil_div(d, 16), units / 16})));
 }
 
 hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
@@ -1333,7 +1336,8 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
   a.out = L.out;
   const int64_t act = std::min<int64_t>(L.E, static_cast<int64_t>(L.T) * L.k);  // experts with copies, at most
   const int64_t strips = ceil_div(L.d, 16);
-  // two token tiles at a time where experts have more than half of one on average
+  // two token tiles at a time where experts have more than half of one on average: 64 tokens, k = 2 of 8, d = 4096,
+  // d_ff = 14336: bf16 629 us, 788 with one; e2m1 291 and 307. With fewer copies the registers are better spent on waves.
   const bool wide = static_cast<int64_t>(L.T) * L.k > 8 * static_cast<int64_t>(L.E);
   return by_weights(L.wt, bf16, wide, [&](auto kind, auto gpt, auto parts, auto two) {
     constexpr WKind kKind = decltype(kind)::value;
@@ -1345,23 +1349,15 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
       few_gate_up_kernel<kKind, kGpt, kParts, kWide, W>
           <<<dim3(static_cast<unsigned>(act * ft)), dim3(W * 64), 0, s>>>(a);
     });
-    // two work-groups a CU; with few strips one of twice the waves, where their sums of the tokens fit the LDS
-    constexpr int kSome = 2 * waves_per_simd(kKind, kParts, kWide), kMany = kParts == 1 ? 2 * kSome : kSome;
-    auto down = [&](auto waves, auto shared) {
-      constexpr int W = decltype(waves)::value;
+    auto down = [&](auto shared) {
+      constexpr int W = 2 * waves_per_simd(kKind, kParts, kWide);  // two work-groups a CU
       few_down_kernel<kKind, kGpt, kParts, kWide, W, decltype(shared)::value>
           <<<dim3(static_cast<unsigned>(strips), L.splits), dim3(W * 64), W * L.T * 64, s>>>(a);
     };
-    auto down_by = [&](auto shared) {
-      if (strips > 256 || L.T > 32)
-        down(std::integral_constant<int, kSome>{}, shared);
-      else
-        down(std::integral_constant<int, kMany>{}, shared);
-    };
     if (L.splits > 1)
-      down_by(std::true_type{});
+      down(std::true_type{});
     else
-      down_by(std::false_type{});
+      down(std::false_type{});
     return hipGetLastError();
   });
 }
