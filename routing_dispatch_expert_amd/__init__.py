@@ -545,8 +545,10 @@ class Q4Weights:
 
 class _On:
     """The device and stream of a call on `device`: the given stream, or
-    torch's current one of that device. Tensors allocated for the call on
-    another stream than torch's current one are marked as used there."""
+    torch's current one of that device. On another stream than torch's current
+    one the call's tensors are marked as used there, so that torch does not hand
+    their memory on before the call is done. (The caller sees to it that the
+    inputs are ready on that stream.)"""
 
     def __init__(self, device, stream):
         import torch
@@ -576,7 +578,9 @@ class _On:
 
     def lent(self, t):
         if self.other is not None:
-            t.record_stream(self.other)
+            for v in (t.codes, t.scale, t.zero) if isinstance(t, Q4Weights) else (t,):
+                if v is not None:
+                    v.record_stream(self.other)
         return t
 
 
@@ -605,7 +609,7 @@ def quantize_q4(W, group=128, kind="u4", zero_points=True, stream=None):
         q = Q4Weights.__new__(Q4Weights)   # of tensors that need no checks
         q._set(on.empty((E, nt, kt, 1024), torch.uint8), on.empty(groups, torch.bfloat16),
                on.empty(groups, torch.uint8) if kind == "u4" and zero_points else None, (E, N, K), int(group), kind)
-        moe_q4_quantize(W, E, N, K, dt, q, on.stream)
+        moe_q4_quantize(on.lent(W), E, N, K, dt, q, on.stream)
     return q
 
 
@@ -615,7 +619,7 @@ def dequantize_q4(q, dtype, stream=None):
     dt = _dtype(dtype)
     with _On(q.device, stream) as on:
         W = on.empty(q.shape, torch.bfloat16 if dt == MOE_DTYPE_BF16 else torch.float32)
-        moe_q4_dequantize(q, *q.shape, dt, W, on.stream)
+        moe_q4_dequantize(on.lent(q), *q.shape, dt, W, on.stream)
     return W
 
 
@@ -646,6 +650,9 @@ def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
             workspace = on.empty(max(nbytes, 1), torch.uint8)
         else:
             on.lent(workspace)
+        if on.other is not None:
+            for t in (x, expert, W):
+                on.lent(t)
         moe_q4_matvec(x, expert, W, R, E, N, K, dt, out, workspace, nbytes, on.stream)
     return {"out": out, "workspace": workspace}
 
@@ -699,6 +706,9 @@ def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None,
             for t in res._bound[2].values():
                 if isinstance(t, torch.Tensor):
                     on.lent(t)
+        if on.other is not None:
+            for t in (x, W_router, router_bias, W_gate, W_up, W_down):
+                on.lent(t)
         _, nbytes, t = res._bound
         call = moe_layer_forward_few_q4 if q4 else moe_layer_forward_few
         call(x, W_router, router_bias, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, max_ranks, dtype, t["out"], t,

@@ -376,10 +376,18 @@ def test_lent_buffers_on_another_stream():
         with torch.cuda.stream(s):
             got = r["out"].clone()
         n = r["workspace"].numel()
+        y = x.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        r = moe.forward_few(y, wr, *dev, k=4, cf=4.0, stream=s, router_bias=None)
+        with torch.cuda.stream(s):
+            again = r["out"].clone()
+        del y
+        torch.empty_like(x).fill_(7)   # must not get y's memory while the call runs
         del r
         torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x7f)
         torch.cuda.synchronize()
         assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        assert torch.equal(again.view(torch.int16), want.view(torch.int16))
 
 
 def test_results_lend_their_buffers():
