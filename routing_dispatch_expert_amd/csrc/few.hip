@@ -440,9 +440,10 @@ __global__ __launch_bounds__(1024) void few_route_small_kernel(Scores sc, int64_
 
 constexpr bool is_dense(WKind k) { return k == kDenseBf16 || k == kDenseF32; }
 
-// Waves a SIMD that the registers are cut for: as many as fit without spills,
-// whose own loads and stores would make every wait one for all loads in flight.
-constexpr int waves_per_simd(WKind, int parts, bool wide) { return parts == 3 ? 2 : wide ? 3 : 4; }
+// Waves a SIMD that the registers are cut for: as many as fit with at most a few
+// spilled words (20 bytes a lane). A spill's own loads and stores make every wait
+// one for all loads in flight.
+constexpr int waves_per_simd(int parts, bool wide) { return parts == 3 ? 2 : wide ? 3 : 4; }
 
 template <WKind KIND>
 using XType = std::conditional_t<KIND == kDenseF32, float, bf16_t>;
@@ -997,7 +998,7 @@ template <WKind KIND, int GPT, int PARTS, bool WIDE, int W>
 constexpr int kPairLds = W * kWaveLds<KIND, GPT, PARTS, 2, WIDE> / 16;
 
 template <WKind KIND, int GPT, int PARTS, bool WIDE, int W>
-__global__ __launch_bounds__(W * 64, waves_per_simd(KIND, PARTS, WIDE)) void few_gate_up_kernel(FewArgs a) {
+__global__ __launch_bounds__(W * 64, waves_per_simd(PARTS, WIDE)) void few_gate_up_kernel(FewArgs a) {
   __shared__ f32x4 lds[kPairLds<KIND, GPT, PARTS, WIDE, W>];
   const int64_t ft = ceil_div(a.f, 16);
   const int64_t i = blockIdx.x / ft;
@@ -1056,7 +1057,7 @@ __device__ inline void wait_for_stores() { asm volatile("s_waitcnt vmcnt(0)" :::
 
 // SHARED: gridDim.y > 1 work-groups a strip.
 template <WKind KIND, int GPT, int PARTS, bool WIDE, int WAVES, bool SHARED>
-__global__ __launch_bounds__(WAVES * 64, waves_per_simd(KIND, PARTS, WIDE)) void few_down_kernel(
+__global__ __launch_bounds__(WAVES * 64, waves_per_simd(PARTS, WIDE)) void few_down_kernel(
     FewArgs a) {
   constexpr int kStage = kWaveLds<KIND, GPT, PARTS, 1, WIDE>;
   static_assert(WAVES * (kStage + kFewMaxT * 64) <= 160 * 1024, "a CU's LDS");
@@ -1206,7 +1207,7 @@ __device__ inline void matvec_tile(const MatvecArgs& a, const RowGroup& g, int p
 }
 
 template <WKind KIND, int GPT, int PARTS, bool WIDE, int W>
-__global__ __launch_bounds__(W * 64, waves_per_simd(KIND, PARTS, WIDE)) void matvec_kernel(MatvecArgs a) {
+__global__ __launch_bounds__(W * 64, waves_per_simd(PARTS, WIDE)) void matvec_kernel(MatvecArgs a) {
   __shared__ f32x4 lds[kPairLds<KIND, GPT, PARTS, WIDE, W>];
   const int64_t nt = ceil_div(a.N, 32);
   const RowGroup g = row_group(a.expert, a.R, a.E, static_cast<int>(blockIdx.x / nt));
@@ -1350,7 +1351,7 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
           <<<dim3(static_cast<unsigned>(act * ft)), dim3(W * 64), 0, s>>>(a);
     });
     auto down = [&](auto shared) {
-      constexpr int W = 2 * waves_per_simd(kKind, kParts, kWide);  // two work-groups a CU
+      constexpr int W = 2 * waves_per_simd(kParts, kWide);  // two work-groups a CU
       few_down_kernel<kKind, kGpt, kParts, kWide, W, decltype(shared)::value>
           <<<dim3(static_cast<unsigned>(strips), L.splits), dim3(W * 64), W * L.T * 64, s>>>(a);
     };
