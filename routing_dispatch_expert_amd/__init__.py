@@ -584,10 +584,11 @@ class _On:
         return t
 
 
-def _same_device(device, **tensors):
-    for n, t in tensors.items():
+def _same_device(device, names, *tensors):
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{n}: need a tensor on {device}, got {t.device}")
+            name = names.split()[[v is t for v in tensors].index(True)]
+            raise ValueError(f"{name}: need a tensor on {device}, got {t.device}")
 
 
 def quantize_q4(W, group=128, kind="u4", zero_points=True, stream=None):
@@ -635,8 +636,9 @@ def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
     _require(x, "x", x.dtype, (R, K))
     if expert is not None:
         _require(expert, "expert", torch.int32, (R,))
-    _same_device(x.device, W=W, expert=expert, out=out, workspace=workspace)
-    with _On(x.device, stream) as on:
+    dev = x.device
+    _same_device(dev, "W expert out workspace", W.codes, expert, out, workspace)
+    with _On(dev, stream) as on:
         if out is None:
             out = on.empty((R, N), x.dtype)
             if expert is not None:
@@ -645,8 +647,8 @@ def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
         else:
             _require(out, "out", x.dtype, (R, N))
             on.lent(out)
-        nbytes = moe_q4_matvec_workspace_size(R, K, dt)
-        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        nbytes = 0 if dt == MOE_DTYPE_BF16 else moe_q4_matvec_workspace_size(R, K, dt)
+        if workspace is None or workspace.nbytes < nbytes:
             workspace = on.empty(max(nbytes, 1), torch.uint8)
         else:
             on.lent(workspace)
@@ -687,7 +689,7 @@ def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None,
             raise ValueError(f"{n}: need 4-bit weights of shape {s}, got {w.shape}")
     if router_bias is not None:
         _require(router_bias, "router_bias", torch.float32, (E,))
-    _same_device(dev, W_router=W_router, W_gate=W_gate, W_up=W_up, W_down=W_down, router_bias=router_bias)
+    _same_device(dev, "W_router W_gate W_up W_down router_bias", W_router, W_gate, W_up, W_down, router_bias)
     with _On(dev, stream) as on:
         key = (T, d, d_ff, E, k, cf, P, dt, q4, dev)
         if out is None:

@@ -244,3 +244,13 @@ def test_matvec_graph_and_streams():
     other = moe.matvec_q4(x, q, expert=e, stream=s)["out"]
     torch.cuda.synchronize()
     assert torch.equal(other, want)
+
+
+def test_tensors_elsewhere_are_refused_by_name():
+    q = moe.quantize_q4(torch.randn(1, 16, 64, device="cuda"), group=32)
+    x = torch.randn(2, 64, device="cuda")
+    for name, t in (("workspace", torch.empty(1 << 16, dtype=torch.uint8)), ("out", torch.empty(2, 16))):
+        with pytest.raises(ValueError, match=name):
+            moe.matvec_q4(x, q, **{name: t})
+    with pytest.raises(ValueError, match="expert"):
+        moe.matvec_q4(x, q, expert=torch.zeros(2, dtype=torch.int32))
