@@ -36,13 +36,17 @@ __device__ inline void operands(u32x4 lo, u32x4 hi, u32x4& a0, u32x4& a1) {
 template <bool U4>
 __device__ inline bf16x8 q4_decode(uint32_t w) {
   if constexpr (U4) {
-    // and-or by hand: the compiler splits it in two, as both constants are literals
-    const uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+    // Opaque constants: of two literals the compiler would split the and-or in two. The instruction itself is the
+    // compiler's, which then keeps the wait states between it and the matrix instructions that use the same registers
+    // (around an instruction in inline assembly it keeps none).
+    uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(sixteen));
     u32x4 v;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const uint32_t shifted = p == 0 ? w << 3 : w >> (4 * p - 3);
-      asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(v[p]) : "v"(shifted), "s"(mask), "v"(sixteen));
+      v[p] = (shifted & mask) | sixteen;
     }
     return __builtin_bit_cast(bf16x8, v);
   } else {
