@@ -316,7 +316,7 @@ def _q4(q) -> "ctypes.POINTER(moe_q4_t) | None":
     if q is None:
         return None
     if isinstance(q, Q4Weights):
-        return q._ref
+        return ctypes.pointer(moe_q4_t(_ptr(q._codes), _ptr(q._scale), _ptr(q._zero), Q4_KINDS[q._kind], q._group))
     codes, scale, zero, kind, group = q
     return ctypes.pointer(moe_q4_t(_ptr(codes), _ptr(scale), _ptr(zero), Q4_KINDS.get(kind, kind), group))
 
@@ -514,7 +514,9 @@ class Q4Weights:
     uint8 [E, ceil(N/16), ceil(K/128), 1024], scale bfloat16 and zero uint8 (or
     None) [E, ceil(N/16), ceil(K/128) 128/group, 16]; kind "u4" or "e2m1". Made
     by quantize_q4(), or from a checkpoint laid out so. The tensors are kept
-    and read in place."""
+    and read in place: codes, scale and zero give views of them, whose values
+    may be changed, but they are not exchanged for others (other tensors make
+    another Q4Weights). Can be copied (copy.deepcopy) and pickled (torch.save)."""
 
     def __init__(self, codes, scale, zero, shape, group, kind):
         import torch
@@ -532,15 +534,23 @@ class Q4Weights:
         for t in (codes, scale, zero):
             if t is not None and t.device != codes.device:
                 raise ValueError("codes, scale and zero must be on one device")
-        self._set(codes, scale, zero, (E, N, K), int(group), kind)
+        # views: what becomes of the caller's tensor objects (x.data = ...) does not touch what was checked here
+        self._set(codes.detach(), scale.detach(), None if zero is None else zero.detach(), (E, N, K), int(group), kind)
 
     def _set(self, codes, scale, zero, shape, group, kind):
-        self.codes, self.scale, self.zero, self.shape, self.group, self.kind = codes, scale, zero, shape, group, kind
-        self._ref = ctypes.pointer(moe_q4_t(_ptr(codes), _ptr(scale), _ptr(zero), Q4_KINDS[kind], self.group))
+        self._codes, self._scale, self._zero = codes, scale, zero
+        self._shape, self._group, self._kind = shape, group, kind
+
+    codes = property(lambda self: self._codes.detach())
+    scale = property(lambda self: self._scale.detach())
+    zero = property(lambda self: None if self._zero is None else self._zero.detach())
+    shape = property(lambda self: self._shape)
+    group = property(lambda self: self._group)
+    kind = property(lambda self: self._kind)
 
     @property
     def device(self):
-        return self.codes.device
+        return self._codes.device
 
 
 class _On:
@@ -578,7 +588,7 @@ class _On:
 
     def lent(self, t):
         if self.other is not None:
-            for v in (t.codes, t.scale, t.zero) if isinstance(t, Q4Weights) else (t,):
+            for v in (t._codes, t._scale, t._zero) if isinstance(t, Q4Weights) else (t,):
                 if v is not None:
                     v.record_stream(self.other)
         return t
@@ -637,7 +647,7 @@ def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
     if expert is not None:
         _require(expert, "expert", torch.int32, (R,))
     dev = x.device
-    _same_device(dev, "W expert out workspace", W.codes, expert, out, workspace)
+    _same_device(dev, "W expert out workspace", W, expert, out, workspace)
     with _On(dev, stream) as on:
         if out is None:
             out = on.empty((R, N), x.dtype)

@@ -1,0 +1,79 @@
+"""The handle of 4-bit weights, on host tensors: what it keeps and hands to the library."""
+import copy
+import io
+
+import pytest
+import torch
+
+import routing_dispatch_expert_amd as moe
+
+
+@pytest.fixture(autouse=True)
+def _on_the_host(monkeypatch):
+    """The handle's own checks want device tensors."""
+    monkeypatch.setattr(moe, "_require", lambda *a: None)
+
+
+def made(zero=True):
+    """A handle of E = 2, N = 20, K = 136, group 64."""
+    z = torch.randint(16, (2, 2, 4, 16), dtype=torch.uint8) if zero else None
+    return moe.Q4Weights(torch.randint(256, (2, 2, 2, 1024), dtype=torch.uint8), torch.rand(2, 2, 4, 16).bfloat16(), z,
+                         (2, 20, 136), 64, "u4")
+
+
+def given(q):
+    """A pointer to the struct that a call with q passes on."""
+    return moe._q4(q)
+
+
+def follows(q):
+    s = given(q).contents
+    assert s.codes == q.codes.data_ptr() and s.scale == q.scale.data_ptr()
+    assert s.zero == (None if q.zero is None else q.zero.data_ptr())
+    assert (s.kind, s.group) == (moe.Q4_KINDS[q.kind], q.group)
+
+
+@pytest.mark.parametrize("zero", [True, False])
+def test_struct_follows_the_tensors(zero):
+    q = made(zero)
+    follows(q)
+    q.scale.mul_(2)   # in place: the same memory
+    follows(q)
+
+
+@pytest.mark.parametrize("name", ["codes", "scale", "zero", "shape", "group", "kind"])
+def test_parts_are_not_exchanged(name):
+    """No part can be replaced beside the address or size that the calls use."""
+    q = made()
+    value = getattr(q, name)
+    other = value.clone() if isinstance(value, torch.Tensor) else value
+    try:
+        setattr(q, name, other)
+    except AttributeError:
+        pass
+    follows(q)
+
+
+def test_tensor_objects_of_others_do_not_matter():
+    codes = torch.randint(256, (1, 1, 1, 1024), dtype=torch.uint8)
+    q = moe.Q4Weights(codes, torch.rand(1, 1, 1, 16).bfloat16(), None, (1, 8, 8), 128, "u4")
+    at = codes.data_ptr()
+    codes.data = torch.zeros(8, dtype=torch.uint8)
+    q.codes.data = torch.zeros(8, dtype=torch.uint8)
+    assert given(q).contents.codes == at and tuple(q.codes.shape) == (1, 1, 1, 1024)
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "save"])
+def test_copied_and_saved(how):
+    q = made()
+    if how == "deepcopy":
+        r = copy.deepcopy(q)
+    else:
+        f = io.BytesIO()
+        torch.save(q, f)
+        f.seek(0)
+        r = torch.load(f, weights_only=False)   # written just above
+    for a, b in ((q.codes, r.codes), (q.scale, r.scale), (q.zero, r.zero)):
+        assert torch.equal(a, b) and a.data_ptr() != b.data_ptr()
+    assert (r.shape, r.group, r.kind) == (q.shape, q.group, q.kind)
+    follows(r)
