@@ -557,20 +557,23 @@ class _On:
     """The device and stream of a call on `device`: the given stream, or
     torch's current one of that device. On another stream than torch's current
     one the call's tensors are marked as used there, so that torch does not hand
-    their memory on before the call is done. (The caller sees to it that the
-    inputs are ready on that stream.)"""
+    their memory on before the call is done, and new ones come from that stream's
+    own memory (the current stream's free blocks may still be in use by work
+    that waits on it), marked as used on the current one. (The caller sees to it
+    that the inputs are ready on that stream, and the results on the current one.)"""
 
     def __init__(self, device, stream):
         import torch
         self.torch, self.device = torch, device
         self.guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
         self.other = None
+        self.current = torch.cuda.current_stream(device)
         if stream is None:
-            stream = torch.cuda.current_stream(device)
+            stream = self.current
         else:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=device)
-            if stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
+            if stream.cuda_stream != self.current.cuda_stream:
                 self.other = stream
         self.stream = stream
 
@@ -584,7 +587,12 @@ class _On:
             self.guard.__exit__(*exc)
 
     def empty(self, shape, dtype):
-        return self.lent(self.torch.empty(shape, dtype=dtype, device=self.device))
+        if self.other is None:
+            return self.torch.empty(shape, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.other):
+            t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(self.current)
+        return t
 
     def lent(self, t):
         if self.other is not None:
