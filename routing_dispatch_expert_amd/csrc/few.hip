@@ -19,6 +19,7 @@
 // Nothing here depends on the order in which work-groups run: every sum has a
 // fixed order, and the expert lists are built by ranks, not by arrival.
 #include "common.h"
+#include "few.h"
 #include "q4.h"
 
 #include <algorithm>

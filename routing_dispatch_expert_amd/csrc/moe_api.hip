@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "common.h"
+#include "few.h"
 
 namespace {
 

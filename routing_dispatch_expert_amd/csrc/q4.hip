@@ -7,6 +7,7 @@
 // 4.2 - 5.6 TB/s, where a plain copy reaches 4.7. With half lines, through the
 // caches, these took 176 and 127 us, a division for each weight included.
 #include "common.h"
+#include "few.h"
 #include "q4.h"
 
 #include <type_traits>
