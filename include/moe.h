@@ -347,8 +347,9 @@ int moe_q4_dequantize(const moe_q4_t* q, int32_t E, int64_t N, int64_t K, moe_dt
  * for every row). A row whose expert is outside [0, E) is left as it was.
  * Products are exact and summed in fp32, out is rounded once. U4 sums are taken
  * as scale * (sum (16 + q) x - (16 + zero) sum x): where a group's sum of |x|
- * passes 2^123, or x is infinite, out is not finite. R == 0 returns MOE_OK. workspace: moe_q4_matvec_workspace_size() bytes (0 for bf16),
- * 256-byte aligned. */
+ * passes 2^123, or x is infinite, out is not finite. R == 0 returns MOE_OK; x and
+ * out may then be NULL. workspace: moe_q4_matvec_workspace_size() bytes (0 for
+ * bf16), 256-byte aligned. */
 int moe_q4_matvec_workspace_size(int32_t R, int64_t K, moe_dtype_t dtype, size_t* bytes);
 int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32_t R, int32_t E, int64_t N, int64_t K,
                   moe_dtype_t dtype, void* out, void* workspace, size_t workspace_bytes, void* stream);
@@ -364,7 +365,8 @@ int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32
  *  - y is not rounded between the down product and the combine;
  *  - no buckets are built: of stats, topk_idx, topk_w, slot, routed_count,
  *    kept_count, send_count and totals are written; the others must be NULL;
- *  - x, W_router, out and the weights must be 16-byte aligned.
+ *  - x, W_router, out and the weights must be 16-byte aligned;
+ *  - with T == 0, x and out may be NULL.
  * Dropless serving takes cf = E / k (C = T). moe_layer_forward_few_q4 takes
  * the experts' matrices in 4 bits (kind, group and the use of zero the same
  * for all three; d and d_ff multiples of 8); dtype is that of x, W_router and

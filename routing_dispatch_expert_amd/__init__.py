@@ -717,6 +717,10 @@ def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None,
                             topk_w=on.empty((T, k), torch.float32), slot=on.empty((T, k), i32),
                             routed_count=on.empty(E, i32), kept_count=on.empty(E, i32), send_count=on.empty(P, i32),
                             totals=on.empty(4, torch.int64), workspace=on.empty(max(nbytes, 1), torch.uint8))
+            if T == 0:   # nothing will be launched: the counts of no tokens
+                with torch.cuda.stream(on.stream):
+                    for name in ("routed_count", "kept_count", "send_count", "totals"):
+                        res[name].zero_()
             # what a later call may write: held here, so that it stays valid whatever becomes of the dict's entries
             res._bound = (key, nbytes, dict(res))
         else:

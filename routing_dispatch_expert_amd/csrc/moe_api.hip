@@ -1106,7 +1106,8 @@ int layer_few(const void* x, const void* W_router, const float* router_bias, con
               void* stream) {
   const int st = check_rank_limit(E, k, P, max_ranks);
   if (st != MOE_OK) return st;
-  if (!x || !W_router || !out) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  // without tokens x and out have no elements: any address will do
+  if ((T && (!x || !out)) || !W_router) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned16(x) || !aligned16(W_router) || !aligned16(out))
     return fail(MOE_ERR_INVALID_ARG, "x, W_router and out must be 16-byte aligned");
   const int eb = elem_bytes(dtype);
@@ -1209,7 +1210,7 @@ int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32
   if (R > moe::kFewMaxT) return fail(MOE_ERR_UNSUPPORTED, "R=%d > %d rows", R, moe::kFewMaxT);
   if (K > moe::kFewMaxWidth)
     return fail(MOE_ERR_UNSUPPORTED, "K must be at most %lld", static_cast<long long>(moe::kFewMaxWidth));
-  if (!x || !out) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (R && (!x || !out)) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned16(x) || !aligned16(out)) return fail(MOE_ERR_INVALID_ARG, "x and out must be 16-byte aligned");
   const size_t eb = elem_bytes(dtype);
   if (overlaps(x, R * K * eb, out, R * N * eb)) return fail(MOE_ERR_INVALID_ARG, "out overlaps x");
