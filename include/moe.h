@@ -302,7 +302,7 @@ int moe_combine(const void* x, const void* y, const int32_t* topk_idx, const flo
  *   MOE_Q4_E2M1: W = scale * v, v = 0, .5, 1, 1.5, 2, 3, 4, 6 by q's low three
  *                bits and negative where the fourth is set; `zero` must be NULL
  * group is 32, 64 or 128 (the last group of a row may be shorter), K a
- * multiple of 8, and a stack has fewer than 2^26 tiles (64 GiB of codes; else
+ * multiple of 8, and a stack has at most 2^26 - 4 tiles (64 GiB of codes; else
  * MOE_ERR_UNSUPPORTED). Layout (device memory, 16-byte aligned):
  *   codes [E][ceil(N/16)][ceil(K/128)][1024 bytes]: tiles of 16 rows by 128
  *     columns. Little-endian 32-bit word s (0 .. 3) of 16-byte piece l (0 .. 63)

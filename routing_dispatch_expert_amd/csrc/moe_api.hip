@@ -1029,10 +1029,10 @@ int check_q4_shape(int32_t E, int64_t N, int64_t K, int32_t group) {
   if (group != 32 && group != 64 && group != 128)
     return fail(MOE_ERR_INVALID_ARG, "group=%d must be 32, 64 or 128", group);
   if (K % 8) return fail(MOE_ERR_UNSUPPORTED, "K=%lld must be a multiple of 8", static_cast<long long>(K));
-  // a launch has fewer than 2^32 threads, 64 for a tile
-  const int64_t lim = int64_t{1} << 31, most = int64_t{1} << 26;
-  if (N >= lim || K >= lim || moe::ceil_div(N, 16) * moe::ceil_div(K, 128) >= moe::ceil_div(most, E))
-    return fail(MOE_ERR_UNSUPPORTED, "the weights must have fewer than 2^26 tiles");
+  // a launch has fewer than 2^32 threads; tiles take 64 each, four to a work-group
+  const int64_t lim = int64_t{1} << 31, most = (int64_t{1} << 26) - 4;
+  if (N >= lim || K >= lim || moe::ceil_div(N, 16) * moe::ceil_div(K, 128) > most / E)
+    return fail(MOE_ERR_UNSUPPORTED, "the weights must have at most 2^26 - 4 tiles");
   return MOE_OK;
 }
 
