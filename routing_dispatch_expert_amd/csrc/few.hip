@@ -35,17 +35,29 @@ enum WKind { kDenseBf16, kDenseF32, kU4, kE2m1 };
 
 // ---------------------------------------------------------------------------
 // Router scores. Block (expert tile, token tile, K slice); its waves split the
-// slice. Every MFMA starts from zero and its fp32 sums of 32 (fp32 inputs: 16)
-// products are added up in fp64, so that the scores' order is decided well
-// below fp32's rounding: sums of different order pick the same experts. Bound by
-// latency: W_router (3.7 MB at E = 256, d = 7168) over 128 work-groups, 4.5 us.
+// slice. Products and sums are taken in fp64 on the matrix cores, where products
+// of bf16 or fp32 numbers are exact: a score is off by at most (d + 16) 2^-53
+// times the sum of its products' magnitudes, so the scores' order is decided far
+// below fp32's rounding, and sums in another order pick the same experts unless
+// their scores are that close. Bound by latency.
 // ---------------------------------------------------------------------------
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+// The numbers of a 16-byte piece.
+template <bool BF16>
+__device__ inline double piece_value(const uint4& v, int i) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (BF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  return __uint_as_float(w[i]);
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void* xv, const void* wv, int T, int E, int64_t d,
                                                               int S, double* __restrict__ part,
                                                               bf16_t* __restrict__ parts) {
   __shared__ double red[kRouterWaves][64][4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16, s = blockIdx.z;
   const int64_t block = (static_cast<int64_t>(s) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
   const int64_t nthreads = static_cast<int64_t>(gridDim.x) * gridDim.y * gridDim.z * kRouterThreads;
@@ -56,7 +68,7 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void* 
   const int64_t er = std::min(e0 + col, E - 1), tr = std::min(t0 + col, T - 1);
   const char* wr = static_cast<const char*>(wv) + er * d * (16 / kVec);
   const char* xr = static_cast<const char*>(xv) + tr * d * (16 / kVec);
-  double acc[4] = {0, 0, 0, 0};
+  f64x4 acc = {0, 0, 0, 0};
   constexpr int U = 8;  // steps whose loads are in flight together
   for (int64_t j = j0; j < j1; j += U) {
     uint4 a[U], b[U];
@@ -71,28 +83,21 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void* 
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      f32x4 p = {0, 0, 0, 0};
-      if constexpr (BF16) {
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[u]), __builtin_bit_cast(bf16x8, b[u]),
-                                                    p, 0, 0, 0);
-      } else {
-        const f32x4 av = __builtin_bit_cast(f32x4, a[u]), bv = __builtin_bit_cast(f32x4, b[u]);
+      if (j + u >= j1) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[i], p, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] += static_cast<double>(p[i]);
+      for (int i = 0; i < kVec; ++i)  // lane: column c + i of expert row lane % 16 and of token lane % 16
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64(piece_value<BF16>(a[u], i), piece_value<BF16>(b[u], i), acc, 0, 0, 0);
     }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) red[wave][lane][i] = acc[i];
   __syncthreads();
-  // thread: element i of lane l, i.e. expert row 4 (l / 16) + i and token l % 16
+  // thread: element i of lane l, i.e. expert row 4 i + l / 16 and token l % 16
   const int l = threadIdx.x >> 2, i = threadIdx.x & 3;
   double v = 0;
 #pragma unroll
   for (int w = 0; w < kRouterWaves; ++w) v += red[w][l][i];
-  const int e = e0 + 4 * (l >> 4) + i, t = t0 + (l & 15);
+  const int e = e0 + 4 * i + (l >> 4), t = t0 + (l & 15);
   if (e < E && t < T) part[(static_cast<int64_t>(s) * T + t) * E + e] = v;
 }
 
