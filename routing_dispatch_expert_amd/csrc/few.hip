@@ -29,7 +29,7 @@
 namespace moe {
 namespace {
 
-constexpr int kRouterWaves = 4, kRouterThreads = 64 * kRouterWaves;
+constexpr int kRouterWaves = 8, kRouterThreads = 64 * kRouterWaves;
 
 enum WKind { kDenseBf16, kDenseF32, kU4, kE2m1 };
 
@@ -92,6 +92,7 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void* 
 #pragma unroll
   for (int i = 0; i < 4; ++i) red[wave][lane][i] = acc[i];
   __syncthreads();
+  if (threadIdx.x >= 256) return;
   // thread: element i of lane l, i.e. expert row 4 i + l / 16 and token l % 16
   const int l = threadIdx.x >> 2, i = threadIdx.x & 3;
   double v = 0;
