@@ -357,8 +357,10 @@ int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32
 /* The layer for few tokens, T <= 64, E <= 1024, d and d_ff <= 2^22 (else
  * MOE_ERR_UNSUPPORTED):
  * the formula, arguments and checks of moe_layer_forward, computed by reading
- * each chosen expert's weights once instead of through capacity-padded
- * buckets. Differences:
+ * each chosen expert's weights for its copies, 16 at a time, instead of through
+ * capacity-padded buckets (32 at a time where T k > 8 E, except with fp32
+ * activations beside 4-bit weights; an expert with more copies has its weights
+ * read again for the next 16 or 32). Differences:
  *  - the scores are summed in fp64 and compared so (moe_layer_forward compares
  *    fp32 sums): experts whose scores differ by less than fp32's rounding may
  *    be ordered differently by the two;

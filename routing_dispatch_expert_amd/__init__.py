@@ -684,7 +684,7 @@ class FewResult(dict):
 
 def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None, stream=None, max_ranks=0, out=None):
     """The layer for up to 64 tokens, as forward(), reading each chosen expert's
-    weights once; W_gate, W_up and W_down are tensors of x's dtype or, all three,
+    weights once for every 16 (or 32: moe.h) of its copies; W_gate, W_up and W_down are tensors of x's dtype or, all three,
     Q4Weights. Returns a dict as forward() does, without buckets or
     activations. out: the result of an earlier call with the same sizes, whose
     tensors this call writes instead of allocating new ones. Runs on torch's
