@@ -646,7 +646,8 @@ def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
     """out[r] = W[expert[r]] x[r] for up to 64 rows x [R, K] and a Q4Weights W
     [E, N, K]; expert int32 [R], or None for matrix 0. Rows whose expert is
     outside [0, E) are left as they are in `out` (zero if it is not given).
-    Returns a dict out, workspace, which may be passed in again."""
+    Returns a dict out, workspace, which may be passed in again (a workspace
+    that is too small is replaced)."""
     import torch
     E, N, K = W.shape
     R = x.shape[0]
@@ -656,6 +657,8 @@ def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
         _require(expert, "expert", torch.int32, (R,))
     dev = x.device
     _same_device(dev, "W expert out workspace", W, expert, out, workspace)
+    if workspace is not None and not workspace.is_contiguous():   # its memory may be less than its size
+        raise ValueError("workspace: need a contiguous tensor")
     with _On(dev, stream) as on:
         if out is None:
             out = on.empty((R, N), x.dtype)

@@ -77,3 +77,44 @@ def test_copied_and_saved(how):
         assert torch.equal(a, b) and a.data_ptr() != b.data_ptr()
     assert (r.shape, r.group, r.kind) == (q.shape, q.group, q.kind)
     follows(r)
+
+
+class _Host:
+    """Stands for the device and stream of a call on host tensors."""
+    stream, other = None, None
+
+    def __init__(self, device, stream):
+        pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        pass
+
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype)
+
+    def lent(self, t):
+        return t
+
+
+@pytest.mark.parametrize("workspace", [None, torch.empty(1, dtype=torch.uint8), torch.empty(1 << 20, dtype=torch.uint8),
+                                       torch.empty(1, dtype=torch.uint8).expand(1 << 20),
+                                       torch.empty(1 << 20, dtype=torch.uint8)[::4096].expand(4096, 256).t()],
+                         ids=["none", "small", "large", "one byte expanded", "strided"])
+def test_workspace_has_the_bytes_it_is_passed_for(workspace, monkeypatch):
+    """What reaches the kernels as a workspace is one block of at least the size needed, whatever is lent."""
+    passed = {}
+    monkeypatch.setattr(moe, "_On", _Host)
+    monkeypatch.setattr(moe, "moe_q4_matvec", lambda *a: passed.update(ws=a[9], n=a[10]))
+    try:
+        moe.matvec_q4(torch.zeros(3, 136), made(), workspace=workspace)
+    except ValueError as e:
+        assert "workspace" in str(e) and not workspace.is_contiguous()
+        return
+    ws, n = passed["ws"], passed["n"]
+    assert n == moe.moe_q4_matvec_workspace_size(3, 136, "f32") > 0
+    assert ws.untyped_storage().nbytes() - ws.storage_offset() * ws.element_size() >= n
+    if workspace is not None and workspace.numel() >= n:
+        assert ws is workspace
