@@ -573,6 +573,8 @@ class _On:
         else:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=device)
+            elif stream.device != device:   # its kernels would run there, on memory that is not theirs
+                raise ValueError(f"stream: need a stream of {device}, got one of {stream.device}")
             if stream.cuda_stream != self.current.cuda_stream:
                 self.other = stream
         self.stream = stream

@@ -118,3 +118,22 @@ def test_workspace_has_the_bytes_it_is_passed_for(workspace, monkeypatch):
     assert ws.untyped_storage().nbytes() - ws.storage_offset() * ws.element_size() >= n
     if workspace is not None and workspace.numel() >= n:
         assert ws is workspace
+
+
+class _Stream:
+    def __init__(self, index, cuda_stream):
+        self.device, self.cuda_stream = torch.device("cuda", index), cuda_stream
+
+
+def test_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: _Stream(1, 16))
+    device = torch.device("cuda", 1)
+    assert moe._On(device, None).stream.cuda_stream == 16
+    on = moe._On(device, _Stream(1, 32))
+    assert on.stream is on.other and on.stream.cuda_stream == 32
+    assert moe._On(device, _Stream(1, 16)).other is None
+    with pytest.raises(ValueError, match="stream"):
+        moe._On(device, _Stream(0, 32))
+    with pytest.raises(ValueError, match="stream"):   # also where the handles happen to be equal (both null streams)
+        moe._On(device, _Stream(0, 16))
