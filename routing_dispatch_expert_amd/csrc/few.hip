@@ -457,7 +457,7 @@ using XType = std::conditional_t<KIND == kDenseF32, float, bf16_t>;
 
 // Units of a contraction of K columns.
 template <WKind KIND>
-__device__ inline int units_of(int64_t K) {
+__host__ __device__ inline int units_of(int64_t K) {
   return static_cast<int>(KIND == kDenseBf16 ? ceil_div(K, 64) : KIND == kDenseF32 ? ceil_div(K, 32) : ceil_div(K, 128));
 }
 
@@ -1263,18 +1263,24 @@ hipError_t by_weights(const FewWeights& w, bool bf16, bool wide, F&& g) {
 // Experts that T tokens with k of E each hit, if each choice were as likely.
 double expected_distinct(int E, int k, int T) { return E * (1 - std::pow(1 - static_cast<double>(k) / E, T)); }
 
-// f(waves of a work-group) for about `items` pairs of strips. The chip holds
-// 4096 waves: with few items more waves share one, so that the memory has
-// enough to do (u4 row product, 128 items of 14336 columns: 13.8 us with eight
-// waves, 17.2 with four; 448 items of 4096: 12.0 and 11.6). Two waves instead of
-// four put 1024 - 2048 items on the chip at once (e2m1, 64 rows: 16.2 us, 19.0
-// with four). With very many, one wave alone spares the joining (64 tokens of
-// a DeepSeek-V3-shaped layer: bf16 3.03 ms, 3.24 with four; u4 1.07 and 1.10);
-// below, its long items would leave the last round's waves alone with the
-// memory (1.2 rounds of single waves: 254 us instead of 219 with four).
-template <int PARTS, typename F>
-void by_waves(double items, F&& f) {
-  if (PARTS == 1 && items <= 512)
+// f(waves of a work-group) for about `items` pairs of strips over K columns. The
+// chip holds 4096 waves: with few items and long rows more waves share one, so
+// that the memory has enough to do; short rows leave eight waves a few units each
+// and the joining to pay. Eight and four waves, one row of 128, 256 and 448 items:
+// u4 row product, K = 14336: 14.6, 15.8, 23.2 and 17.6, 21.0, 24.7 us; K = 8192:
+// 10.3, 11.8, 16.0 and 11.0, 12.3, 15.9; K = 5632 (44 units): 9.0, 10.2, 13.9 and
+// 9.2, 10.9, 13.0; K = 4096 (32): 8.3, 10.6, 12.6 and 7.8, 8.8, 11.0; K = 2048: 6.4,
+// 7.2, 9.4 and 6.0, 6.4, 8.1. The layer with one chosen expert, bf16, d = 8192 (128
+// units): 46, 57, 85 and 47, 64, 95 us; d = 4096 (64): 36, 40, 53 and 36, 39, 51;
+// d = 2048: 27, 35, 41 and 26, 32, 38; fp32, d = 4096 (128): 46, 58, 85 and 47, 59,
+// 83. Two waves instead of four put 1024 - 2048 items on the chip at once (e2m1,
+// 64 rows: 16.2 us, 19.0 with four). With very many, one wave alone spares the
+// joining (64 tokens of a DeepSeek-V3-shaped layer: bf16 3.03 ms, 3.24 with four);
+// below, its long items would leave the last round's waves alone with the memory
+// (1.2 rounds of single waves: 254 us instead of 219 with four).
+template <WKind KIND, int PARTS, typename F>
+void by_waves(double items, int64_t K, F&& f) {
+  if (PARTS == 1 && items <= 512 && units_of<KIND>(K) >= (is_dense(KIND) ? 80 : 40))
     f(std::integral_constant<int, 8>{});
   else if (items > 1024 && items <= 2048)
     f(std::integral_constant<int, 2>{});
@@ -1356,7 +1362,7 @@ hipError_t launch_few_layer(const FewLayer& L, hipStream_t s) {
     constexpr int kGpt = decltype(gpt)::value, kParts = decltype(parts)::value;
     constexpr bool kWide = decltype(two)::value;
     const int64_t ft = ceil_div(L.f, 16);
-    by_waves<kParts>(expected_distinct(L.E, L.k, L.T) * ft, [&](auto waves) {
+    by_waves<kKind, kParts>(expected_distinct(L.E, L.k, L.T) * ft, L.d, [&](auto waves) {
       constexpr int W = decltype(waves)::value;
       few_gate_up_kernel<kKind, kGpt, kParts, kWide, W>
           <<<dim3(static_cast<unsigned>(act * ft)), dim3(W * 64), 0, s>>>(a);
@@ -1398,7 +1404,7 @@ hipError_t launch_q4_matvec(const void* x, bool bf16, const int32_t* expert, con
       constexpr int kGpt = decltype(gpt)::value, kParts = decltype(parts_)::value;
       constexpr bool kWide = decltype(two)::value;
       const int64_t nt = ceil_div(N, 32);
-      by_waves<kParts>((expert ? expected_distinct(E, 1, R) : 1) * nt, [&](auto waves) {
+      by_waves<kKind, kParts>((expert ? expected_distinct(E, 1, R) : 1) * nt, K, [&](auto waves) {
         constexpr int W = decltype(waves)::value;
         matvec_kernel<kKind, kGpt, kParts, kWide, W>
             <<<dim3(static_cast<unsigned>(groups * nt)), dim3(W * 64), 0, s>>>(a);
