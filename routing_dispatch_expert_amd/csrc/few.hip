@@ -107,7 +107,8 @@ __global__ __launch_bounds__(kRouterThreads) void few_router_kernel(const void* 
 // token, so that the lists need no second launch. Bound by latency, k rounds of
 // a maximum over a wave in a row (each by register shifts; scores loaded
 // together): 5 us (4 tokens, E = 8) to 27 us (64 tokens, E = 256, k = 8, where
-// the products after it take 3 ms).
+// the products after it take 3 ms). With more than 256 experts a lane holds 16
+// scores, and the kernel spills about 80 registers (330 bytes a lane).
 // ---------------------------------------------------------------------------
 
 // Monotone map of a double to uint64 and back; NaN sorts below every number
@@ -1258,8 +1259,6 @@ hipError_t by_weights(const FewWeights& w, bool bf16, bool wide, F&& g) {
   return group(integral_constant<WKind, kE2m1>{});
 }
 
-}  // namespace
-
 // Experts that T tokens with k of E each hit, if each choice were as likely.
 double expected_distinct(int E, int k, int T) { return E * (1 - std::pow(1 - static_cast<double>(k) / E, T)); }
 
@@ -1289,6 +1288,8 @@ void by_waves(double items, int64_t K, F&& f) {
   else
     f(std::integral_constant<int, 1>{});
 }
+
+}  // namespace
 
 // Slices of d for the router scores: enough work-groups to spread W_router
 // over the chip, slices of 512 columns at least, and few enough partial scores
