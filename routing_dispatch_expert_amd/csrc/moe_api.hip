@@ -553,6 +553,8 @@ int moe_backward_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E, i
   return MOE_OK;
 }
 
+}  // extern "C"
+
 namespace {
 
 // The backward; with `saved` (a kept forward state) the routing, buckets and
@@ -720,6 +722,8 @@ int layer_backward(const void* x, const void* W_router, const float* router_bias
 }
 
 }  // namespace
+
+extern "C" {
 
 int moe_layer_backward(const void* x, const void* W_router, const float* router_bias, const void* W_gate,
                        const void* W_up, const void* W_down, const void* dout, int64_t T, int64_t d, int64_t d_ff,
@@ -1020,6 +1024,8 @@ int moe_combine(const void* x, const void* y, const int32_t* topk_idx, const flo
   return MOE_OK;
 }
 
+}  // extern "C"
+
 namespace {
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -1156,6 +1162,8 @@ int layer_few(const void* x, const void* W_router, const float* router_bias, con
 }
 
 }  // namespace
+
+extern "C" {
 
 int moe_q4_size(int32_t E, int64_t N, int64_t K, int32_t group, size_t* codes_bytes, size_t* scale_bytes,
                 size_t* zero_bytes) {
