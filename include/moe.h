@@ -372,7 +372,8 @@ int moe_q4_matvec(const void* x, const int32_t* expert, const moe_q4_t* W, int32
  * Dropless serving takes cf = E / k (C = T). moe_layer_forward_few_q4 takes
  * the experts' matrices in 4 bits (kind, group and the use of zero the same
  * for all three; d and d_ff multiples of 8); dtype is that of x, W_router and
- * out, and the activations keep its precision (h is rounded to it). workspace:
+ * out, and the activations keep its precision (h is rounded to it). U4 sums are
+ * taken as moe_q4_matvec takes them, with its limit on x and h. workspace:
  * moe_few_workspace_size() bytes, 256-byte aligned; q4 is 1 for 4-bit weights,
  * else 0. */
 int moe_few_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P,

@@ -13,8 +13,8 @@
 // experts with the lists of their copies (one work-group), the gate and up
 // products with h = silu(g) u, and the down product with the combine. With one
 // token of a DeepSeek-V3-shaped layer (d = 7168, d_ff = 2048, 8 of 256 experts)
-// they take 4.5, 7.9, 74 and 46 us in bf16 (705 MB of weights at 5.9 TB/s in the
-// two products), and 4.5, 7.9, 26 - 31 and 15 - 17 us in u4 (184 MB at 4.1).
+// they take 5.8, 8.1, 75 and 45 us in bf16 (705 MB of weights at 5.9 TB/s in the
+// two products), and 5.8, 8.1, 27 and 17 us in u4 (184 MB at 4.2).
 //
 // Nothing here depends on the order in which work-groups run: every sum has a
 // fixed order, and the expert lists are built by ranks, not by arrival.
@@ -39,7 +39,10 @@ enum WKind { kDenseBf16, kDenseF32, kU4, kE2m1 };
 // of bf16 or fp32 numbers are exact: a score is off by at most (d + 16) 2^-53
 // times the sum of its products' magnitudes, so the scores' order is decided far
 // below fp32's rounding, and sums in another order pick the same experts unless
-// their scores are that close. Bound by latency.
+// their scores are that close. Bound by latency: W_router (3.7 MB at E = 256, d =
+// 7168) over 128 work-groups and then 32 products of four columns a wave, one
+// after the other, 5.8 us for one token; 9.0 us and 56 products for 64 tokens.
+// (Four waves a work-group, with twice as many products each: 1 us more.)
 // ---------------------------------------------------------------------------
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
@@ -967,7 +970,10 @@ __device__ inline void gate_up_tile(const FewArgs& a, int64_t e, int p0, int n, 
     if constexpr (KIND == kDenseF32) {
       *reinterpret_cast<f32x4*>(static_cast<float*>(a.h) + at) = h;
     } else if constexpr (PARTS == 1) {
-      uint2 b;  // rounded as the layer rounds h between its two products
+      // Rounded as moe_layer_forward rounds h between its two products, so that the down product takes one matrix
+      // instruction a step: out's relative error (root mean square, against 64 bits) grows from 1.64 - 1.66e-3, the
+      // rounding of out alone, to 1.67 - 1.79e-3. Two bf16 parts would take twice the products and staged h.
+      uint2 b;
       b.x = f32_to_bf16(h[0]) | static_cast<uint32_t>(f32_to_bf16(h[1])) << 16;
       b.y = f32_to_bf16(h[2]) | static_cast<uint32_t>(f32_to_bf16(h[3])) << 16;
       *reinterpret_cast<uint2*>(static_cast<bf16_t*>(a.h) + at) = b;
