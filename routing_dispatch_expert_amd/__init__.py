@@ -684,7 +684,8 @@ def matvec_q4(x, W, expert=None, out=None, workspace=None, stream=None):
 
 class FewResult(dict):
     """What forward_few returns. Passed to a later call as `out` it lends that
-    call its outputs and workspace."""
+    call the outputs and workspace that it was made with, and shows them again
+    whatever became of its entries meanwhile."""
 
 
 def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None, stream=None, max_ranks=0, out=None):
@@ -732,6 +733,7 @@ def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None,
             res = out
             if not isinstance(res, FewResult) or res._bound[0] != key:
                 raise ValueError("out: need the result of a forward_few call with the same sizes, types and device")
+            res.update(res._bound[2])   # entries that were replaced or removed are this call's outputs again
             for t in res._bound[2].values():
                 if isinstance(t, torch.Tensor):
                     on.lent(t)

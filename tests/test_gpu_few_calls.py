@@ -198,3 +198,21 @@ def test_streams_at_once_on_larger_layers():
     for i in range(3):
         for o in got[i]:
             assert torch.equal(o.view(torch.int16), want[i].view(torch.int16)), i
+
+
+def test_lent_result_shows_what_the_call_wrote():
+    """Entries of a result that were replaced or taken out hold the later call's outputs, not what was put there."""
+    wr, *ws = weights(torch.bfloat16)
+    x = [torch.randn(5, 256, device="cuda").bfloat16() for _ in range(2)]
+    want = {k: v.clone() for k, v in moe.forward_few(x[1], wr, *ws, k=2, cf=0.5).items() if isinstance(v, torch.Tensor)}
+    r = moe.forward_few(x[0], wr, *ws, k=2, cf=0.5)
+    r["out"] = r["out"].clone()
+    r["topk_w"] = r["topk_w"].double()
+    del r["slot"], r["C"]
+    r["workspace"] = None
+    r["mine"] = 1
+    s = moe.forward_few(x[1], wr, *ws, k=2, cf=0.5, out=r)
+    torch.cuda.synchronize()
+    assert s is r and s["C"] == 1 and s["mine"] == 1
+    for name in ("out", "topk_idx", "topk_w", "slot", "routed_count", "kept_count", "send_count", "totals"):
+        assert torch.equal(s[name], want[name]), name
