@@ -690,11 +690,12 @@ class FewResult(dict):
 
 def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None, stream=None, max_ranks=0, out=None):
     """The layer for up to 64 tokens, as forward(), reading each chosen expert's
-    weights once for every 16 (or 32: moe.h) of its copies; W_gate, W_up and W_down are tensors of x's dtype or, all three,
-    Q4Weights. Returns a dict as forward() does, without buckets or
-    activations. out: the result of an earlier call with the same sizes, whose
-    tensors this call writes instead of allocating new ones. Runs on torch's
-    current stream unless one is given."""
+    weights once for every 16 (or 32: moe.h) of its copies; W_gate, W_up and
+    W_down are tensors of x's dtype or, all three, Q4Weights. Returns a dict as
+    forward() does, without buckets or activations. out: the result of an
+    earlier call with the same sizes, whose tensors this call writes instead of
+    allocating new ones. Runs on torch's current stream unless one is given (a
+    stream of x's device or its address, which outlives the call's tensors)."""
     import torch
     T, d = x.shape
     E = W_router.shape[0]
