@@ -387,6 +387,41 @@ int moe_layer_forward_few_q4(const void* x, const void* W_router, const float* r
                              int32_t E, int32_t k, float cf, int32_t P, int32_t max_ranks, moe_dtype_t dtype,
                              void* out, moe_stats_t* stats, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The gate in its general form ----
+ *
+ * Scores s of the logits l [T, E] (fp32): MOE_SCORE_SOFTMAX over all E experts,
+ * or MOE_SCORE_SIGMOID. The experts are ordered by v = s + bias (bias [E] fp32, a
+ * balance correction that moves the choice and not the weights), or by l, the
+ * order of s, where bias is NULL; on a tie the lower index is first.
+ * groups > 1 (E % groups == 0, at most 64): group g has the experts [g E/groups,
+ * (g + 1) E/groups); its value is the sum of its group_best (1 or 2, at most
+ * E/groups) largest v (without a bias: of s for 2, of l for 1); the k experts are
+ * taken from the top_groups best groups (lower group first on a tie).
+ * topk_w[t, j] = scale * s_j, with renormalize divided by the sum of the chosen s
+ * (0 where that sum is 0). Scores and order are evaluated in fp64, topk_w is
+ * rounded to fp32. A NaN sorts below every number; the k experts are distinct
+ * whatever the logits are. Limits (else MOE_ERR_UNSUPPORTED): E <= 4096, k <= 32,
+ * T k < 2^31. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct {
+  int32_t score;
+  int32_t groups;      /* 1: no limit */
+  int32_t top_groups;  /* 1 .. groups, top_groups * E/groups >= k */
+  int32_t group_best;  /* 1 or 2 */
+  int32_t renormalize; /* 0 or 1 */
+  float scale;         /* finite */
+} moe_gate_t;
+int moe_gate(const float* logits, const float* bias, const moe_gate_t* gate, int64_t T, int32_t E, int32_t k,
+             int32_t* topk_idx, float* topk_w, void* stream);
+
+/* dlogits [T, E] of the gradients d_topk_w [T, k] of the weights of the chosen
+ * topk_idx and, optionally, d_scores [T, E] of all scores s (a balance loss's);
+ * the choice is held fixed, of `gate` score, renormalize and scale are used. An
+ * index that a row has twice counts twice; one outside [0, E) passes no gradient.
+ * Written, not accumulated; dlogits must not overlap logits or d_scores. */
+int moe_gate_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, const float* d_scores,
+                      const moe_gate_t* gate, int64_t T, int32_t E, int32_t k, float* dlogits, void* stream);
+
 /* Stages of moe_layer_forward (and of moe_layer_forward_replicated, whose
  * ROUTE stage also ranks each expert's copies and deals them to instances),
  * in launch order. */

@@ -22,6 +22,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP
 MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
 MOE_Q4_U4, MOE_Q4_E2M1 = 0, 1
 Q4_KINDS = {"u4": MOE_Q4_U4, "e2m1": MOE_Q4_E2M1}
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 FEW_MAX_TOKENS = 64   # tokens of moe_layer_forward_few, rows of moe_q4_matvec
 TOTALS = ("dropped", "fully_dropped_tokens", "padded_rows", "offrank_bytes")
 
@@ -30,7 +32,7 @@ EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_layer_forward", "moe_backw
            "moe_permute_workspace_size", "moe_permute", "moe_permute_static", "moe_grouped_gemm_workspace_size",
            "moe_grouped_gemm", "moe_combine", "moe_q4_size", "moe_q4_quantize", "moe_q4_dequantize",
            "moe_q4_matvec_workspace_size", "moe_q4_matvec", "moe_few_workspace_size", "moe_layer_forward_few",
-           "moe_layer_forward_few_q4", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
+           "moe_layer_forward_few_q4", "moe_gate", "moe_gate_backward", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
 STAGES = ("router", "route", "slots", "scatter", "gate_up", "down", "combine")
 
 
@@ -51,6 +53,11 @@ class moe_stats_t(ctypes.Structure):
 class moe_q4_t(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
                 ("kind", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class moe_gate_t(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -91,6 +98,8 @@ _SIGS = {
     "moe_layer_forward_few_q4": [_P, _P, _P, ctypes.POINTER(moe_q4_t), ctypes.POINTER(moe_q4_t),
                                  ctypes.POINTER(moe_q4_t), _I64, _I64, _I64, _I32, _I32, _F32, _I32, _I32,
                                  ctypes.c_int, _P, ctypes.POINTER(moe_stats_t), _P, _SZ, _P],
+    "moe_gate": [_P, _P, ctypes.POINTER(moe_gate_t), _I64, _I32, _I32, _P, _P, _P],
+    "moe_gate_backward": [_P, _P, _P, _P, ctypes.POINTER(moe_gate_t), _I64, _I32, _I32, _P, _P],
     "moe_set_stage_events": [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int],
     "moe_stage_ran": [ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
 }
@@ -362,6 +371,24 @@ def moe_layer_forward_few_q4(x, W_router, router_bias, W_gate, W_up, W_down, T, 
                                           _q4(W_down), T, d, d_ff, E, k, cf, P, max_ranks, _dtype(dtype), _ptr(out),
                                           _stats(stats), _ptr(workspace), workspace_bytes, _stream(stream)),
            "moe_layer_forward_few_q4")
+
+
+def _gate(gate) -> "ctypes.POINTER(moe_gate_t) | None":
+    """gate: None or (score, groups, top_groups, group_best, renormalize, scale)."""
+    if gate is None:
+        return None
+    score, groups, top_groups, group_best, renormalize, scale = gate
+    return ctypes.pointer(moe_gate_t(SCORES.get(score, score), groups, top_groups, group_best, int(renormalize), scale))
+
+
+def moe_gate(logits, bias, gate, T, E, k, topk_idx, topk_w, stream=None):
+    _check(lib().moe_gate(_ptr(logits), _ptr(bias), _gate(gate), T, E, k, _ptr(topk_idx), _ptr(topk_w),
+                          _stream(stream)), "moe_gate")
+
+
+def moe_gate_backward(logits, topk_idx, d_topk_w, d_scores, gate, T, E, k, dlogits, stream=None):
+    _check(lib().moe_gate_backward(_ptr(logits), _ptr(topk_idx), _ptr(d_topk_w), _ptr(d_scores), _gate(gate), T, E, k,
+                                   _ptr(dlogits), _stream(stream)), "moe_gate_backward")
 
 
 def moe_set_stage_events(events):
@@ -746,3 +773,103 @@ def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None,
         call(x, W_router, router_bias, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, max_ranks, dtype, t["out"], t,
              t["workspace"], nbytes, on.stream)
     return res
+
+
+# ---------------------------------------------------- the gate
+
+def _gate_rule(score, groups, top_groups, group_best, renormalize, scale):
+    if score not in SCORES:
+        raise ValueError(f"score: need one of {sorted(SCORES)}, got {score!r}")
+    return score, groups, top_groups or groups, group_best, bool(renormalize), scale
+
+
+def _lent_result(out, key, what):
+    """The tensors of an earlier call's result, if it was of the same sizes."""
+    if not isinstance(out, Result) or out._bound[0] != key:
+        raise ValueError(f"out: need the result of a call of {what} with the same sizes, types and device")
+    out.update(out._bound[1])   # entries that were replaced or removed are this call's outputs again
+    return out
+
+
+class Result(dict):
+    """What gate, rmsnorm, rmsnorm_backward, experts_mx8 and forward_mx8 return.
+    Passed to a later call as `out` it lends that call the outputs and workspace
+    that it was made with, and shows them again whatever became of its entries."""
+
+    @classmethod
+    def of(cls, key, **entries):
+        res = cls(entries)
+        res._bound = (key, dict(res))
+        return res
+
+
+def gate(logits, k, score="softmax", bias=None, groups=1, top_groups=0, group_best=1, renormalize=True, scale=1.0,
+         out=None, stream=None):
+    """The choice of k experts a token and their weights from logits [T, E] (fp32).
+
+    score: "softmax" (over all experts) or "sigmoid". bias [E] fp32 or None is
+    added to the scores for the choice only. groups > 1: the experts come from the
+    top_groups (0: all) groups with the best sums of their group_best (1 or 2)
+    largest scores. topk_w is scale * score, divided by the chosen scores' sum
+    where renormalize. Ties go to the lower index (moe.h has the formulas).
+    Returns a dict topk_idx int32 [T, k], topk_w fp32 [T, k]. out: the result of
+    an earlier call with the same sizes, whose tensors this call writes. Runs on
+    torch's current stream unless one is given."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError(f"logits: need [T, E], got {tuple(logits.shape)}")
+    T, E = logits.shape
+    _require(logits, "logits", torch.float32, (T, E))
+    if bias is not None:
+        _require(bias, "bias", torch.float32, (E,))
+    rule = _gate_rule(score, groups, top_groups, group_best, renormalize, scale)
+    dev = logits.device
+    _same_device(dev, "bias", bias)
+    key = ("gate", T, E, k, dev)
+    with _On(dev, stream) as on:
+        if out is None:
+            res = Result.of(key, topk_idx=on.empty((T, k), torch.int32), topk_w=on.empty((T, k), torch.float32))
+        else:
+            res = _lent_result(out, key, "gate")
+            for t in res._bound[1].values():
+                on.lent(t)
+        if on.other is not None:
+            for t in (logits, bias):
+                if t is not None:
+                    on.lent(t)
+        t = res._bound[1]
+        moe_gate(logits, bias, rule, T, E, k, t["topk_idx"], t["topk_w"], on.stream)
+    return res
+
+
+def gate_backward(logits, topk_idx, d_topk_w, score="softmax", renormalize=True, scale=1.0, d_scores=None, out=None,
+                  stream=None):
+    """The logits' gradient [T, E] of gate()'s weights' gradient d_topk_w [T, k] for
+    the experts topk_idx that it chose and, optionally, of the scores' gradient
+    d_scores [T, E] (a balance loss's); score, renormalize and scale as for gate().
+    Written into `out` if it is given."""
+    import torch
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("logits, topk_idx: need [T, E] and [T, k]")
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    _require(logits, "logits", torch.float32, (T, E))
+    _require(topk_idx, "topk_idx", torch.int32, (T, k))
+    _require(d_topk_w, "d_topk_w", torch.float32, (T, k))
+    if d_scores is not None:
+        _require(d_scores, "d_scores", torch.float32, (T, E))
+    rule = _gate_rule(score, 1, 1, 1, renormalize, scale)
+    dev = logits.device
+    _same_device(dev, "topk_idx d_topk_w d_scores out", topk_idx, d_topk_w, d_scores, out)
+    with _On(dev, stream) as on:
+        if out is None:
+            out = on.empty((T, E), torch.float32)
+        else:
+            _require(out, "out", torch.float32, (T, E))
+            on.lent(out)
+        if on.other is not None:
+            for t in (logits, topk_idx, d_topk_w, d_scores):
+                if t is not None:
+                    on.lent(t)
+        moe_gate_backward(logits, topk_idx, d_topk_w, d_scores, rule, T, E, k, out, on.stream)
+    return out

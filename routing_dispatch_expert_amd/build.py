@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libmoe_hip.so")
 ARCH = "gfx950"
 
 SOURCES = ["moe_api.hip", "router.hip", "permute.hip", "grouped_gemm.hip", "combine.hip", "backward.hip",
-           "few.hip", "q4.hip"]
+           "few.hip", "q4.hip", "gate.hip"]
 
 
 def hipcc() -> str:

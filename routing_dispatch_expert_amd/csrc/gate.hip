@@ -1,0 +1,335 @@
+// The gate of the MoE layer in its general form, and its gradient (gfx950).
+//
+// Sources: "Expert Parallelism" (klaylearn.com glossary) - scores, top-k choice
+// and combine weights; "Expert Parallelism & All-to-All" (neelmishra.github.io),
+// "The bandwidth bill" - a token's experts limited to a few nodes.
+//
+//   s = sigmoid(l) or softmax(l) over the E experts;  v = s + bias, or the order of
+//   l itself without a bias (s grows with l); a group's value: the sum of its
+//   `best` largest v (of s without a bias and best = 2; max l with best = 1)
+//   idx = the k largest v of the top_groups best groups' experts
+//   w_j = scale s_j / sum over the chosen of s, or scale s_j
+//
+// Scores, sums and comparisons are in fp64: the scores of 256 experts lie so
+// close that in fp32 a rounding would swap one token's neighbours in some tens
+// of thousands, and the choice is compared elsewhere for equality. A wave has a
+// token; lane l holds the experts l, l + 64, ...
+#include "block.h"
+
+#include <climits>
+
+namespace moe {
+namespace {
+
+// Monotone map of a double to uint64; NaN lies below every number.
+__device__ inline uint64_t order_of(double v) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));  // -0 as 0
+  const uint64_t key = (u >> 63) ? ~u : (u | (uint64_t{1} << 63));
+  return v != v ? 0 : key;
+}
+
+template <typename V>
+__device__ inline V shfl_xor64(V v, int off) {
+  return __shfl_xor(v, off, 64);
+}
+
+__device__ inline double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+__device__ inline double wave_sum(double v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += shfl_xor64(v, off);
+  return v;
+}
+
+__device__ inline double wave_max(double v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = fmax(v, shfl_xor64(v, off));
+  return v;
+}
+
+// Lanes that share a group's experts when its value is formed: 64 over the
+// groups, rounded down to a power of two.
+__device__ inline int lanes_of_group(int groups) { return 1 << (31 - __clz(64 / groups)); }
+
+// NE: scores a lane holds (E <= 64 NE). LDS: [waves][E] doubles with groups.
+template <int NE>
+__global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
+                                                   GateRule g, int64_t T, int E, int k, int32_t* __restrict__ idx,
+                                                   float* __restrict__ w) {
+  extern __shared__ double smem[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 6) + wave;
+  if (t >= T) return;  // no barrier below
+  double l[NE], s[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane + 64 * i;
+    l[i] = e < E ? static_cast<double>(logits[t * E + e]) : -INFINITY;
+  }
+  // the scores, where the choice needs them
+  const bool scores = bias || (g.groups > 1 && g.best > 1) || (!g.sigmoid && !g.renormalize);
+  double top = 0, total = 1;
+  if (!g.sigmoid && scores) {
+    top = l[0];
+#pragma unroll
+    for (int i = 1; i < NE; ++i) top = fmax(top, l[i]);
+    top = wave_max(top);
+    if (top == -INFINITY) top = 0;  // every expert masked: all scores are 0
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      s[i] = lane + 64 * i < E ? exp(l[i] - top) : 0;
+      total += s[i];
+    }
+    total = wave_sum(total);
+    if (total == 0) total = 1;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s[i] /= total;
+  } else if (scores) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s[i] = sigmoid64(l[i]);
+  }
+  uint64_t key[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane + 64 * i;
+    key[i] = e < E ? order_of(bias ? s[i] + static_cast<double>(bias[e]) : l[i]) : 0;
+  }
+  uint64_t taken = 0;  // bit i: expert lane + 64 i is chosen already or not allowed (NE <= 64)
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    if (lane + 64 * i >= E) taken |= uint64_t{1} << i;
+  if (g.groups > 1) {
+    const int per = E / g.groups, lpg = lanes_of_group(g.groups), sub = lane % lpg, mine = lane / lpg;
+    double* v = smem + wave * E;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = lane + 64 * i;
+      if (e < E) v[e] = bias ? s[i] + static_cast<double>(bias[e]) : g.best > 1 ? s[i] : l[i];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    double a = -INFINITY, b = -INFINITY;  // the two largest of the lane's part of its group
+    if (mine < g.groups)
+      for (int i = sub; i < per; i += lpg) {
+        const double x = v[mine * per + i];
+        if (x > a) {
+          b = a;
+          a = x;
+        } else if (x > b) {
+          b = x;
+        }
+      }
+    for (int off = 1; off < lpg; off <<= 1) {
+      const double oa = shfl_xor64(a, off), ob = shfl_xor64(b, off);
+      b = fmax(fmin(a, oa), fmax(b, ob));
+      a = fmax(a, oa);
+    }
+    const uint64_t value = order_of(g.best > 1 ? a + b : a);
+    int ahead = 0;  // groups that are better, or as good and before this one
+    for (int o = 0; o < g.groups; ++o) {
+      const uint64_t ov = __shfl(value, o * lpg, 64);
+      ahead += (ov > value || (ov == value && o < mine)) ? 1 : 0;
+    }
+    const uint64_t kept = __ballot(mine < g.groups && ahead < g.top_groups);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = lane + 64 * i;
+      if (e < E && !((kept >> (e / per * lpg)) & 1)) taken |= uint64_t{1} << i;
+    }
+  }
+  int my_e = 0;  // lane j < k: the j-th choice
+  double my_l = 0;
+  for (int j = 0; j < k; ++j) {
+    uint64_t best = 0;
+    int be = INT_MAX;
+    double bl = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (!((taken >> i) & 1) && (be == INT_MAX || key[i] > best)) {
+        best = key[i];
+        be = lane + 64 * i;
+        bl = l[i];
+      }
+    int win = lane;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      const uint64_t ok = shfl_xor64(best, off);
+      const int oe = shfl_xor64(be, off), ow = shfl_xor64(win, off);
+      if (be == INT_MAX ? oe != INT_MAX : (oe != INT_MAX && (ok > best || (ok == best && oe < be)))) {
+        best = ok;
+        be = oe;
+        win = ow;
+      }
+    }
+    bl = __shfl(bl, win, 64);
+    if (lane == be % 64) taken |= uint64_t{1} << (be / 64);
+    if (lane == j) {
+      my_e = be;
+      my_l = bl;
+    }
+  }
+  // weights of the chosen
+  const bool in = lane < k;
+  double z;
+  if (g.sigmoid) {
+    z = in ? sigmoid64(my_l) : 0;
+  } else if (g.renormalize) {  // a softmax over the chosen
+    const double m = wave_max(in ? my_l : -INFINITY);
+    z = in && m > -INFINITY ? exp(my_l - m) : 0;
+  } else {
+    z = in ? exp(my_l - top) / total : 0;
+  }
+  if (g.renormalize) {
+    const double sum = wave_sum(z);
+    z = sum > 0 ? z / sum : 0;
+  }
+  if (in) {
+    idx[t * k + lane] = my_e;
+    w[t * k + lane] = static_cast<float>(static_cast<double>(g.scale) * z);
+  }
+}
+
+// The gradient: with q_j = scale dw_j and D = sum q_i r_i over the chosen,
+//   renormalised: r_j = s_j / sum s, and dl_j += r_j (q_j - D) (1 - s_j for sigmoid, 1 for softmax)
+//   not:          sigmoid dl_j += q_j s_j (1 - s_j); softmax as if d_scores[j] were larger by q_j
+//   d_scores:     sigmoid dl_e += ds_e s_e (1 - s_e), softmax dl_e += s_e (ds_e - sum_i ds_i s_i)
+// The chosen ones' terms are in fp64 (a few a token), the dense ones in fp32.
+template <int NE>
+__global__ __launch_bounds__(256) void gate_backward_kernel(const float* __restrict__ logits,
+                                                            const int32_t* __restrict__ idx,
+                                                            const float* __restrict__ dw,
+                                                            const float* __restrict__ dscores, GateRule g, int64_t T,
+                                                            int E, int k, float* __restrict__ dlogits) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x * 4ll + wave;
+  if (t >= T) return;
+  float l[NE], ds[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane + 64 * i;
+    l[i] = e < E ? logits[t * E + e] : -INFINITY;
+    ds[i] = dscores && e < E ? dscores[t * E + e] : 0.f;
+  }
+  int e_j = -1;
+  double l_j = 0, q_j = 0;
+  if (lane < k) {
+    e_j = idx[t * k + lane];
+    if (e_j >= 0 && e_j < E) {
+      l_j = logits[t * E + e_j];
+      q_j = static_cast<double>(g.scale) * static_cast<double>(dw[t * k + lane]);
+    } else {
+      e_j = -1;  // an index outside passes no gradient
+    }
+  }
+  const bool in = e_j >= 0;
+  double term;  // of dl, or of d_scores where softmax scores are not renormalised
+  if (g.renormalize) {
+    double z;
+    if (g.sigmoid) {
+      z = in ? sigmoid64(l_j) : 0;
+    } else {
+      const double m = wave_max(in ? l_j : -INFINITY);
+      z = in && m > -INFINITY ? exp(l_j - m) : 0;
+    }
+    const double sum = wave_sum(z);
+    const double r = sum > 0 ? z / sum : 0;
+    const double D = wave_sum(q_j * r);
+    term = r * (q_j - D) * (g.sigmoid ? sigmoid64(-l_j) : 1.0);
+  } else {
+    term = g.sigmoid ? q_j * sigmoid64(l_j) * sigmoid64(-l_j) : q_j;
+  }
+  const float add = in ? static_cast<float>(term) : 0.f;
+  const bool soft = !g.sigmoid && !g.renormalize;  // the term belongs to d_scores
+  float dl[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) dl[i] = 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int e = __builtin_amdgcn_readlane(e_j, j);
+    const float v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(add), j));
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (e == lane + 64 * i) {
+        if (soft)
+          ds[i] += v;
+        else
+          dl[i] += v;
+      }
+  }
+  if (dscores || soft) {
+    if (g.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const float a = expf(-fabsf(l[i])), b = 1.f / (1.f + a);  // s and 1 - s are b and a b
+        dl[i] += ds[i] * (a * b * b);
+      }
+    } else {
+      float m = l[0];
+#pragma unroll
+      for (int i = 1; i < NE; ++i) m = fmaxf(m, l[i]);
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, shfl_xor64(m, off));
+      float p[NE], sum = 0.f, dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        p[i] = lane + 64 * i < E && m > -INFINITY ? expf(l[i] - m) : 0.f;
+        sum += p[i];
+        dot += p[i] * ds[i];
+      }
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) {
+        sum += shfl_xor64(sum, off);
+        dot += shfl_xor64(dot, off);
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      dot *= inv;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) dl[i] += p[i] * inv * (ds[i] - dot);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane + 64 * i;
+    if (e < E) dlogits[t * E + e] = dl[i];
+  }
+}
+
+}  // namespace
+
+#define MOE_GATE_BY_E(CALL)   \
+  do {                        \
+    if (E <= 64) {            \
+      CALL(1);                \
+    } else if (E <= 128) {    \
+      CALL(2);                \
+    } else if (E <= 256) {    \
+      CALL(4);                \
+    } else if (E <= 512) {    \
+      CALL(8);                \
+    } else if (E <= 1024) {   \
+      CALL(16);               \
+    } else {                  \
+      CALL(64);               \
+    }                         \
+  } while (0)
+
+hipError_t launch_gate(const float* logits, const float* bias, const GateRule& g, int64_t T, int E, int k, int32_t* idx,
+                       float* w, hipStream_t s) {
+  const int waves = E <= 1024 ? 4 : 1;  // at most 32 KiB of LDS
+  const dim3 grid(static_cast<unsigned>(ceil_div(T, waves)));
+  const size_t lds = g.groups > 1 ? waves * static_cast<size_t>(E) * sizeof(double) : 0;
+#define MOE_CALL(NE) gate_kernel<NE><<<grid, dim3(64 * waves), lds, s>>>(logits, bias, g, T, E, k, idx, w)
+  MOE_GATE_BY_E(MOE_CALL);
+#undef MOE_CALL
+  return hipGetLastError();
+}
+
+hipError_t launch_gate_backward(const float* logits, const int32_t* idx, const float* dw, const float* dscores,
+                                const GateRule& g, int64_t T, int E, int k, float* dlogits, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(T, 4)));
+#define MOE_CALL(NE) gate_backward_kernel<NE><<<grid, dim3(256), 0, s>>>(logits, idx, dw, dscores, g, T, E, k, dlogits)
+  MOE_GATE_BY_E(MOE_CALL);
+#undef MOE_CALL
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "block.h"
 #include "common.h"
 #include "few.h"
 
@@ -1280,6 +1281,78 @@ int moe_layer_forward_few_q4(const void* x, const void* W_router, const float* r
                              {W_gate->scale, W_up->scale, W_down->scale}, {W_gate->zero, W_up->zero, W_down->zero}};
   return layer_few(x, W_router, router_bias, w, T, d, d_ff, E, k, C, P, max_ranks, dtype, out, stats, workspace,
                    workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_gate(const moe_gate_t* g, int64_t T, int32_t E, int32_t k) {
+  if (!g) return fail(MOE_ERR_INVALID_ARG, "gate is NULL");
+  if (T < 0 || E < 1 || k < 1 || k > E) return fail(MOE_ERR_INVALID_ARG, "need T >= 0, 1 <= k <= E");
+  if (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARG, "unknown score %d", g->score);
+  if (g->renormalize != 0 && g->renormalize != 1) return fail(MOE_ERR_INVALID_ARG, "renormalize must be 0 or 1");
+  if (!std::isfinite(g->scale)) return fail(MOE_ERR_INVALID_ARG, "scale must be finite");
+  if (g->groups < 1 || E % g->groups) return fail(MOE_ERR_INVALID_ARG, "groups=%d must be >= 1 and divide E=%d", g->groups, E);
+  if (E > kMaxE || k > kMaxK) return fail(MOE_ERR_UNSUPPORTED, "E or k too large");
+  if (g->groups > 1) {
+    const int per = E / g->groups;
+    if (g->groups > moe::kGateMaxGroups)
+      return fail(MOE_ERR_UNSUPPORTED, "groups=%d > %d", g->groups, moe::kGateMaxGroups);
+    if (g->group_best < 1 || g->group_best > 2 || g->group_best > per)
+      return fail(MOE_ERR_INVALID_ARG, "group_best=%d must be 1 or 2 and at most E/groups=%d", g->group_best, per);
+    if (g->top_groups < 1 || g->top_groups > g->groups)
+      return fail(MOE_ERR_INVALID_ARG, "top_groups=%d must be in [1, groups=%d]", g->top_groups, g->groups);
+    if (static_cast<int64_t>(g->top_groups) * per < k)
+      return fail(MOE_ERR_INVALID_ARG, "top_groups=%d groups of %d experts hold fewer than k=%d", g->top_groups, per, k);
+  }
+  // a launch has fewer than 2^32 threads, 64 of them a token
+  if (T >= (int64_t{1} << 26) - 4 || T * k >= (int64_t{1} << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "T must stay below 2^26 - 4 and T*k below 2^31");
+  return MOE_OK;
+}
+
+moe::GateRule gate_rule(const moe_gate_t& g) {
+  moe::GateRule r;
+  r.sigmoid = g.score == MOE_SCORE_SIGMOID;
+  r.renormalize = g.renormalize != 0;
+  r.groups = g.top_groups >= g.groups ? 1 : g.groups;  // all groups kept: no limit
+  r.top_groups = g.top_groups;
+  r.best = g.group_best;
+  r.scale = g.scale;
+  return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_gate(const float* logits, const float* bias, const moe_gate_t* gate, int64_t T, int32_t E, int32_t k,
+             int32_t* topk_idx, float* topk_w, void* stream) {
+  const int st = check_gate(gate, T, E, k);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_w) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  MOE_HIP_TRY(moe::launch_gate(logits, bias, gate_rule(*gate), T, E, k, topk_idx, topk_w,
+                               static_cast<hipStream_t>(stream)),
+              "gate");
+  return MOE_OK;
+}
+
+int moe_gate_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, const float* d_scores,
+                      const moe_gate_t* gate, int64_t T, int32_t E, int32_t k, float* dlogits, void* stream) {
+  const int st = check_gate(gate, T, E, k);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !d_topk_w || !dlogits) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  const size_t n = static_cast<size_t>(T) * E * sizeof(float);
+  if (overlaps(dlogits, n, logits, n) || (d_scores && overlaps(dlogits, n, d_scores, n)))
+    return fail(MOE_ERR_INVALID_ARG, "dlogits overlaps logits or d_scores");
+  MOE_HIP_TRY(moe::launch_gate_backward(logits, topk_idx, d_topk_w, d_scores, gate_rule(*gate), T, E, k, dlogits,
+                                        static_cast<hipStream_t>(stream)),
+              "gate backward");
+  return MOE_OK;
 }
 
 }  // extern "C"
