@@ -422,6 +422,61 @@ int moe_gate(const float* logits, const float* bias, const moe_gate_t* gate, int
 int moe_gate_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, const float* d_scores,
                       const moe_gate_t* gate, int64_t T, int32_t E, int32_t k, float* dlogits, void* stream);
 
+/* ---- 8-bit matrices ----
+ *
+ * A stack of matrices [E, N, K], or rows [R, K] (E = 1, N = R), in 8 bits: e4m3
+ * codes with a power-of-two scale for every 32 columns of a row (the last group
+ * may be shorter), as the matrix cores take them. K is a multiple of 16, E ceil(N/8)
+ * ceil(K/128) below 2^26 - 4 (else MOE_ERR_UNSUPPORTED). Device memory, 16-byte aligned:
+ *   codes [E][N][K] bytes
+ *   scale [E][ceil(K/128)][N][4] bytes: byte b of [s][n] belongs to row n's columns
+ *     128 s + 32 b .. + 31. Byte v: the scale 2^(v - 127); 255: NaN. Bytes of
+ *     groups that begin past K may hold anything (moe_mx8_quantize and moe_rmsnorm
+ *     write 127).
+ * A value is its code times its group's scale. */
+typedef struct {
+  void* codes;
+  void* scale;
+} moe_mx8_t;
+
+/* Bytes of codes and scale (either pointer may be NULL). Host only. */
+int moe_mx8_size(int32_t E, int64_t N, int64_t K, size_t* codes_bytes, size_t* scale_bytes);
+
+/* W [E, N, K] (dtype, 16-byte aligned) in 8 bits. A group's scale is the smallest
+ * power of two, at least 2^-126, of which 448 times is no less than the largest
+ * |w| (1 for a group of zeros), so that nothing saturates; codes are rounded to the
+ * nearest, ties to even. A group with an infinity or a NaN becomes NaN.
+ * moe_mx8_dequantize writes the values, rounded to dtype (bf16 holds them all but
+ * those below its smallest number). */
+int moe_mx8_quantize(const void* W, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, const moe_mx8_t* q, void* stream);
+int moe_mx8_dequantize(const moe_mx8_t* q, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, void* W, void* stream);
+
+/* ---- The norm in front of the layer ----
+ *
+ * For rows r < R of width d (a multiple of 8, fp32: of 4, with y8 of 16; at most
+ * 65536, fp32 32768):
+ *   h = x + residual, rounded to dtype (residual NULL: h = x, and h_out must be NULL)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)          fp32, sums of squares in fp32
+ *   y = h rstd weight                         rounded to dtype, and y8 to 8 bits, each from the fp32 value
+ * x, residual, weight [d], h_out, y: dtype, 16-byte aligned; of h_out, y, y8 (rows
+ * [R, d]) and rstd [R] any may be NULL. h_out may be x or residual itself; other
+ * outputs overlap no input. eps >= 0, finite. R below 2^22 (rows of up to 2048
+ * 16-byte words: 2^24, up to 256: 2^26). R == 0 returns MOE_OK. */
+int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int64_t R, int64_t d,
+                moe_dtype_t dtype, void* h_out, void* y, const moe_mx8_t* y8, float* rstd, void* stream);
+
+/* Its gradient, of dy [R, d] (dtype) for y and, if not NULL, dh_in [R, d] that
+ * arrives at h by another way (the stream's), from the forward's h and rstd:
+ *   a = dy weight, n = h rstd:  dh = rstd (a - n mean(a n)) + dh_in  (x's and residual's gradient both)
+ *   dweight = sum over rows of dy n
+ * rounded to dtype; sums in fp32 in an order that the sizes alone fix. dh may be
+ * dy, h or dh_in itself, else overlaps no input. R == 0 sets dweight to 0.
+ * workspace: moe_rmsnorm_backward_workspace_size() bytes, 256-byte aligned. */
+int moe_rmsnorm_backward_workspace_size(int64_t R, int64_t d, moe_dtype_t dtype, size_t* bytes);
+int moe_rmsnorm_backward(const void* dy, const void* h, const void* weight, const float* rstd, const void* dh_in,
+                         int64_t R, int64_t d, moe_dtype_t dtype, void* dh, void* dweight, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* Stages of moe_layer_forward (and of moe_layer_forward_replicated, whose
  * ROUTE stage also ranks each expert's copies and deals them to instances),
  * in launch order. */

@@ -32,7 +32,9 @@ EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_layer_forward", "moe_backw
            "moe_permute_workspace_size", "moe_permute", "moe_permute_static", "moe_grouped_gemm_workspace_size",
            "moe_grouped_gemm", "moe_combine", "moe_q4_size", "moe_q4_quantize", "moe_q4_dequantize",
            "moe_q4_matvec_workspace_size", "moe_q4_matvec", "moe_few_workspace_size", "moe_layer_forward_few",
-           "moe_layer_forward_few_q4", "moe_gate", "moe_gate_backward", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
+           "moe_layer_forward_few_q4", "moe_gate", "moe_gate_backward", "moe_mx8_size",
+           "moe_mx8_quantize", "moe_mx8_dequantize", "moe_rmsnorm", "moe_rmsnorm_backward_workspace_size",
+           "moe_rmsnorm_backward", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
 STAGES = ("router", "route", "slots", "scatter", "gate_up", "down", "combine")
 
 
@@ -58,6 +60,10 @@ class moe_q4_t(ctypes.Structure):
 class moe_gate_t(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
                 ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class moe_mx8_t(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -100,6 +106,12 @@ _SIGS = {
                                  ctypes.c_int, _P, ctypes.POINTER(moe_stats_t), _P, _SZ, _P],
     "moe_gate": [_P, _P, ctypes.POINTER(moe_gate_t), _I64, _I32, _I32, _P, _P, _P],
     "moe_gate_backward": [_P, _P, _P, _P, ctypes.POINTER(moe_gate_t), _I64, _I32, _I32, _P, _P],
+    "moe_mx8_size": [_I32, _I64, _I64, _P, _P],
+    "moe_mx8_quantize": [_P, _I32, _I64, _I64, ctypes.c_int, ctypes.POINTER(moe_mx8_t), _P],
+    "moe_mx8_dequantize": [ctypes.POINTER(moe_mx8_t), _I32, _I64, _I64, ctypes.c_int, _P, _P],
+    "moe_rmsnorm": [_P, _P, _P, _F32, _I64, _I64, ctypes.c_int, _P, _P, ctypes.POINTER(moe_mx8_t), _P, _P],
+    "moe_rmsnorm_backward_workspace_size": [_I64, _I64, ctypes.c_int, _P],
+    "moe_rmsnorm_backward": [_P, _P, _P, _P, _P, _I64, _I64, ctypes.c_int, _P, _P, _P, _SZ, _P],
     "moe_set_stage_events": [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int],
     "moe_stage_ran": [ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
 }
@@ -391,6 +403,47 @@ def moe_gate_backward(logits, topk_idx, d_topk_w, d_scores, gate, T, E, k, dlogi
                                    _ptr(dlogits), _stream(stream)), "moe_gate_backward")
 
 
+def moe_mx8_size(E, N, K) -> tuple[int, int]:
+    """Bytes of an 8-bit matrix stack's codes and scales."""
+    a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().moe_mx8_size(E, N, K, ctypes.byref(a), ctypes.byref(b)), "moe_mx8_size")
+    return a.value, b.value
+
+
+def _mx8(q) -> "ctypes.POINTER(moe_mx8_t) | None":
+    """q: None, an Mx8, or (codes, scale)."""
+    if q is None:
+        return None
+    codes, scale = (q._codes, q._scale) if isinstance(q, Mx8) else q
+    return ctypes.pointer(moe_mx8_t(_ptr(codes), _ptr(scale)))
+
+
+def moe_mx8_quantize(W, E, N, K, dtype, q, stream=None):
+    _check(lib().moe_mx8_quantize(_ptr(W), E, N, K, _dtype(dtype), _mx8(q), _stream(stream)), "moe_mx8_quantize")
+
+
+def moe_mx8_dequantize(q, E, N, K, dtype, W, stream=None):
+    _check(lib().moe_mx8_dequantize(_mx8(q), E, N, K, _dtype(dtype), _ptr(W), _stream(stream)), "moe_mx8_dequantize")
+
+
+def moe_rmsnorm(x, residual, weight, eps, R, d, dtype, h_out, y, y8, rstd, stream=None):
+    _check(lib().moe_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), eps, R, d, _dtype(dtype), _ptr(h_out), _ptr(y),
+                             _mx8(y8), _ptr(rstd), _stream(stream)), "moe_rmsnorm")
+
+
+def moe_rmsnorm_backward_workspace_size(R, d, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_rmsnorm_backward_workspace_size(R, d, _dtype(dtype), ctypes.byref(n)),
+           "moe_rmsnorm_backward_workspace_size")
+    return n.value
+
+
+def moe_rmsnorm_backward(dy, h, weight, rstd, dh_in, R, d, dtype, dh, dweight, workspace, workspace_bytes, stream=None):
+    _check(lib().moe_rmsnorm_backward(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh_in), R, d, _dtype(dtype),
+                                      _ptr(dh), _ptr(dweight), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "moe_rmsnorm_backward")
+
+
 def moe_set_stage_events(events):
     """events: None (off) or 2 * len(STAGES) raw hipEvent_t handles (ints)."""
     if events is None:
@@ -624,8 +677,10 @@ class _On:
         return t
 
     def lent(self, t):
-        if self.other is not None:
-            for v in (t._codes, t._scale, t._zero) if isinstance(t, Q4Weights) else (t,):
+        if self.other is not None and t is not None:
+            of = ((t._codes, t._scale, t._zero) if isinstance(t, Q4Weights) else
+                  (t._codes, t._scale) if isinstance(t, Mx8) else (t,))
+            for v in of:
                 if v is not None:
                     v.record_stream(self.other)
         return t
@@ -835,8 +890,7 @@ def gate(logits, k, score="softmax", bias=None, groups=1, top_groups=0, group_be
                 on.lent(t)
         if on.other is not None:
             for t in (logits, bias):
-                if t is not None:
-                    on.lent(t)
+                on.lent(t)
         t = res._bound[1]
         moe_gate(logits, bias, rule, T, E, k, t["topk_idx"], t["topk_w"], on.stream)
     return res
@@ -869,7 +923,150 @@ def gate_backward(logits, topk_idx, d_topk_w, score="softmax", renormalize=True,
             on.lent(out)
         if on.other is not None:
             for t in (logits, topk_idx, d_topk_w, d_scores):
-                if t is not None:
-                    on.lent(t)
+                on.lent(t)
         moe_gate_backward(logits, topk_idx, d_topk_w, d_scores, rule, T, E, k, out, on.stream)
     return out
+
+
+# ---------------------------------------------------- 8-bit matrices, the norm
+
+class Mx8:
+    """8-bit matrices [E, N, K] or rows [R, K] (the layout of moe_mx8_t in moe.h):
+    codes float8_e4m3fn of that shape, scale uint8 [E, ceil(K/128), N, 4] or
+    [ceil(K/128), R, 4]. Made by quantize_mx8() or rmsnorm(), or from tensors laid
+    out so, which are kept and read in place; codes and scale give views of them,
+    whose values may be changed. Can be copied (copy.deepcopy) and pickled."""
+
+    def __init__(self, codes, scale):
+        import torch
+        if codes.dim() not in (2, 3):
+            raise ValueError(f"codes: need [E, N, K] or [R, K], got {tuple(codes.shape)}")
+        lead, (N, K) = tuple(codes.shape[:-2]), codes.shape[-2:]
+        moe_mx8_size(*lead or (1,), N, K)   # checks the sizes
+        _require(codes, "codes", torch.float8_e4m3fn, tuple(codes.shape))
+        _require(scale, "scale", torch.uint8, (*lead, -(-K // 128), N, 4))
+        if scale.device != codes.device:
+            raise ValueError("codes and scale must be on one device")
+        self._set(codes.detach(), scale.detach())
+
+    def _set(self, codes, scale):
+        self._codes, self._scale, self._shape = codes, scale, tuple(codes.shape)
+
+    @classmethod
+    def _empty(cls, on, shape):
+        """One of new memory; the sizes are checked where it is filled."""
+        import torch
+        q = cls.__new__(cls)
+        q._set(on.empty(shape, torch.float8_e4m3fn), on.empty((*shape[:-2], -(-shape[-1] // 128), shape[-2], 4), torch.uint8))
+        return q
+
+    codes = property(lambda self: self._codes.detach())
+    scale = property(lambda self: self._scale.detach())
+    shape = property(lambda self: self._shape)
+
+    @property
+    def device(self):
+        return self._codes.device
+
+
+def quantize_mx8(W, stream=None):
+    """W [E, N, K] or [R, K] (bf16 or fp32; K a multiple of 16) in 8 bits: an Mx8.
+    Runs on torch's current stream unless one is given."""
+    if W.dim() not in (2, 3):
+        raise ValueError(f"W: need [E, N, K] or [R, K], got {tuple(W.shape)}")
+    shape = tuple(W.shape)
+    _require(W, "W", W.dtype, shape)
+    dt = _dtype(W.dtype)
+    E, N, K = shape if len(shape) == 3 else (1, *shape)
+    moe_mx8_size(E, N, K)   # checks the sizes
+    with _On(W.device, stream) as on:
+        q = Mx8._empty(on, shape)
+        moe_mx8_quantize(on.lent(W), E, N, K, dt, q, on.stream)
+    return q
+
+
+def dequantize_mx8(q, dtype, stream=None):
+    """The values that an Mx8 stands for, rounded to dtype, in its shape."""
+    import torch
+    dt = _dtype(dtype)
+    E, N, K = q.shape if len(q.shape) == 3 else (1, *q.shape)
+    with _On(q.device, stream) as on:
+        W = on.empty(q.shape, torch.bfloat16 if dt == MOE_DTYPE_BF16 else torch.float32)
+        moe_mx8_dequantize(on.lent(q), E, N, K, dt, W, on.stream)
+    return W
+
+
+def rmsnorm(x, weight, eps=1e-6, residual=None, want_y=True, mx8=False, out=None, stream=None):
+    """The norm in front of the layer for rows x [R, d] (bf16 or fp32):
+    h = x + residual (x itself without one), y = h / sqrt(mean(h^2) + eps) weight.
+
+    Returns a dict h (x without a residual), y (unless want_y is false), y8 (an
+    Mx8, with mx8) and rstd fp32 [R], which rmsnorm_backward takes. out: the result
+    of an earlier call with the same sizes and outputs, whose tensors this call
+    writes. Runs on torch's current stream unless one is given."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x: need [R, d], got {tuple(x.shape)}")
+    R, d = x.shape
+    dt, dev = x.dtype, x.device
+    dtype = _dtype(dt)
+    _require(x, "x", dt, (R, d))
+    _require(weight, "weight", dt, (d,))
+    if residual is not None:
+        _require(residual, "residual", dt, (R, d))
+    if mx8:
+        moe_mx8_size(1, R, d)   # checks the sizes
+    _same_device(dev, "weight residual", weight, residual)
+    key = ("rmsnorm", R, d, dt, dev, residual is not None, bool(want_y), bool(mx8))
+    with _On(dev, stream) as on:
+        if out is None:
+            res = Result.of(key, h=on.empty((R, d), dt) if residual is not None else None,
+                            y=on.empty((R, d), dt) if want_y else None, y8=Mx8._empty(on, (R, d)) if mx8 else None,
+                            rstd=on.empty((R,), torch.float32))
+        else:
+            res = _lent_result(out, key, "rmsnorm")
+            for t in res._bound[1].values():
+                on.lent(t)
+        if on.other is not None:
+            for t in (x, weight, residual):
+                on.lent(t)
+        t = res._bound[1]
+        moe_rmsnorm(x, residual, weight, eps, R, d, dtype, t["h"], t["y"], t["y8"], t["rstd"], on.stream)
+    if residual is None:
+        res["h"] = x
+    return res
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dh=None, out=None, stream=None):
+    """Gradient of rmsnorm(): of dy [R, d] for y and, if given, dh [R, d] that
+    arrives at h otherwise. Returns a dict dh (the gradient of x and of residual
+    both), dweight, workspace. out: the result of an earlier call with the same
+    sizes, whose tensors this call writes."""
+    import torch
+    if dy.dim() != 2:
+        raise ValueError(f"dy: need [R, d], got {tuple(dy.shape)}")
+    R, d = dy.shape
+    dt, dev = dy.dtype, dy.device
+    dtype = _dtype(dt)
+    for t, n, s in ((dy, "dy", (R, d)), (h, "h", (R, d)), (weight, "weight", (d,)), (dh, "dh", (R, d))):
+        if t is not None:
+            _require(t, n, dt, s)
+    _require(rstd, "rstd", torch.float32, (R,))
+    _same_device(dev, "h weight rstd dh", h, weight, rstd, dh)
+    key = ("rmsnorm_backward", R, d, dt, dev)
+    with _On(dev, stream) as on:
+        if out is None:
+            nbytes = moe_rmsnorm_backward_workspace_size(R, d, dtype)
+            res = Result.of(key, dh=on.empty((R, d), dt), dweight=on.empty((d,), dt),
+                            workspace=on.empty((max(nbytes, 1),), torch.uint8))
+        else:
+            res = _lent_result(out, key, "rmsnorm_backward")
+            for t in res._bound[1].values():
+                on.lent(t)
+        if on.other is not None:
+            for t in (dy, h, weight, rstd, dh):
+                on.lent(t)
+        t = res._bound[1]
+        moe_rmsnorm_backward(dy, h, weight, rstd, dh, R, d, dtype, t["dh"], t["dweight"], t["workspace"],
+                             t["workspace"].numel(), on.stream)
+    return res

@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libmoe_hip.so")
 ARCH = "gfx950"
 
 SOURCES = ["moe_api.hip", "router.hip", "permute.hip", "grouped_gemm.hip", "combine.hip", "backward.hip",
-           "few.hip", "q4.hip", "gate.hip"]
+           "few.hip", "q4.hip", "gate.hip", "mx8.hip",
+           "norm.hip"]
 
 
 def hipcc() -> str:

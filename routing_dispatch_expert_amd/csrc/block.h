@@ -21,4 +21,22 @@ hipError_t launch_gate(const float* logits, const float* bias, const GateRule& g
 hipError_t launch_gate_backward(const float* logits, const int32_t* idx, const float* dw, const float* dscores,
                                 const GateRule& g, int64_t T, int E, int k, float* dlogits, hipStream_t s);
 
+// ---- 8-bit matrices (mx8.hip): codes [E][N][K], scale dwords [E][ceil(K/128)][N] ----
+int64_t mx8_units(int64_t E, int64_t N, int64_t K, bool bf16);  // waves of a launch
+hipError_t launch_mx8_quantize(const void* W, bool bf16, int64_t E, int64_t N, int64_t K, uint8_t* codes, uint32_t* scale,
+                               hipStream_t s);
+hipError_t launch_mx8_dequantize(const uint8_t* codes, const uint32_t* scale, int64_t E, int64_t N, int64_t K, bool bf16,
+                                 void* W, hipStream_t s);
+
+// ---- the norm (norm.hip) ----
+// residual, h, y, codes (with scale), rstd and dres may be NULL; h is written with a residual only.
+int64_t rmsnorm_max_width(bool bf16);
+hipError_t launch_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int64_t R, int64_t d,
+                          bool bf16, void* h, void* y, uint8_t* codes, uint32_t* scale, float* rstd, hipStream_t s);
+// parts: fp32 [rmsnorm_shares()][d].
+int64_t rmsnorm_shares(int64_t R, int64_t d, bool bf16);
+hipError_t launch_rmsnorm_backward(const void* dy, const void* h, const void* weight, const float* rstd,
+                                   const void* dres, int64_t R, int64_t d, bool bf16, void* dh, void* dweight,
+                                   float* parts, hipStream_t s);
+
 }  // namespace moe

@@ -1356,3 +1356,144 @@ int moe_gate_backward(const float* logits, const int32_t* topk_idx, const float*
 }
 
 }  // extern "C"
+
+namespace {
+
+int check_mx8_shape(int64_t E, int64_t N, int64_t K) {
+  if (E < 1 || N < 0 || K < 1) return fail(MOE_ERR_INVALID_ARG, "need E >= 1, N >= 0, K >= 1");
+  if (K % 16) return fail(MOE_ERR_UNSUPPORTED, "K=%lld must be a multiple of 16", static_cast<long long>(K));
+  // a launch has fewer than 2^32 threads; 8 rows of a 128-column step take 64 at most
+  const int64_t lim = int64_t{1} << 31, most = (int64_t{1} << 26) - 5;
+  if (N >= lim || K >= lim || moe::ceil_div(N, 8) * moe::ceil_div(K, 128) > most / E)
+    return fail(MOE_ERR_UNSUPPORTED, "E ceil(N/8) ceil(K/128) must stay below 2^26 - 4");
+  return MOE_OK;
+}
+
+int check_mx8(const moe_mx8_t* q, const char* name) {
+  if (!q) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!q->codes || !q->scale) return fail(MOE_ERR_INVALID_ARG, "%s: codes or scale is NULL", name);
+  if (!aligned16(q->codes) || !aligned16(q->scale))
+    return fail(MOE_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  return MOE_OK;
+}
+
+size_t mx8_scale_bytes(int64_t E, int64_t N, int64_t K) {
+  return static_cast<size_t>(E) * moe::ceil_div(K, 128) * N * 4;
+}
+
+uint8_t* mx8_codes(const moe_mx8_t* q) { return static_cast<uint8_t*>(q->codes); }
+uint32_t* mx8_scale(const moe_mx8_t* q) { return static_cast<uint32_t*>(q->scale); }
+
+int check_norm_shape(int64_t R, int64_t d, int dtype) {
+  if (!valid_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (R < 0 || d < 1) return fail(MOE_ERR_INVALID_ARG, "need R >= 0, d >= 1");
+  const auto dt = static_cast<moe_dtype_t>(dtype);
+  const int st = check_width(d, dt, "d");
+  if (st != MOE_OK) return st;
+  const bool bf16 = dt == MOE_DTYPE_BF16;
+  if (d > moe::rmsnorm_max_width(bf16))
+    return fail(MOE_ERR_UNSUPPORTED, "d=%lld > %lld", static_cast<long long>(d),
+                static_cast<long long>(moe::rmsnorm_max_width(bf16)));
+  // a launch has fewer than 2^32 threads
+  const int64_t words = d / (bf16 ? 8 : 4);
+  if (R >= (words <= 256 ? int64_t{1} << 26 : words <= 2048 ? int64_t{1} << 24 : int64_t{1} << 22) - 4)
+    return fail(MOE_ERR_UNSUPPORTED, "R=%lld rows of this width are too many", static_cast<long long>(R));
+  return MOE_OK;
+}
+
+// Whether out overlaps in other than by being the same array.
+bool overlaps_askew(const void* out, const void* in, size_t n) { return out != in && overlaps(out, n, in, n); }
+
+}  // namespace
+
+extern "C" {
+
+int moe_mx8_size(int32_t E, int64_t N, int64_t K, size_t* codes_bytes, size_t* scale_bytes) {
+  const int st = check_mx8_shape(E, N, K);
+  if (st != MOE_OK) return st;
+  if (codes_bytes) *codes_bytes = static_cast<size_t>(E) * N * K;
+  if (scale_bytes) *scale_bytes = mx8_scale_bytes(E, N, K);
+  return MOE_OK;
+}
+
+int moe_mx8_quantize(const void* W, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, const moe_mx8_t* q,
+                     void* stream) {
+  if (!valid_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  int st = check_mx8_shape(E, N, K);
+  if (st != MOE_OK) return st;
+  if (N == 0) return MOE_OK;
+  if ((st = check_mx8(q, "q")) != MOE_OK) return st;
+  if (!W || !aligned16(W)) return fail(MOE_ERR_INVALID_ARG, "W is NULL or not 16-byte aligned");
+  MOE_HIP_TRY(moe::launch_mx8_quantize(W, dtype == MOE_DTYPE_BF16, E, N, K, mx8_codes(q), mx8_scale(q),
+                                       static_cast<hipStream_t>(stream)),
+              "quantize");
+  return MOE_OK;
+}
+
+int moe_mx8_dequantize(const moe_mx8_t* q, int32_t E, int64_t N, int64_t K, moe_dtype_t dtype, void* W, void* stream) {
+  if (!valid_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  int st = check_mx8_shape(E, N, K);
+  if (st != MOE_OK) return st;
+  if (N == 0) return MOE_OK;
+  if ((st = check_mx8(q, "q")) != MOE_OK) return st;
+  if (!W || !aligned16(W)) return fail(MOE_ERR_INVALID_ARG, "W is NULL or not 16-byte aligned");
+  MOE_HIP_TRY(moe::launch_mx8_dequantize(mx8_codes(q), mx8_scale(q), E, N, K, dtype == MOE_DTYPE_BF16, W,
+                                         static_cast<hipStream_t>(stream)),
+              "dequantize");
+  return MOE_OK;
+}
+
+int moe_rmsnorm(const void* x, const void* residual, const void* weight, float eps, int64_t R, int64_t d,
+                moe_dtype_t dtype, void* h_out, void* y, const moe_mx8_t* y8, float* rstd, void* stream) {
+  int st = check_norm_shape(R, d, dtype);
+  if (st != MOE_OK) return st;
+  if (!std::isfinite(eps) || eps < 0.f) return fail(MOE_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (y8 && (st = check_mx8_shape(1, R, d)) != MOE_OK) return st;
+  if (h_out && !residual) return fail(MOE_ERR_INVALID_ARG, "h_out without a residual");
+  if (R == 0) return MOE_OK;
+  if (!x || !weight) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (y8 && (st = check_mx8(y8, "y8")) != MOE_OK) return st;
+  for (const void* p : {x, residual, weight, static_cast<const void*>(h_out), static_cast<const void*>(y)})
+    if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "x, residual, weight, h_out and y must be 16-byte aligned");
+  const size_t n = static_cast<size_t>(R) * d * elem_bytes(dtype);
+  if (h_out && (overlaps_askew(h_out, x, n) || overlaps_askew(h_out, residual, n)))
+    return fail(MOE_ERR_INVALID_ARG, "h_out overlaps an input that it is not");
+  if (y && (overlaps(y, n, x, n) || (residual && overlaps(y, n, residual, n)) || (h_out && overlaps(y, n, h_out, n))))
+    return fail(MOE_ERR_INVALID_ARG, "y overlaps x, residual or h_out");
+  MOE_HIP_TRY(moe::launch_rmsnorm(x, residual, weight, eps, R, d, dtype == MOE_DTYPE_BF16, h_out, y,
+                                  y8 ? mx8_codes(y8) : nullptr, y8 ? mx8_scale(y8) : nullptr, rstd,
+                                  static_cast<hipStream_t>(stream)),
+              "rmsnorm");
+  return MOE_OK;
+}
+
+int moe_rmsnorm_backward_workspace_size(int64_t R, int64_t d, moe_dtype_t dtype, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  const int st = check_norm_shape(R, d, dtype);
+  if (st != MOE_OK) return st;
+  *bytes = align_up(static_cast<size_t>(moe::rmsnorm_shares(R, d, dtype == MOE_DTYPE_BF16)) * d * sizeof(float));
+  return MOE_OK;
+}
+
+int moe_rmsnorm_backward(const void* dy, const void* h, const void* weight, const float* rstd, const void* dh_in,
+                         int64_t R, int64_t d, moe_dtype_t dtype, void* dh, void* dweight, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  size_t need;
+  const int st = moe_rmsnorm_backward_workspace_size(R, d, dtype, &need);
+  if (st != MOE_OK) return st;
+  if (!weight || !dweight || (R && (!dy || !h || !rstd || !dh)))
+    return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  for (const void* p : {dy, h, weight, dh_in, static_cast<const void*>(dh)})
+    if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "dy, h, weight, dh_in and dh must be 16-byte aligned");
+  const size_t n = static_cast<size_t>(R) * d * elem_bytes(dtype);
+  if (overlaps_askew(dh, dy, n) || overlaps_askew(dh, h, n) || (dh_in && overlaps_askew(dh, dh_in, n)))
+    return fail(MOE_ERR_INVALID_ARG, "dh overlaps an input that it is not");
+  if (need && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % kAlign))
+    return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned", need);
+  MOE_HIP_TRY(moe::launch_rmsnorm_backward(dy, h, weight, rstd, dh_in, R, d, dtype == MOE_DTYPE_BF16, dh, dweight,
+                                           static_cast<float*>(workspace), static_cast<hipStream_t>(stream)),
+              "rmsnorm backward");
+  return MOE_OK;
+}
+
+}  // extern "C"
