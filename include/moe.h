@@ -477,6 +477,31 @@ int moe_rmsnorm_backward(const void* dy, const void* h, const void* weight, cons
                          int64_t R, int64_t d, moe_dtype_t dtype, void* dh, void* dweight, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/* ---- The experts with 8-bit rows and weights ----
+ *
+ * From a given routing (moe_gate's, moe_route's or any other), rows x [T, d] and
+ * W_gate, W_up [E, d_ff, d], W_down [E, d, d_ff] in 8 bits:
+ *   C = moe_capacity(T, E, k, cf); slot = stable token-order rank of each copy among its expert's, dropped (-1) if >= C
+ *   h = silu(x W_gate^T) * (x W_up^T), put into 8 bits as moe_mx8_quantize does it
+ *   y = h W_down^T, rounded to dtype
+ *   out[t] = residual[t] + sum_j [slot >= 0] topk_w[t,j] y[t,j]      (j ascending, in fp32)
+ * residual, out [T, d]: dtype, 16-byte aligned (out may be residual itself); a token
+ * without a kept copy passes bit for bit. A topk_idx entry outside [0, E) is
+ * dropped and counted nowhere; an expert that a token names twice counts twice.
+ * Products are exact and summed on the matrix cores into fp32 (of one
+ * instruction's products those some 2^13 below its largest are cut off). Of stats,
+ * slot, routed_count and kept_count are written; the others must be NULL.
+ * d and d_ff are multiples of 16; limits (else MOE_ERR_UNSUPPORTED) as for the
+ * layer, and T * max(d, d_ff) and d * d_ff below 2^31, T * ceil(d / 1024) and
+ * min(E, T k) * ceil(max(d, d_ff) / 32) below 2^22. workspace:
+ * moe_experts_mx8_workspace_size() bytes, 256-byte aligned. */
+int moe_experts_mx8_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf,
+                                   moe_dtype_t dtype, size_t* bytes);
+int moe_experts_mx8(const moe_mx8_t* x, const void* residual, const int32_t* topk_idx, const float* topk_w,
+                    const moe_mx8_t* W_gate, const moe_mx8_t* W_up, const moe_mx8_t* W_down, int64_t T, int64_t d,
+                    int64_t d_ff, int32_t E, int32_t k, float cf, moe_dtype_t dtype, void* out, moe_stats_t* stats,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Stages of moe_layer_forward (and of moe_layer_forward_replicated, whose
  * ROUTE stage also ranks each expert's copies and deals them to instances),
  * in launch order. */

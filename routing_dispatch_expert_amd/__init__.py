@@ -34,7 +34,7 @@ EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_layer_forward", "moe_backw
            "moe_q4_matvec_workspace_size", "moe_q4_matvec", "moe_few_workspace_size", "moe_layer_forward_few",
            "moe_layer_forward_few_q4", "moe_gate", "moe_gate_backward", "moe_mx8_size",
            "moe_mx8_quantize", "moe_mx8_dequantize", "moe_rmsnorm", "moe_rmsnorm_backward_workspace_size",
-           "moe_rmsnorm_backward", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
+           "moe_rmsnorm_backward", "moe_experts_mx8_workspace_size", "moe_experts_mx8", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
 STAGES = ("router", "route", "slots", "scatter", "gate_up", "down", "combine")
 
 
@@ -112,6 +112,10 @@ _SIGS = {
     "moe_rmsnorm": [_P, _P, _P, _F32, _I64, _I64, ctypes.c_int, _P, _P, ctypes.POINTER(moe_mx8_t), _P, _P],
     "moe_rmsnorm_backward_workspace_size": [_I64, _I64, ctypes.c_int, _P],
     "moe_rmsnorm_backward": [_P, _P, _P, _P, _P, _I64, _I64, ctypes.c_int, _P, _P, _P, _SZ, _P],
+    "moe_experts_mx8_workspace_size": [_I64, _I64, _I64, _I32, _I32, _F32, ctypes.c_int, _P],
+    "moe_experts_mx8": [ctypes.POINTER(moe_mx8_t), _P, _P, _P, ctypes.POINTER(moe_mx8_t), ctypes.POINTER(moe_mx8_t),
+                        ctypes.POINTER(moe_mx8_t), _I64, _I64, _I64, _I32, _I32, _F32, ctypes.c_int, _P,
+                        ctypes.POINTER(moe_stats_t), _P, _SZ, _P],
     "moe_set_stage_events": [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int],
     "moe_stage_ran": [ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
 }
@@ -442,6 +446,21 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dh_in, R, d, dtype, dh, dweight, w
     _check(lib().moe_rmsnorm_backward(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh_in), R, d, _dtype(dtype),
                                       _ptr(dh), _ptr(dweight), _ptr(workspace), workspace_bytes, _stream(stream)),
            "moe_rmsnorm_backward")
+
+
+def moe_experts_mx8_workspace_size(T, d, d_ff, E, k, cf, dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_experts_mx8_workspace_size(T, d, d_ff, E, k, cf, _dtype(dtype), ctypes.byref(n)),
+           "moe_experts_mx8_workspace_size")
+    return n.value
+
+
+def moe_experts_mx8(x, residual, topk_idx, topk_w, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, dtype, out, stats,
+                    workspace, workspace_bytes, stream=None):
+    """x, W_gate, W_up, W_down: as for _mx8 (an Mx8 each)."""
+    _check(lib().moe_experts_mx8(_mx8(x), _ptr(residual), _ptr(topk_idx), _ptr(topk_w), _mx8(W_gate), _mx8(W_up),
+                                 _mx8(W_down), T, d, d_ff, E, k, cf, _dtype(dtype), _ptr(out), _stats(stats),
+                                 _ptr(workspace), workspace_bytes, _stream(stream)), "moe_experts_mx8")
 
 
 def moe_set_stage_events(events):
@@ -1069,4 +1088,55 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, out=None, stream=None):
         t = res._bound[1]
         moe_rmsnorm_backward(dy, h, weight, rstd, dh, R, d, dtype, t["dh"], t["dweight"], t["workspace"],
                              t["workspace"].numel(), on.stream)
+    return res
+
+
+def experts_mx8(x, topk_idx, topk_w, W_gate, W_up, W_down, residual, cf, out=None, stream=None):
+    """The experts from a given routing, with 8-bit rows x [T, d] and weights W_gate,
+    W_up [E, d_ff, d] and W_down [E, d, d_ff] (an Mx8 each), added to residual
+    [T, d] (bf16 or fp32): topk_idx int32 and topk_w fp32 [T, k] as gate() or the
+    layer's router return them; cf = E / k drops nothing. Returns a dict out [T, d],
+    slot [T, k], routed_count, kept_count [E], workspace. out: the result of an
+    earlier call with the same sizes, whose tensors this call writes. Runs on
+    torch's current stream unless one is given."""
+    import torch
+    for q, n, dims in ((x, "x", 2), (W_gate, "W_gate", 3), (W_up, "W_up", 3), (W_down, "W_down", 3)):
+        if not isinstance(q, Mx8) or len(q.shape) != dims:
+            raise ValueError(f"{n}: need an Mx8 of {dims} dimensions")
+    T, d = x.shape
+    E, d_ff = W_gate.shape[:2]
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx: need [T, k], got {tuple(topk_idx.shape)}")
+    k = topk_idx.shape[1]
+    for q, n, s in ((W_gate, "W_gate", (E, d_ff, d)), (W_up, "W_up", (E, d_ff, d)), (W_down, "W_down", (E, d, d_ff))):
+        if q.shape != s:
+            raise ValueError(f"{n}: need 8-bit weights of shape {s}, got {q.shape}")
+    dt, dev = residual.dtype, x.device
+    dtype = _dtype(dt)
+    _require(residual, "residual", dt, (T, d))
+    _require(topk_idx, "topk_idx", torch.int32, (T, k))
+    _require(topk_w, "topk_w", torch.float32, (T, k))
+    _same_device(dev, "topk_idx topk_w W_gate W_up W_down residual", topk_idx, topk_w, W_gate, W_up, W_down, residual)
+    key = ("experts_mx8", T, d, d_ff, E, k, cf, dt, dev)
+    with _On(dev, stream) as on:
+        if out is None:
+            nbytes = moe_experts_mx8_workspace_size(T, d, d_ff, E, k, cf, dtype)
+            i32 = torch.int32
+            res = Result.of(key, out=on.empty((T, d), dt), slot=on.empty((T, k), i32), routed_count=on.empty((E,), i32),
+                            kept_count=on.empty((E,), i32), workspace=on.empty((max(nbytes, 1),), torch.uint8))
+            if T == 0:   # nothing will be launched: the counts of no tokens
+                with torch.cuda.stream(on.stream):
+                    for name in ("routed_count", "kept_count"):
+                        res[name].zero_()
+        else:
+            res = _lent_result(out, key, "experts_mx8")
+            for t in res._bound[1].values():
+                on.lent(t)
+        if on.other is not None:
+            for t in (x, topk_idx, topk_w, W_gate, W_up, W_down, residual):
+                on.lent(t)
+        t = res._bound[1]
+        stats = {n: t[n] for n in ("slot", "routed_count", "kept_count")}
+        moe_experts_mx8(x, residual, topk_idx, topk_w, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, dtype, t["out"], stats,
+                        t["workspace"], t["workspace"].numel(), on.stream)
     return res

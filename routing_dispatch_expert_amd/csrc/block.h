@@ -39,4 +39,32 @@ hipError_t launch_rmsnorm_backward(const void* dy, const void* h, const void* we
                                    const void* dres, int64_t R, int64_t d, bool bf16, void* dh, void* dweight,
                                    float* parts, hipStream_t s);
 
+// ---- the experts with 8-bit rows and weights (mx8_experts.hip) ----
+struct Mx8Ptr {
+  uint8_t* codes;
+  uint32_t* scale;
+};
+// The kept copies by expert, in token order: row off[e] + i is copy (flat t k + j)
+// copy[off[e] + i]; act [n_act]: the experts that have rows; tile: prefix of the
+// experts' row tiles.
+struct ExpertLists {
+  int32_t *off, *tile, *n_act, *act, *copy;  // [E + 1], [E + 1], [1], [min(E, T k)], [T k]
+};
+struct ExpertsMx8 {
+  Mx8Ptr x, gate, up, down;
+  const void* residual;
+  const int32_t* idx;
+  const float* w;
+  int64_t T, d, f, C;
+  int E, k;
+  bool bf16;       // residual, y and out
+  void* out;
+  int32_t *slot, *routed, *kept;  // routed and kept may be NULL
+  // workspace
+  ExpertLists ls;
+  Mx8Ptr h;        // rows [T k][f]
+  void* y;         // [T k][d]
+};
+hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s);
+
 }  // namespace moe

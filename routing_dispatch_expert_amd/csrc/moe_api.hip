@@ -1497,3 +1497,113 @@ int moe_rmsnorm_backward(const void* dy, const void* h, const void* weight, cons
 }
 
 }  // extern "C"
+
+namespace {
+
+struct ExpertsPlan {
+  moe::ExpertLists ls;
+  moe::Mx8Ptr h;
+  int32_t* slot;
+  void* y;
+  size_t bytes;
+};
+
+ExpertsPlan plan_experts_mx8(void* ws, int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, int eb) {
+  Carver c(ws);
+  ExpertsPlan p;
+  const size_t n = static_cast<size_t>(T) * k;
+  p.ls.off = c.take<int32_t>(static_cast<size_t>(E) + 1);
+  p.ls.tile = c.take<int32_t>(static_cast<size_t>(E) + 1);
+  p.ls.n_act = c.take<int32_t>(1);
+  p.ls.act = c.take<int32_t>(std::min<size_t>(E, n));
+  p.ls.copy = c.take<int32_t>(n);
+  p.slot = c.take<int32_t>(n);
+  p.h.codes = c.take<uint8_t>(n * d_ff);
+  p.h.scale = c.take<uint32_t>(mx8_scale_bytes(1, n, d_ff) / 4);
+  p.y = c.take<char>(n * d * eb);
+  p.bytes = align_up(c.off);
+  return p;
+}
+
+int check_experts_mx8(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int dtype, int64_t* C) {
+  int st = check_layer_shape(T, d, d_ff, E, k, cf, 1, dtype, C);
+  if (st != MOE_OK) return st;
+  if (d % 16 || d_ff % 16) return fail(MOE_ERR_UNSUPPORTED, "d and d_ff must be multiples of 16");
+  const int64_t lim = int64_t{1} << 31, wide = std::max(d, d_ff);
+  if (d * d_ff >= lim || T >= lim / wide)
+    return fail(MOE_ERR_UNSUPPORTED, "d * d_ff and T * max(d, d_ff) must stay below 2^31");
+  // a launch has fewer than 2^32 threads
+  if (T * moe::ceil_div(d, 1024) >= (int64_t{1} << 22) ||
+      std::min<int64_t>(E, T * k) * moe::ceil_div(wide, 32) >= (int64_t{1} << 22))
+    return fail(MOE_ERR_UNSUPPORTED, "too many rows or weight tiles");
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_experts_mx8_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf,
+                                   moe_dtype_t dtype, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  int64_t C;
+  const int st = check_experts_mx8(T, d, d_ff, E, k, cf, dtype, &C);
+  if (st != MOE_OK) return st;
+  *bytes = plan_experts_mx8(nullptr, T, d, d_ff, E, k, elem_bytes(dtype)).bytes;
+  return MOE_OK;
+}
+
+int moe_experts_mx8(const moe_mx8_t* x, const void* residual, const int32_t* topk_idx, const float* topk_w,
+                    const moe_mx8_t* W_gate, const moe_mx8_t* W_up, const moe_mx8_t* W_down, int64_t T, int64_t d,
+                    int64_t d_ff, int32_t E, int32_t k, float cf, moe_dtype_t dtype, void* out, moe_stats_t* stats,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  int64_t C;
+  int st = check_experts_mx8(T, d, d_ff, E, k, cf, dtype, &C);
+  if (st != MOE_OK) return st;
+  if ((st = check_mx8(W_gate, "W_gate")) != MOE_OK || (st = check_mx8(W_up, "W_up")) != MOE_OK ||
+      (st = check_mx8(W_down, "W_down")) != MOE_OK)
+    return st;
+  moe_stats_t S;
+  std::memset(&S, 0, sizeof(S));
+  if (stats) S = *stats;
+  if (S.topk_idx || S.topk_w || S.src || S.send_count || S.totals || S.buckets || S.instance || S.g || S.u || S.h)
+    return fail(MOE_ERR_INVALID_ARG, "the 8-bit experts write slot, routed_count and kept_count alone");
+  if (T == 0) return MOE_OK;
+  if ((st = check_mx8(x, "x")) != MOE_OK) return st;
+  if (!residual || !topk_idx || !topk_w || !out) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(residual) || !aligned16(out))
+    return fail(MOE_ERR_INVALID_ARG, "residual and out must be 16-byte aligned");
+  const int eb = elem_bytes(dtype);
+  if (overlaps_askew(out, residual, static_cast<size_t>(T) * d * eb))
+    return fail(MOE_ERR_INVALID_ARG, "out overlaps residual");
+  const ExpertsPlan p = plan_experts_mx8(workspace, T, d, d_ff, E, k, eb);
+  if (!workspace || workspace_bytes < p.bytes || reinterpret_cast<uintptr_t>(workspace) % kAlign)
+    return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned", p.bytes);
+  moe::ExpertsMx8 L;
+  auto ptr = [](const moe_mx8_t* q) { return moe::Mx8Ptr{mx8_codes(q), mx8_scale(q)}; };
+  L.x = ptr(x);
+  L.gate = ptr(W_gate);
+  L.up = ptr(W_up);
+  L.down = ptr(W_down);
+  L.residual = residual;
+  L.idx = topk_idx;
+  L.w = topk_w;
+  L.T = T;
+  L.d = d;
+  L.f = d_ff;
+  L.C = C;
+  L.E = E;
+  L.k = k;
+  L.bf16 = dtype == MOE_DTYPE_BF16;
+  L.out = out;
+  L.slot = pick(S.slot, p.slot);
+  L.routed = S.routed_count;
+  L.kept = S.kept_count;
+  L.ls = p.ls;
+  L.h = p.h;
+  L.y = p.y;
+  MOE_HIP_TRY(moe::launch_experts_mx8(L, static_cast<hipStream_t>(stream)), "8-bit experts");
+  return MOE_OK;
+}
+
+}  // extern "C"

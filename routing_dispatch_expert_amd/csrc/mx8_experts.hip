@@ -1,0 +1,445 @@
+// The experts of the MoE layer with 8-bit rows and weights, from a given routing
+// (gfx950).
+//
+// Sources: "Expert Parallelism" (infra.bea.ai guide), section 1 - three weight
+// matrices per expert; "Expert Parallelism & All-to-All" (neelmishra.github.io),
+// "All-to-all: the distributed transpose" - gate-weighted sum into the residual.
+//
+//   h = mx8(silu(x Wg^T) * (x Wu^T));  y = h Wd^T, rounded to the output's type
+//   out[t] = residual[t] + sum_j [slot[t, j] >= 0] w[t, j] y[t, j]
+//
+// The products run on the scaled 8-bit matrix instructions: 128 (or 64) columns
+// an instruction, a scale for every 32. The weights are the A operand (an
+// accumulator's rows are output features), the tokens the columns of B: a lane
+// then has neighbouring features of one token, so that the 32 features that share
+// a scale of h lie in a few lanes and four codes make a word. Within one
+// instruction the matrix unit aligns the products to the largest one and drops
+// what lies some 2^13 below it; the accumulators are fp32: sums over 4096 Gaussian
+// products are off by 1.3e-5 of their size, far below the 2^-4 that the 8-bit
+// operands are rounded by.
+//
+// No bucket is built: lists of the kept copies by expert, in token order, say
+// which rows of x an expert reads and which rows of y it writes.
+#include "mx8.h"
+#include "q4.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+__device__ inline float silu(float g) { return g / (1.0f + expf(-g)); }
+
+// ---------------------------------------------------------------------------
+// Lists, by one work-group. Copies are taken 64 a wave and up to 16 waves at a
+// time; a copy's rank among its expert's is found by ballots over the expert's
+// bits within its wave, by the waves' counts in LDS before that, and by the
+// expert's running count: token order, nothing depends on arrival.
+// ---------------------------------------------------------------------------
+constexpr int kPlanCounts = 16384;  // counts of a round's waves: waves * E
+
+// Exclusive prefix sum over the block's 1024 values; the total goes to *total.
+__device__ inline int block_prefix(int v, int* sums, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(s, off, 64);
+    if (lane >= off) s += o;
+  }
+  __syncthreads();
+  if (lane == 63) sums[wave] = s;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (i < wave) before += sums[i];
+    all += sums[i];
+  }
+  *total = all;
+  return before + s - v;
+}
+
+__global__ __launch_bounds__(1024) void experts_plan_kernel(const int32_t* __restrict__ idx, int64_t T, int k, int E,
+                                                            int64_t C, int bt, int32_t* __restrict__ slot,
+                                                            int32_t* __restrict__ routed, int32_t* __restrict__ kept,
+                                                            ExpertLists ls) {
+  __shared__ int cc[kPlanCounts];
+  __shared__ int cnt[4096];
+  __shared__ int sums[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int W = min(16, kPlanCounts / E);  // at least 4
+  const int64_t n = T * k;
+  const int nbits = E > 1 ? 32 - __clz(E - 1) : 0;
+  const unsigned long long below = (1ull << lane) - 1ull;
+  for (int e = tid; e < E; e += 1024) cnt[e] = 0;
+  for (int64_t c0 = 0; c0 < n; c0 += 64 * W) {
+    for (int i = tid; i < W * E; i += 1024) cc[i] = 0;
+    __syncthreads();
+    const int64_t i = c0 + tid;
+    int e = -1, r = 0;
+    if (wave < W) {
+      if (i < n) e = idx[i];
+      if (e >= E) e = -1;
+      unsigned long long mask = __ballot(e >= 0);
+      for (int bit = 0; bit < nbits; ++bit) {
+        const bool set = (e >> bit) & 1;
+        const unsigned long long m = __ballot(e >= 0 && set);
+        mask &= set ? m : ~m;
+      }
+      if (e >= 0) {
+        r = __popcll(mask & below);
+        if (r == 0) cc[wave * E + e] = __popcll(mask);
+      }
+    }
+    __syncthreads();
+    for (int x = tid; x < E; x += 1024) {
+      int run = cnt[x];
+      for (int w = 0; w < W; ++w) {
+        const int c = cc[w * E + x];
+        cc[w * E + x] = run;
+        run += c;
+      }
+      cnt[x] = run;
+    }
+    __syncthreads();
+    if (wave < W && i < n) {
+      const int64_t rank = e >= 0 ? r + cc[wave * E + e] : C;
+      slot[i] = rank < C ? static_cast<int32_t>(rank) : -1;
+    }
+    __syncthreads();
+  }
+  // rows, row tiles and places among the experts that have rows, as prefix sums over the experts
+  int rows0 = 0, tiles0 = 0, act0 = 0;
+  for (int e0 = 0; e0 < E; e0 += 1024) {
+    const int e = e0 + tid;
+    const int all = e < E ? cnt[e] : 0;
+    const int mine = static_cast<int>(min(static_cast<int64_t>(all), C));
+    int rows, tiles, act;
+    const int at = rows0 + block_prefix(mine, sums, &rows);
+    const int tile = tiles0 + block_prefix((mine + bt - 1) / bt, sums, &tiles);
+    const int place = act0 + block_prefix(mine > 0 ? 1 : 0, sums, &act);
+    if (e < E) {
+      if (routed) routed[e] = all;
+      if (kept) kept[e] = mine;
+      cnt[e] = at;
+      ls.off[e] = at;
+      ls.tile[e] = tile;
+      if (mine > 0) ls.act[place] = e;
+    }
+    rows0 += rows;
+    tiles0 += tiles;
+    act0 += act;
+  }
+  if (tid == 0) {
+    ls.off[E] = rows0;
+    ls.tile[E] = tiles0;
+    *ls.n_act = act0;
+  }
+  __syncthreads();
+  // every thread places the copies whose slots it wrote
+  for (int64_t c0 = 0; c0 < n; c0 += 64 * W) {
+    const int64_t i = c0 + tid;
+    if (wave < W && i < n) {
+      const int s = slot[i];
+      if (s >= 0) ls.copy[cnt[idx[i]] + s] = static_cast<int32_t>(i);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows an expert: the weights' strips stream from memory into the operand
+// registers. A work-group has a strip of 16 NA weight rows (GU: NA / 2 gate rows'
+// tiles and the up rows' of the same features) and the 16 NT rows of x; its waves
+// share the columns in turn, 128 at a time, and add their sums in LDS.
+// An instruction's A operand is, in lane l, the bytes 16 (l / 16) .. + 15 and 64 +
+// 16 (l / 16) .. + 15 of row l % 16's 128, its scale operand the byte of columns 32
+// (l / 16) .. + 31. Rows are loaded in whole 128-byte lines, eight rows an
+// instruction, and rotated into place (operands()).
+// ---------------------------------------------------------------------------
+struct Mx8 {
+  const uint8_t* codes;   // [E][N][K]
+  const uint32_t* scale;  // [E][steps][N]
+};
+
+struct FewArgs {
+  Mx8 a0, a1;         // weights: gate and up, or down alone
+  int64_t N, K;       // of one matrix
+  Mx8 x;              // rows [R][K]
+  int64_t R;
+  ExpertLists ls;
+  int k;
+  uint8_t* hcodes;    // GU: h [rows][N], scale [steps][H]
+  uint8_t* hscale;
+  int64_t H;
+  void* y;            // else: [copies][N]
+  bool y_bf16;
+};
+
+template <int NA, int NT>
+struct FewStep {
+  u32x4 lo[NA], hi[NA], x0[NT], x1[NT];
+  uint32_t sa[NA], sx[NT];
+};
+
+template <bool GU, int NA, int NT, int WAVES>
+__device__ inline void few_rows(const FewArgs& a, int e, int row0, int n, int64_t strip, float* red) {
+  constexpr int FT = GU ? NA / 2 : NA;  // tiles of 16 output features
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int quad = lane >> 4, half = (lane >> 3) & 1, col = lane & 15;
+  const int64_t steps = ceil_div(a.K, 128), n0 = strip * 16 * FT;
+  const uint8_t* wp[NA];
+  const uint8_t* wq[NA];
+  const uint32_t* sp[NA];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const Mx8& m = GU && i >= FT ? a.a1 : a.a0;
+    const int64_t f0 = n0 + 16 * (i % FT);
+    // rows past the matrix are the last one again; their features are not stored
+    wp[i] = m.codes + (e * a.N + min(f0 + (lane & 7), a.N - 1)) * a.K;
+    wq[i] = m.codes + (e * a.N + min(f0 + 8 + (lane & 7), a.N - 1)) * a.K;
+    sp[i] = m.scale + e * steps * a.N + min(f0 + col, a.N - 1);
+  }
+  const uint8_t* xp[NT];
+  const uint32_t* xs[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = row0 + min(16 * t + col, n - 1);  // columns past the last row are it again
+    const int64_t xr = GU ? a.ls.copy[r] / a.k : r;
+    xp[t] = a.x.codes + xr * a.K;
+    xs[t] = a.x.scale + xr;
+  }
+  f32x4 acc[NA][NT];
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  using Step = FewStep<NA, NT>;
+  auto load = [&](Step& b, int64_t s) {
+    const int64_t k0 = s * 128;
+    const int64_t ca = k0 + 16 * (quad + 4 * half), c0 = k0 + 16 * quad, c1 = c0 + 64;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      b.lo[i] = b.hi[i] = u32x4{0, 0, 0, 0};
+      if (ca < a.K) {
+        b.lo[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + ca));
+        b.hi[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wq[i] + ca));
+      }
+      b.sa[i] = sp[i][s * a.N];
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      b.x0[t] = b.x1[t] = u32x4{0, 0, 0, 0};
+      if (c0 < a.K) b.x0[t] = *reinterpret_cast<const u32x4*>(xp[t] + c0);
+      if (c1 < a.K) b.x1[t] = *reinterpret_cast<const u32x4*>(xp[t] + c1);
+      b.sx[t] = xs[t][s * a.R];
+    }
+  };
+  auto multiply = [&](const Step& b, int64_t s) {
+    const bool past = s * 128 + 32 * quad >= a.K;  // bytes of columns past the last may be anything
+    i32x8 x[NT];
+    int sx[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        x[t][q] = static_cast<int>(b.x0[t][q]);
+        x[t][4 + q] = static_cast<int>(b.x1[t][q]);
+      }
+      sx[t] = past ? 127 : static_cast<int>(b.sx[t] >> (8 * quad));
+    }
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      u32x4 p, q;
+      operands(b.lo[i], b.hi[i], p, q);
+      i32x8 w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = static_cast<int>(p[j]);
+        w[4 + j] = static_cast<int>(q[j]);
+      }
+      const int sa = past ? 127 : static_cast<int>(b.sa[i] >> (8 * quad));
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[t], acc[i][t], 0, 0, 0, sa, 0, sx[t]);
+    }
+  };
+  if (wave < steps) {
+    Step b0, b1;
+    load(b0, wave);
+    int64_t s = wave;
+    for (; s + WAVES < steps; s += 2 * WAVES) {
+      load(b1, s + WAVES);
+      multiply(b0, s);
+      if (s + 2 * WAVES < steps) load(b0, s + 2 * WAVES);
+      multiply(b1, s + WAVES);
+    }
+    if (s < steps) multiply(b0, s);
+  }
+  // the waves' sums, in their order: wave t has token tile t
+  f32x4* mine = reinterpret_cast<f32x4*>(red);
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) mine[((wave * NT + t) * NA + i) * 64 + lane] = acc[i][t];
+  __syncthreads();
+  static_assert(WAVES >= NT, "a wave a token tile");
+  if (wave < NT) {
+    f32x4 v[NA];
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      v[i] = mine[(wave * NA + i) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) v[i] += mine[((w * NT + wave) * NA + i) * 64 + lane];
+    }
+    const int c = 16 * wave + col;  // the row, of n
+    if constexpr (GU) {
+      static_assert(FT == 2, "a strip is the 32 features of a scale");
+      uint32_t big = 0;
+      f32x4 h[FT];
+#pragma unroll
+      for (int i = 0; i < FT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h[i][q] = n0 + 16 * i + 4 * quad + q < a.N ? silu(v[i][q]) * v[FT + i][q] : 0.f;
+          big = max(big, __float_as_uint(h[i][q]) & 0x7fffffffu);
+        }
+      big = max(big, static_cast<uint32_t>(__shfl_xor(big, 16, 64)));
+      big = max(big, static_cast<uint32_t>(__shfl_xor(big, 32, 64)));
+      const uint32_t byte = mx8_scale_byte(big);
+      const float inv = mx8_inverse(byte);
+      if (c < n) {
+        const int64_t r = row0 + c;
+        if (quad == 0) a.hscale[mx8_scale_at(n0 / 128, a.H, r) * 4 + n0 / 32 % 4] = static_cast<uint8_t>(byte);
+#pragma unroll
+        for (int i = 0; i < FT; ++i)
+          if (n0 + 16 * i < a.N)
+            *reinterpret_cast<uint32_t*>(a.hcodes + r * a.N + n0 + 16 * i + 4 * quad) =
+                mx8_codes(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv);
+      }
+    } else if (c < n) {
+      const int64_t r = a.ls.copy[row0 + c];
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        const int64_t f = n0 + 16 * i + 4 * quad;
+        if (f >= a.N) continue;
+        if (a.y_bf16)
+          *reinterpret_cast<uint2*>(static_cast<bf16_t*>(a.y) + r * a.N + f) =
+              uint2{f32_to_bf16(v[i][0]) | static_cast<uint32_t>(f32_to_bf16(v[i][1])) << 16,
+                    f32_to_bf16(v[i][2]) | static_cast<uint32_t>(f32_to_bf16(v[i][3])) << 16};
+        else
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + r * a.N + f) = v[i];
+      }
+    }
+  }
+  __syncthreads();  // the sums are read before the next rows' are written
+}
+
+template <bool GU, int NA, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(FewArgs a, int strips) {
+  __shared__ float red[WAVES * 2 * NA * 64 * 4];
+  const int i = static_cast<int>(blockIdx.x / strips);
+  if (i >= *a.ls.n_act) return;
+  const int e = a.ls.act[i];
+  const int64_t strip = blockIdx.x % strips;
+  const int end = a.ls.off[e + 1];
+  for (int r = a.ls.off[e]; r < end; r += 32) {
+    const int n = min(end - r, 32);
+    if (n <= 16)
+      few_rows<GU, NA, 1, WAVES>(a, e, r, n, strip, red);
+    else
+      few_rows<GU, NA, 2, WAVES>(a, e, r, n, strip, red);
+  }
+}
+
+// out[t] = residual[t] + sum_j w y[t, j] over the kept copies, j ascending, in
+// fp32; a token without a kept copy passes bit for bit.
+template <bool BF16>
+__global__ __launch_bounds__(256) void experts_combine_kernel(const uint4* __restrict__ residual,
+                                                              const uint4* __restrict__ y,
+                                                              const float* __restrict__ w,
+                                                              const int32_t* __restrict__ slot, int k, int64_t V,
+                                                              int64_t blocks, uint4* __restrict__ out) {
+  constexpr int P = BF16 ? 8 : 4;
+  const int64_t t = blockIdx.x / blocks, v = blockIdx.x % blocks * 256 + threadIdx.x;
+  if (v >= V) return;
+  const uint4 in = load_stream(residual + t * V + v);
+  float acc[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) acc[i] = 0.f;
+  bool any = false;
+  for (int j = 0; j < k; ++j) {
+    if (slot[t * k + j] < 0) continue;
+    any = true;
+    const uint4 word = load_stream(y + (t * k + j) * V + v);
+    const float g = w[t * k + j];
+    const uint32_t u[4] = {word.x, word.y, word.z, word.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if constexpr (BF16) {
+        acc[2 * q] = fmaf(g, __uint_as_float(u[q] << 16), acc[2 * q]);
+        acc[2 * q + 1] = fmaf(g, __uint_as_float(u[q] & 0xffff0000u), acc[2 * q + 1]);
+      } else {
+        acc[q] = fmaf(g, __uint_as_float(u[q]), acc[q]);
+      }
+  }
+  uint32_t u[4] = {in.x, in.y, in.z, in.w};
+  if (any) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if constexpr (BF16)
+        u[q] = f32_to_bf16(__uint_as_float(u[q] << 16) + acc[2 * q]) |
+               static_cast<uint32_t>(f32_to_bf16(__uint_as_float(u[q] & 0xffff0000u) + acc[2 * q + 1])) << 16;
+      else
+        u[q] = __float_as_uint(__uint_as_float(u[q]) + acc[q]);
+  }
+  store_stream(out + t * V + v, uint4{u[0], u[1], u[2], u[3]});
+}
+
+Mx8 view(const Mx8Ptr& p) { return {p.codes, p.scale}; }
+
+}  // namespace
+
+hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
+  experts_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.idx, L.T, L.k, L.E, L.C, 256, L.slot, L.routed, L.kept, L.ls);
+  const int64_t copies = L.T * L.k, act = std::min<int64_t>(L.E, copies);
+  FewArgs a;
+  a.a0 = view(L.gate);
+  a.a1 = view(L.up);
+  a.N = L.f;
+  a.K = L.d;
+  a.x = view(L.x);
+  a.R = L.T;
+  a.ls = L.ls;
+  a.k = L.k;
+  a.hcodes = L.h.codes;
+  a.hscale = reinterpret_cast<uint8_t*>(L.h.scale);
+  a.H = copies;
+  a.y = nullptr;
+  a.y_bf16 = L.bf16;
+  int strips = static_cast<int>(ceil_div(L.f, 32));
+  few_rows_kernel<true, 4, 8><<<dim3(static_cast<unsigned>(act * strips)), dim3(512), 0, s>>>(a, strips);
+  FewArgs b = a;
+  b.a0 = b.a1 = view(L.down);
+  b.N = L.d;
+  b.K = L.f;
+  b.x = view(L.h);
+  b.R = copies;
+  b.y = L.y;
+  strips = static_cast<int>(ceil_div(L.d, 32));
+  few_rows_kernel<false, 2, 4><<<dim3(static_cast<unsigned>(act * strips)), dim3(256), 0, s>>>(b, strips);
+  const int64_t V = L.d / (L.bf16 ? 8 : 4), blocks = ceil_div(V, 256);
+  const dim3 grid(static_cast<unsigned>(L.T * blocks));
+  const auto* rv = static_cast<const uint4*>(L.residual);
+  const auto* yv = static_cast<const uint4*>(L.y);
+  if (L.bf16)
+    experts_combine_kernel<true><<<grid, dim3(256), 0, s>>>(rv, yv, L.w, L.slot, L.k, V, blocks, static_cast<uint4*>(L.out));
+  else
+    experts_combine_kernel<false><<<grid, dim3(256), 0, s>>>(rv, yv, L.w, L.slot, L.k, V, blocks, static_cast<uint4*>(L.out));
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -42,7 +42,7 @@ def pack_scale(groups, K):
     """Bytes [.., N, ceil(K/32)] in the layout [.., ceil(K/128), N, 4], padding 127."""
     pad = -groups.shape[-1] % 4
     g = np.concatenate([groups, np.full((*groups.shape[:-1], pad), 127)], -1)
-    return np.swapaxes(g.reshape(*groups.shape[:-1], -1, 4), -3, -2).astype(np.uint8)
+    return np.ascontiguousarray(np.swapaxes(g.reshape(*groups.shape[:-1], -1, 4), -3, -2), np.uint8)
 
 
 def unpack_scale(scale, K):
