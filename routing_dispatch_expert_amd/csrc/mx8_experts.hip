@@ -20,17 +20,13 @@
 //
 // No bucket is built: lists of the kept copies by expert, in token order, say
 // which rows of x an expert reads and which rows of y it writes.
-#include "mx8.h"
+#include "mx8_experts.h"
 #include "q4.h"
 
 #include <algorithm>
 
 namespace moe {
 namespace {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-__device__ inline float silu(float g) { return g / (1.0f + expf(-g)); }
 
 // ---------------------------------------------------------------------------
 // Lists, by one work-group. Copies are taken 64 a wave and up to 16 waves at a
@@ -159,25 +155,6 @@ __global__ __launch_bounds__(1024) void experts_plan_kernel(const int32_t* __res
 // (l / 16) .. + 31. Rows are loaded in whole 128-byte lines, eight rows an
 // instruction, and rotated into place (operands()).
 // ---------------------------------------------------------------------------
-struct Mx8 {
-  const uint8_t* codes;   // [E][N][K]
-  const uint32_t* scale;  // [E][steps][N]
-};
-
-struct FewArgs {
-  Mx8 a0, a1;         // weights: gate and up, or down alone
-  int64_t N, K;       // of one matrix
-  Mx8 x;              // rows [R][K]
-  int64_t R;
-  ExpertLists ls;
-  int k;
-  uint8_t* hcodes;    // GU: h [rows][N], scale [steps][H]
-  uint8_t* hscale;
-  int64_t H;
-  void* y;            // else: [copies][N]
-  bool y_bf16;
-};
-
 template <int NA, int NT>
 struct FewStep {
   u32x4 lo[NA], hi[NA], x0[NT], x1[NT];
@@ -185,7 +162,7 @@ struct FewStep {
 };
 
 template <bool GU, int NA, int NT, int WAVES>
-__device__ inline void few_rows(const FewArgs& a, int e, int row0, int n, int64_t strip, float* red) {
+__device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int64_t strip, float* red) {
   constexpr int FT = GU ? NA / 2 : NA;  // tiles of 16 output features
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int quad = lane >> 4, half = (lane >> 3) & 1, col = lane & 15;
@@ -339,7 +316,7 @@ __device__ inline void few_rows(const FewArgs& a, int e, int row0, int n, int64_
 }
 
 template <bool GU, int NA, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(FewArgs a, int strips) {
+__global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(Mx8Gemm a, int strips) {
   __shared__ float red[WAVES * 2 * NA * 64 * 4];
   const int i = static_cast<int>(blockIdx.x / strips);
   if (i >= *a.ls.n_act) return;
@@ -404,9 +381,9 @@ Mx8 view(const Mx8Ptr& p) { return {p.codes, p.scale}; }
 }  // namespace
 
 hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
-  experts_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.idx, L.T, L.k, L.E, L.C, 256, L.slot, L.routed, L.kept, L.ls);
+  experts_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.idx, L.T, L.k, L.E, L.C, mx8_tile_rows(), L.slot, L.routed, L.kept, L.ls);
   const int64_t copies = L.T * L.k, act = std::min<int64_t>(L.E, copies);
-  FewArgs a;
+  Mx8Gemm a;
   a.a0 = view(L.gate);
   a.a1 = view(L.up);
   a.N = L.f;
@@ -420,9 +397,16 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   a.H = copies;
   a.y = nullptr;
   a.y_bf16 = L.bf16;
+  const bool many = copies > 64 * act;
+  const int64_t tiles = copies / mx8_tile_rows() + act;
   int strips = static_cast<int>(ceil_div(L.f, 32));
-  few_rows_kernel<true, 4, 8><<<dim3(static_cast<unsigned>(act * strips)), dim3(512), 0, s>>>(a, strips);
-  FewArgs b = a;
+  if (many) {
+    const hipError_t e = launch_mx8_tiles(a, true, L.E, tiles, s);
+    if (e != hipSuccess) return e;
+  } else {
+    few_rows_kernel<true, 4, 8><<<dim3(static_cast<unsigned>(act * strips)), dim3(512), 0, s>>>(a, strips);
+  }
+  Mx8Gemm b = a;
   b.a0 = b.a1 = view(L.down);
   b.N = L.d;
   b.K = L.f;
@@ -430,7 +414,12 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   b.R = copies;
   b.y = L.y;
   strips = static_cast<int>(ceil_div(L.d, 32));
-  few_rows_kernel<false, 2, 4><<<dim3(static_cast<unsigned>(act * strips)), dim3(256), 0, s>>>(b, strips);
+  if (many) {
+    const hipError_t e = launch_mx8_tiles(b, false, L.E, tiles, s);
+    if (e != hipSuccess) return e;
+  } else {
+    few_rows_kernel<false, 2, 4><<<dim3(static_cast<unsigned>(act * strips)), dim3(256), 0, s>>>(b, strips);
+  }
   const int64_t V = L.d / (L.bf16 ? 8 : 4), blocks = ceil_div(V, 256);
   const dim3 grid(static_cast<unsigned>(L.T * blocks));
   const auto* rv = static_cast<const uint4*>(L.residual);

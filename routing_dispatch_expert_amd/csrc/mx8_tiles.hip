@@ -1,0 +1,347 @@
+// The experts' products with 8-bit rows and weights where an expert has many rows
+// (gfx950): blocks of 256 weight rows by 256 rows of x, brought into LDS by the
+// buffer unit, two stages of 128 columns (a row's stage is a 128-byte line).
+//
+// As in mx8_experts.hip the weights are the A operand: lane l of a 32 x 32 x 64
+// instruction holds, of row l % 32, the bytes 16 (l / 32) .. + 15 and 32 + 16 (l /
+// 32) .. + 15 of 64 columns, and the scale byte of columns 32 (l / 32) .. + 31; its
+// accumulator element q is feature 8 (q / 4) + 4 (l / 32) + q % 4 of row l % 32 of x.
+// With gate and up a wave has the gate rows' and the up rows' tiles of the same
+// features, so silu(g) u, the scale of 32 features and the codes stay in its lanes.
+//
+// LDS rows are eight 16-byte pieces; piece c of row r sits at c ^ ((r / 2) % 8), so
+// that 16 lanes reading 16 neighbouring rows meet 16 bank groups. One DMA
+// instruction of a wave fills 8 rows: lane L writes row L / 8, position L % 8,
+// and fetches the piece that belongs there.
+#include "mx8_experts.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+#define MOE_LDS(p) ((__attribute__((address_space(3))) void*)(p))
+
+__device__ inline __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(bytes),
+                                           0x00020000);
+}
+
+// s_waitcnt: everything of this wave's loads, and its LDS reads.
+__device__ inline __attribute__((unused)) void wait_all() { __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (0 << 8)); }
+
+constexpr int kFeatureGroup = 8;  // feature tiles that go through an expert's row tiles together (shared in L2)
+
+// Block b of the live tiles: XCD b % 8 takes a contiguous eighth of them.
+struct Tile {
+  int e, row0, rows;  // rows of the expert's list
+  int64_t n0;
+};
+
+__device__ inline bool tile_of_block(const ExpertLists& ls, int E, int row_tile, int feature_tile, int64_t N, Tile* t) {
+  const int ft = static_cast<int>((N + feature_tile - 1) / feature_tile);
+  const int64_t live = static_cast<int64_t>(ls.tile[E]) * ft, per = (live + 7) / 8;
+  const int64_t at = blockIdx.x / 8, id = blockIdx.x % 8 * per + at;
+  if (at >= per || id >= live) return false;
+  const int rt = static_cast<int>(id / ft);
+  int lo = 0, hi = E;  // tile[lo] <= rt < tile[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ls.tile[mid] <= rt)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int first = ls.tile[lo], n = ls.tile[lo + 1] - first;
+  const int64_t in = id - static_cast<int64_t>(first) * ft;
+  const int64_t group = in / (static_cast<int64_t>(n) * kFeatureGroup);
+  const int wide = static_cast<int>(min(static_cast<int64_t>(kFeatureGroup), ft - group * kFeatureGroup));
+  const int rest = static_cast<int>(in - group * n * kFeatureGroup);
+  t->e = lo;
+  t->n0 = (group * kFeatureGroup + rest % wide) * feature_tile;
+  // the expert's rows are shared evenly by its tiles, in whole blocks of 32
+  const int all = ls.off[lo + 1] - ls.off[lo], each = 32 * ((all + 32 * n - 1) / (32 * n));
+  t->row0 = rest / wide * each;
+  t->rows = min(all - t->row0, each);
+  return true;
+}
+
+// WM x WN waves of TM x TN tiles of 32 x 32.
+template <bool GU, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM* WN / 4, WM* WN / 4))) void mx8_tile_kernel(
+    Mx8Gemm a, int E) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass has no scaled matrix instruction and would drop the kernel without a word
+  constexpr int NW = WM * WN, MA = WM * TM * 32, MX = WN * TN * 32;
+  constexpr int FW = (GU ? TM / 2 : TM) * 32;          // features of a wave
+  constexpr int FB = WM * FW;                          // and of the block
+  constexpr int PA = MA / 8 / NW, PX = MX / 8 / NW;    // 8-row DMA pieces of a wave
+  static_assert((MA + MX) / 64 == NW || (MA + MX) / 64 == 2 * NW, "a wave loads one or two sets of 64 scales");
+  constexpr int PS = (MA + MX) / 64 / NW;
+  __shared__ uint4 As0[MA * 8], As1[MA * 8], Xs0[MX * 8], Xs1[MX * 8];
+  __shared__ uint32_t Sc0[MA + MX], Sc1[MA + MX];
+
+  Tile tl;
+  if (!tile_of_block(a.ls, E, MX, FB, a.N, &tl)) return;
+  const int e = __builtin_amdgcn_readfirstlane(tl.e);
+  const int rows = __builtin_amdgcn_readfirstlane(tl.rows);
+  const int first = __builtin_amdgcn_readfirstlane(a.ls.off[e] + tl.row0);  // row of the lists
+  const int64_t n0 = __builtin_amdgcn_readfirstlane(static_cast<int>(tl.n0));
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN, lr = lane & 31, lq = lane >> 5;
+  const int64_t K = a.K, N = a.N, steps = ceil_div(K, 128);
+
+  // row r of the block's A operand: feature and matrix
+  auto feature = [&](int r) {
+    const int w = r / (TM * 32), i = r / 32 % TM, in = r & 31;
+    return min(n0 + w * FW + (GU ? i % (TM / 2) : i) * 32 + in, N - 1);  // past the matrix: the last one again
+  };
+  auto is_up = [&](int r) { return GU && r / 32 % TM >= TM / 2; };
+  const int64_t span = N * K;
+  const auto ra0 = rsrc(a.a0.codes + e * span, span), ra1 = rsrc(a.a1.codes + e * span, span);
+  // GU reads the tokens' rows (all of x), else the lists' rows from the expert's first
+  const int64_t xbase = GU ? 0 : first, xrows = GU ? a.R : rows;
+  const auto rx = rsrc(a.x.codes + xbase * K, xrows * K);
+  auto x_row = [&](int r) {
+    const int at = first + min(r, rows - 1);  // past the last row: it again
+    return GU ? static_cast<int64_t>(a.ls.copy[at] / a.k) : static_cast<int64_t>(at);
+  };
+  uint32_t va[PA], vx[PX];
+#pragma unroll
+  for (int i = 0; i < PA; ++i) {
+    const int r = (wave * PA + i) * 8 + (lane >> 3);
+    va[i] = static_cast<uint32_t>(feature(r) * K + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
+  }
+#pragma unroll
+  for (int i = 0; i < PX; ++i) {
+    const int r = (wave * PX + i) * 8 + (lane >> 3);
+    vx[i] = static_cast<uint32_t>((x_row(r) - xbase) * K + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
+  }
+  // the scales: rows 64 (PS wave + i) + lane of A's (of one matrix: TM % 4 == 0), then of x's
+  static_assert(!GU || TM % 4 == 0, "64 rows of A are of one matrix");
+  const int64_t sbytes = steps * N * 4;
+  const auto rs0 = rsrc(a.a0.scale + e * steps * N, sbytes), rs1 = rsrc(a.a1.scale + e * steps * N, sbytes);
+  const auto rsx = rsrc(a.x.scale, steps * a.R * 4);
+  uint32_t vs[PS];
+#pragma unroll
+  for (int i = 0; i < PS; ++i) {
+    const int r = (wave * PS + i) * 64;
+    vs[i] = static_cast<uint32_t>(4 * (r < MA ? feature(r + lane) : x_row(r + lane - MA)));
+  }
+  auto dma = [&](uint4* as, uint4* xs, uint32_t* sc, int64_t s) {
+    const int k0 = static_cast<int>(s * 128);
+    const bool tail = k0 + 128 > K;  // pieces past the last column: zero (an offset past the buffer)
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+      const int r = (wave * PA + i) * 8;
+      uint32_t v = va[i];
+      if (tail && k0 + 16 * ((lane & 7) ^ (((r + (lane >> 3)) >> 1) & 7)) >= K) v = 0x80000000u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_up(r) ? ra1 : ra0, MOE_LDS(as + r * 8), 16, v, k0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < PX; ++i) {
+      const int r = (wave * PX + i) * 8;
+      uint32_t v = vx[i];
+      if (tail && k0 + 16 * ((lane & 7) ^ (((r + (lane >> 3)) >> 1) & 7)) >= K) v = 0x80000000u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MOE_LDS(xs + r * 8), 16, v, k0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < PS; ++i) {
+      const int r = (wave * PS + i) * 64;
+      const int soff = static_cast<int>(s * (r < MA ? N : a.R) * 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r >= MA ? rsx : is_up(r) ? rs1 : rs0, MOE_LDS(sc + r), 4, vs[i], soff, 0, 0);
+    }
+  };
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+
+  // a wave multiplies the 32-row blocks of x that have rows
+  const int left = rows - wn * TN * 32;
+  const int live = __builtin_amdgcn_readfirstlane(left <= 0 ? 0 : min(TN, (left + 31) / 32));
+  const int sw = (lr >> 1) & 7;
+  auto loop = [&](auto live_c) {
+    constexpr int TX = decltype(live_c)::value;
+    i32x8 fa[2][TM], fx[2][TN];
+    uint32_t sa[TM], sx[TN];
+    auto read = [&](const uint4* base, int row, int h) {
+      const uint4* p = base + row * 8;
+      const uint4 lo = p[(4 * h + lq) ^ sw], hi = p[(4 * h + 2 + lq) ^ sw];
+      return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
+                   static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
+    };
+    auto fload = [&](const uint4* as, const uint4* xs, int h, int slot) {
+      if constexpr (TX > 0) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[slot][i] = read(as, (wm * TM + i) * 32 + lr, h);
+#pragma unroll
+        for (int j = 0; j < TX; ++j) fx[slot][j] = read(xs, (wn * TN + j) * 32 + lr, h);
+      }
+    };
+    // byte 0 of a scale operand is that of the first 64 columns' block lq, byte 2 of the second's
+    auto sload = [&](const uint32_t* sc, int64_t s) {
+      if constexpr (TX > 0) {
+        const int64_t groups = ceil_div(K - s * 128, 32);  // with columns; bytes past them may be anything
+        const uint32_t mask = groups >= 4 ? ~0u : (1u << (8 * groups)) - 1;
+        auto fix = [&](uint32_t v) { return ((v & mask) | (0x7f7f7f7fu & ~mask)) >> (8 * lq); };
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = fix(sc[(wm * TM + i) * 32 + lr]);
+#pragma unroll
+        for (int j = 0; j < TX; ++j) sx[j] = fix(sc[MA + (wn * TN + j) * 32 + lr]);
+      }
+    };
+    auto multiply = [&](auto half) {
+      constexpr int H = decltype(half)::value;
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TX; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[H][i], fx[H][j], acc[i][j], 0, 0, 2 * H,
+                                                                     static_cast<int>(sa[i]), 2 * H, static_cast<int>(sx[j]));
+    };
+    using Half0 = std::integral_constant<int, 0>;
+    using Half1 = std::integral_constant<int, 1>;
+    // stage s is in (as, xs, sc), its first half's operands in slot 0; stage s + 1 is on its way into the other.
+    // Whether there are stages s + 1 and s + 2 is known here: a branch around the matrix work instead made the
+    // compiler keep the accumulators twice.
+    auto stage = [&](auto next, auto next2, uint4* as, uint4* xs, uint32_t* sc, uint4* an, uint4* xn, uint32_t* sn,
+                     int64_t s) {
+      fload(as, xs, 1, 1);
+      multiply(Half0{});
+      if constexpr (decltype(next)::value) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_all();                    // own share of stage s + 1 landed, reads of stage s done ...
+        __builtin_amdgcn_s_barrier();  // ... and everyone's
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(next2)::value) dma(as, xs, sc, s + 2);
+        fload(an, xn, 0, 0);
+      }
+      multiply(Half1{});
+      if constexpr (decltype(next)::value) sload(sn, s + 1);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    int64_t s = steps & 1;
+    if (s) {  // an odd number of stages: one by itself, then pairs
+      dma(As0, Xs0, Sc0, 0);
+      wait_all();
+      __builtin_amdgcn_s_barrier();
+      fload(As0, Xs0, 0, 0);
+      sload(Sc0, 0);
+      stage(No{}, No{}, As0, Xs0, Sc0, As1, Xs1, Sc1, 0);
+      wait_all();
+      __builtin_amdgcn_s_barrier();
+    }
+    if (s < steps) {
+      dma(As0, Xs0, Sc0, s);
+      wait_all();
+      __builtin_amdgcn_s_barrier();
+      dma(As1, Xs1, Sc1, s + 1);
+      fload(As0, Xs0, 0, 0);
+      sload(Sc0, s);
+      for (; s + 2 < steps; s += 2) {
+        stage(Yes{}, Yes{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
+        stage(Yes{}, Yes{}, As1, Xs1, Sc1, As0, Xs0, Sc0, s + 1);
+      }
+      stage(Yes{}, No{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
+      stage(No{}, No{}, As1, Xs1, Sc1, As0, Xs0, Sc0, s + 1);
+    }
+  };
+  if (live == TN)
+    loop(std::integral_constant<int, TN>{});
+  else if (TN > 2 && live > TN / 2)
+    loop(std::integral_constant<int, TN>{});
+  else if (live > 0)
+    loop(std::integral_constant<int, (TN + 1) / 2>{});
+  else
+    loop(std::integral_constant<int, 0>{});
+
+  const int64_t nw = n0 + wm * FW;  // the wave's first feature
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int c = (wn * TN + j) * 32 + lr;  // the row, of `rows`
+    if constexpr (GU) {
+      const int64_t r = first + c;
+#pragma unroll
+      for (int i = 0; i < TM / 2; ++i) {
+        const int64_t f0 = nw + 32 * i;
+        float h[16];
+        uint32_t big = 0;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          h[q] = f0 + 8 * (q / 4) + 4 * lq + q % 4 < N ? silu(acc[i][j][q]) * acc[i + TM / 2][j][q] : 0.f;
+          big = max(big, __float_as_uint(h[q]) & 0x7fffffffu);
+        }
+        big = max(big, static_cast<uint32_t>(__shfl_xor(big, 32, 64)));
+        const uint32_t byte = mx8_scale_byte(big);
+        const float inv = mx8_inverse(byte);
+        uint32_t w[4];  // words 0, 2, 4, 6 (lanes 0 - 31) or 1, 3, 5, 7 of the 32 codes
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          w[g] = mx8_codes(h[4 * g] * inv, h[4 * g + 1] * inv, h[4 * g + 2] * inv, h[4 * g + 3] * inv);
+        // the halves exchange two words each and have 16 codes in a row
+        const uint32_t o0 = __shfl_xor(lq ? w[0] : w[2], 32, 64), o1 = __shfl_xor(lq ? w[1] : w[3], 32, 64);
+        const uint4 out = lq ? uint4{o0, w[2], o1, w[3]} : uint4{w[0], o0, w[1], o1};
+        if (c < rows && f0 + 16 * lq < N) {
+          *reinterpret_cast<uint4*>(a.hcodes + r * N + f0 + 16 * lq) = out;
+          if (lq == 0) a.hscale[mx8_scale_at(f0 / 128, a.H, r) * 4 + f0 / 32 % 4] = static_cast<uint8_t>(byte);
+        }
+      }
+    } else {
+      const int64_t r = c < rows ? a.ls.copy[first + c] : 0;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int64_t f0 = nw + 32 * i;
+        if (a.y_bf16) {
+          uint2 w[4];  // features 8 g + 4 lq .. + 3
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            w[g] = uint2{f32_to_bf16(acc[i][j][4 * g]) | static_cast<uint32_t>(f32_to_bf16(acc[i][j][4 * g + 1])) << 16,
+                         f32_to_bf16(acc[i][j][4 * g + 2]) | static_cast<uint32_t>(f32_to_bf16(acc[i][j][4 * g + 3])) << 16};
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {  // lanes 0 - 31 get features 8 g .. + 7, the others 8 g + 8 .. + 15
+            const uint2 give = lq ? w[g] : w[g + 1];
+            const uint2 got = uint2{static_cast<uint32_t>(__shfl_xor(give.x, 32, 64)), static_cast<uint32_t>(__shfl_xor(give.y, 32, 64))};
+            const int64_t f = f0 + 8 * g + 8 * lq;
+            if (c < rows && f < N)
+              *reinterpret_cast<uint4*>(static_cast<bf16_t*>(a.y) + r * N + f) =
+                  lq ? uint4{got.x, got.y, w[g + 1].x, w[g + 1].y} : uint4{w[g].x, w[g].y, got.x, got.y};
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int64_t f = f0 + 8 * g + 4 * lq;
+            if (c < rows && f < N)
+              *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + r * N + f) =
+                  f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+          }
+        }
+      }
+    }
+  }
+#endif
+}
+
+template <bool GU>
+hipError_t launch(const Mx8Gemm& a, int E, int64_t tiles, hipStream_t s) {
+  constexpr int WM = 2, WN = 2, TM = 4, TN = 4;
+  const int64_t ft = ceil_div(a.N, WM * (GU ? TM / 2 : TM) * 32);
+  const dim3 grid(static_cast<unsigned>(ceil_div(tiles * ft, 8) * 8));
+  mx8_tile_kernel<GU, WM, WN, TM, TN><<<grid, dim3(WM * WN * 64), 0, s>>>(a, E);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int mx8_tile_rows() { return 256; }
+
+hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, hipStream_t s) {
+  return gate_up ? launch<true>(a, E, tiles, s) : launch<false>(a, E, tiles, s);
+}
+
+}  // namespace moe
