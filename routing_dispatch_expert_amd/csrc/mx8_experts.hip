@@ -24,6 +24,7 @@
 #include "q4.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -155,6 +156,26 @@ __global__ __launch_bounds__(1024) void experts_plan_kernel(const int32_t* __res
 // (l / 16) .. + 31. Rows are loaded in whole 128-byte lines, eight rows an
 // instruction, and rotated into place (operands()).
 // ---------------------------------------------------------------------------
+// A range of memory for loads at an offset that is the same for all lanes plus a
+// lane's own; a lane past the end gets 0 and touches nothing.
+struct Range {
+  const void* base;
+  uint32_t bytes;
+  __device__ inline __amdgpu_buffer_rsrc_t rsrc() const {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(bytes),
+                                             0x00020000);
+  }
+  template <bool ONCE>  // read once: not to be kept in the caches
+  __device__ inline u32x4 load16(uint32_t lane_off, uint32_t off) const {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(rsrc(), static_cast<int>(lane_off), static_cast<int>(off), ONCE ? 2 : 0);
+    return u32x4{static_cast<uint32_t>(v[0]), static_cast<uint32_t>(v[1]), static_cast<uint32_t>(v[2]), static_cast<uint32_t>(v[3])};
+  }
+  __device__ inline uint32_t load4(uint32_t lane_off, uint32_t off) const {
+    return __builtin_amdgcn_raw_buffer_load_b32(rsrc(), static_cast<int>(lane_off), static_cast<int>(off), 0);
+  }
+};
+constexpr uint32_t kNowhere = 0x80000000u;  // a lane's offset past every range
+
 template <int NA, int NT>
 struct FewStep {
   u32x4 lo[NA], hi[NA], x0[NT], x1[NT];
@@ -162,31 +183,27 @@ struct FewStep {
 };
 
 template <bool GU, int NA, int NT, int WAVES>
-__device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int64_t strip, float* red) {
+__device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int strip, float* red) {
   constexpr int FT = GU ? NA / 2 : NA;  // tiles of 16 output features
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int quad = lane >> 4, half = (lane >> 3) & 1, col = lane & 15;
-  const int64_t steps = ceil_div(a.K, 128), n0 = strip * 16 * FT;
-  const uint8_t* wp[NA];
-  const uint8_t* wq[NA];
-  const uint32_t* sp[NA];
-#pragma unroll
-  for (int i = 0; i < NA; ++i) {
-    const Mx8& m = GU && i >= FT ? a.a1 : a.a0;
-    const int64_t f0 = n0 + 16 * (i % FT);
-    // rows past the matrix are the last one again; their features are not stored
-    wp[i] = m.codes + (e * a.N + min(f0 + (lane & 7), a.N - 1)) * a.K;
-    wq[i] = m.codes + (e * a.N + min(f0 + 8 + (lane & 7), a.N - 1)) * a.K;
-    sp[i] = m.scale + e * steps * a.N + min(f0 + col, a.N - 1);
-  }
-  const uint8_t* xp[NT];
-  const uint32_t* xs[NT];
+  const int K = static_cast<int>(a.K), N = static_cast<int>(a.N), steps = (K + 127) / 128, n0 = strip * 16 * FT;
+  const uint32_t span = static_cast<uint32_t>(N) * K, sspan = static_cast<uint32_t>(steps) * N * 4;
+  // Rows past the matrix read as zeros, with some other row's scales: what becomes of their features is not stored.
+  const Range w0 = {a.a0.codes + static_cast<int64_t>(e) * span, span}, w1 = {a.a1.codes + static_cast<int64_t>(e) * span, span};
+  const Range s0 = {a.a0.scale + static_cast<int64_t>(e) * steps * N, sspan}, s1 = {a.a1.scale + static_cast<int64_t>(e) * steps * N, sspan};
+  // x's rows: the tokens' (of all) with GU, else the lists' from row0 on
+  const int64_t xbase = GU ? 0 : row0;
+  const Range x = {a.x.codes + xbase * K, static_cast<uint32_t>((GU ? a.R : n) * K)};
+  const Range xs = {a.x.scale, static_cast<uint32_t>(steps * a.R * 4)};
+  const uint32_t wv = static_cast<uint32_t>(n0 + (lane & 7)) * K + 16 * (quad + 4 * half), sv = 4 * (n0 + col);
+  uint32_t xv[NT], xsv[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = row0 + min(16 * t + col, n - 1);  // columns past the last row are it again
-    const int64_t xr = GU ? a.ls.copy[r] / a.k : r;
-    xp[t] = a.x.codes + xr * a.K;
-    xs[t] = a.x.scale + xr;
+    const uint32_t xr = GU ? a.ls.copy[r] / a.k : r;
+    xv[t] = static_cast<uint32_t>(xr - xbase) * K + 16 * quad;
+    xsv[t] = 4 * xr;
   }
   f32x4 acc[NA][NT];
 #pragma unroll
@@ -195,36 +212,36 @@ __device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int64_
     for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   using Step = FewStep<NA, NT>;
-  auto load = [&](Step& b, int64_t s) {
-    const int64_t k0 = s * 128;
-    const int64_t ca = k0 + 16 * (quad + 4 * half), c0 = k0 + 16 * quad, c1 = c0 + 64;
+  auto load = [&](Step& b, int s) {
+    const uint32_t k0 = s * 128;
+    const bool tail = k0 + 128 > static_cast<uint32_t>(K);
+    const uint32_t ca = tail && k0 + 16 * (quad + 4 * half) >= static_cast<uint32_t>(K) ? kNowhere : wv;
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-      b.lo[i] = b.hi[i] = u32x4{0, 0, 0, 0};
-      if (ca < a.K) {
-        b.lo[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + ca));
-        b.hi[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wq[i] + ca));
-      }
-      b.sa[i] = sp[i][s * a.N];
+      const uint32_t at = k0 + 16 * (i % FT) * K;
+      const Range& w = GU && i >= FT ? w1 : w0;
+      b.lo[i] = w.load16<true>(ca, at);
+      b.hi[i] = w.load16<true>(ca, at + 8 * K);
+      b.sa[i] = (GU && i >= FT ? s1 : s0).load4(sv, 4 * (s * N + 16 * (i % FT)));
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      b.x0[t] = b.x1[t] = u32x4{0, 0, 0, 0};
-      if (c0 < a.K) b.x0[t] = *reinterpret_cast<const u32x4*>(xp[t] + c0);
-      if (c1 < a.K) b.x1[t] = *reinterpret_cast<const u32x4*>(xp[t] + c1);
-      b.sx[t] = xs[t][s * a.R];
+      const bool no0 = tail && k0 + 16 * quad >= static_cast<uint32_t>(K), no1 = tail && k0 + 16 * quad + 64 >= static_cast<uint32_t>(K);
+      b.x0[t] = x.load16<false>(no0 ? kNowhere : xv[t], k0);
+      b.x1[t] = x.load16<false>(no1 ? kNowhere : xv[t], k0 + 64);
+      b.sx[t] = xs.load4(xsv[t], static_cast<uint32_t>(s * a.R * 4));
     }
   };
-  auto multiply = [&](const Step& b, int64_t s) {
-    const bool past = s * 128 + 32 * quad >= a.K;  // bytes of columns past the last may be anything
-    i32x8 x[NT];
+  auto multiply = [&](const Step& b, int s) {
+    const bool past = s * 128 + 32 * quad >= K;  // bytes of columns past the last may be anything
+    i32x8 xx[NT];
     int sx[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        x[t][q] = static_cast<int>(b.x0[t][q]);
-        x[t][4 + q] = static_cast<int>(b.x1[t][q]);
+        xx[t][q] = static_cast<int>(b.x0[t][q]);
+        xx[t][4 + q] = static_cast<int>(b.x1[t][q]);
       }
       sx[t] = past ? 127 : static_cast<int>(b.sx[t] >> (8 * quad));
     }
@@ -241,17 +258,20 @@ __device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int64_
       const int sa = past ? 127 : static_cast<int>(b.sa[i] >> (8 * quad));
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x[t], acc[i][t], 0, 0, 0, sa, 0, sx[t]);
+        acc[i][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, xx[t], acc[i][t], 0, 0, 0, sa, 0, sx[t]);
     }
   };
+  // a step is asked for before the last one is multiplied
   if (wave < steps) {
     Step b0, b1;
     load(b0, wave);
-    int64_t s = wave;
+    int s = wave;
     for (; s + WAVES < steps; s += 2 * WAVES) {
       load(b1, s + WAVES);
+      __builtin_amdgcn_sched_barrier(0);
       multiply(b0, s);
-      if (s + 2 * WAVES < steps) load(b0, s + 2 * WAVES);
+      load(b0, min(s + 2 * WAVES, steps - 1));
+      __builtin_amdgcn_sched_barrier(0);
       multiply(b1, s + WAVES);
     }
     if (s < steps) multiply(b0, s);
@@ -315,21 +335,28 @@ __device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int64_
   __syncthreads();  // the sums are read before the next rows' are written
 }
 
+// Up to 32 rows at a time; an expert with more has its weights read again. Bound by
+// memory: one token of a DeepSeek-V3-shaped layer (d = 7168, d_ff = 2048, 8 experts)
+// 40.5 us for gate and up (242 MB, 6.0 TB/s) and 23.5 for down, 64 tokens 1.03 ms
+// (6.7 GB, 6.6 TB/s) and 0.55. With eight waves a work-group gate and up took 42 us
+// and 1.06 ms (d_ff = 1408, 24 copies: 28 us instead of 21).
 template <bool GU, int NA, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(Mx8Gemm a, int strips) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass has no scaled matrix instruction
   __shared__ float red[WAVES * 2 * NA * 64 * 4];
   const int i = static_cast<int>(blockIdx.x / strips);
   if (i >= *a.ls.n_act) return;
-  const int e = a.ls.act[i];
-  const int64_t strip = blockIdx.x % strips;
-  const int end = a.ls.off[e + 1];
-  for (int r = a.ls.off[e]; r < end; r += 32) {
+  const int e = __builtin_amdgcn_readfirstlane(a.ls.act[i]);
+  const int strip = blockIdx.x % strips;
+  const int end = __builtin_amdgcn_readfirstlane(a.ls.off[e + 1]);
+  for (int r = __builtin_amdgcn_readfirstlane(a.ls.off[e]); r < end; r += 32) {
     const int n = min(end - r, 32);
     if (n <= 16)
       few_rows<GU, NA, 1, WAVES>(a, e, r, n, strip, red);
     else
       few_rows<GU, NA, 2, WAVES>(a, e, r, n, strip, red);
   }
+#endif
 }
 
 // out[t] = residual[t] + sum_j w y[t, j] over the kept copies, j ascending, in
@@ -397,15 +424,19 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   a.H = copies;
   a.y = nullptr;
   a.y_bf16 = L.bf16;
-  const bool many = copies > 64 * act;
+  // Row tiles from 28 rows an expert on, where both take the same time (d = 4096, d_ff = 14336, 8 experts with 32
+  // rows each: 527 us by strips, 541 by tiles; d = 2048, d_ff = 1408, 64 experts: 24 rows 167 and 238, 48 rows 304
+  // and 244). 16 columns of x where an expert has that few rows, else 32: with 16 alone the second case takes 267 us.
+  const bool many = copies > 28 * act;
   const int64_t tiles = copies / mx8_tile_rows() + act;
-  int strips = static_cast<int>(ceil_div(L.f, 32));
-  if (many) {
-    const hipError_t e = launch_mx8_tiles(a, true, L.E, tiles, s);
-    if (e != hipSuccess) return e;
-  } else {
-    few_rows_kernel<true, 4, 8><<<dim3(static_cast<unsigned>(act * strips)), dim3(512), 0, s>>>(a, strips);
-  }
+  auto few = [&](auto gu, const Mx8Gemm& g) {
+    constexpr bool GU = decltype(gu)::value;
+    const int strips = static_cast<int>(ceil_div(g.N, 32));
+    few_rows_kernel<GU, GU ? 4 : 2, 4><<<dim3(static_cast<unsigned>(act * strips)), dim3(256), 0, s>>>(g, strips);
+    return hipGetLastError();
+  };
+  hipError_t e = many ? launch_mx8_tiles(a, true, L.E, tiles, s) : few(std::true_type{}, a);
+  if (e != hipSuccess) return e;
   Mx8Gemm b = a;
   b.a0 = b.a1 = view(L.down);
   b.N = L.d;
@@ -413,13 +444,8 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   b.x = view(L.h);
   b.R = copies;
   b.y = L.y;
-  strips = static_cast<int>(ceil_div(L.d, 32));
-  if (many) {
-    const hipError_t e = launch_mx8_tiles(b, false, L.E, tiles, s);
-    if (e != hipSuccess) return e;
-  } else {
-    few_rows_kernel<false, 2, 4><<<dim3(static_cast<unsigned>(act * strips)), dim3(256), 0, s>>>(b, strips);
-  }
+  e = many ? launch_mx8_tiles(b, false, L.E, tiles, s) : few(std::false_type{}, b);
+  if (e != hipSuccess) return e;
   const int64_t V = L.d / (L.bf16 ? 8 : 4), blocks = ceil_div(V, 256);
   const dim3 grid(static_cast<unsigned>(L.T * blocks));
   const auto* rv = static_cast<const uint4*>(L.residual);
