@@ -13,6 +13,7 @@ with torch and calls moe_layer_forward once.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -50,6 +51,9 @@ class moe_stats_t(ctypes.Structure):
                 ("kept_count", ctypes.c_void_p), ("send_count", ctypes.c_void_p),
                 ("totals", ctypes.c_void_p), ("buckets", ctypes.c_void_p), ("instance", ctypes.c_void_p),
                 ("g", ctypes.c_void_p), ("u", ctypes.c_void_p), ("h", ctypes.c_void_p)]
+
+
+_STATS = frozenset(name for name, _ in moe_stats_t._fields_)
 
 
 class moe_q4_t(ctypes.Structure):
@@ -204,8 +208,9 @@ def _stats(stats) -> "ctypes.POINTER(moe_stats_t) | None":
     if stats is None:
         return None
     s = moe_stats_t()
-    for name, _ in moe_stats_t._fields_:
-        setattr(s, name, _ptr(stats.get(name)))
+    for name, t in stats.items():
+        if name in _STATS:
+            setattr(s, name, _ptr(t))
     return ctypes.pointer(s)
 
 
@@ -389,6 +394,7 @@ def moe_layer_forward_few_q4(x, W_router, router_bias, W_gate, W_up, W_down, T, 
            "moe_layer_forward_few_q4")
 
 
+@functools.lru_cache(maxsize=64)
 def _gate(gate) -> "ctypes.POINTER(moe_gate_t) | None":
     """gate: None or (score, groups, top_groups, group_best, renormalize, scale)."""
     if gate is None:
@@ -695,6 +701,10 @@ class _On:
         t.record_stream(self.current)
         return t
 
+    def zero(self, t):
+        with self.torch.cuda.stream(self.stream):
+            t.zero_()
+
     def lent(self, t):
         if self.other is not None and t is not None:
             of = ((t._codes, t._scale, t._zero) if isinstance(t, Q4Weights) else
@@ -703,6 +713,40 @@ class _On:
                 if v is not None:
                     v.record_stream(self.other)
         return t
+
+
+class _Here:
+    """_On for the usual call: on torch's current device and current stream, whose
+    address is all that is needed. (Making torch's stream and device objects
+    takes longer than a small kernel's launch.)"""
+    other = None
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        pass
+
+    def empty(self, shape, dtype):
+        import torch
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def lent(self, t):
+        return t
+
+    def zero(self, t):
+        t.zero_()
+
+
+def _on(device, stream):
+    """The device and stream of a call on tensors of `device`."""
+    import torch
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return _Here(device, torch._C._cuda_getCurrentRawStream(device.index))
+    return _On(device, stream)
 
 
 def _same_device(device, names, *tensors):
@@ -900,15 +944,13 @@ def gate(logits, k, score="softmax", bias=None, groups=1, top_groups=0, group_be
     dev = logits.device
     _same_device(dev, "bias", bias)
     key = ("gate", T, E, k, dev)
-    with _On(dev, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
             res = Result.of(key, topk_idx=on.empty((T, k), torch.int32), topk_w=on.empty((T, k), torch.float32))
         else:
             res = _lent_result(out, key, "gate")
-            for t in res._bound[1].values():
-                on.lent(t)
         if on.other is not None:
-            for t in (logits, bias):
+            for t in (*res._bound[1].values(), logits, bias):
                 on.lent(t)
         t = res._bound[1]
         moe_gate(logits, bias, rule, T, E, k, t["topk_idx"], t["topk_w"], on.stream)
@@ -934,7 +976,7 @@ def gate_backward(logits, topk_idx, d_topk_w, score="softmax", renormalize=True,
     rule = _gate_rule(score, 1, 1, 1, renormalize, scale)
     dev = logits.device
     _same_device(dev, "topk_idx d_topk_w d_scores out", topk_idx, d_topk_w, d_scores, out)
-    with _On(dev, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
             out = on.empty((T, E), torch.float32)
         else:
@@ -998,7 +1040,7 @@ def quantize_mx8(W, stream=None):
     dt = _dtype(W.dtype)
     E, N, K = shape if len(shape) == 3 else (1, *shape)
     moe_mx8_size(E, N, K)   # checks the sizes
-    with _On(W.device, stream) as on:
+    with _on(W.device, stream) as on:
         q = Mx8._empty(on, shape)
         moe_mx8_quantize(on.lent(W), E, N, K, dt, q, on.stream)
     return q
@@ -1009,7 +1051,7 @@ def dequantize_mx8(q, dtype, stream=None):
     import torch
     dt = _dtype(dtype)
     E, N, K = q.shape if len(q.shape) == 3 else (1, *q.shape)
-    with _On(q.device, stream) as on:
+    with _on(q.device, stream) as on:
         W = on.empty(q.shape, torch.bfloat16 if dt == MOE_DTYPE_BF16 else torch.float32)
         moe_mx8_dequantize(on.lent(q), E, N, K, dt, W, on.stream)
     return W
@@ -1033,21 +1075,19 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, want_y=True, mx8=False, out=None
     _require(weight, "weight", dt, (d,))
     if residual is not None:
         _require(residual, "residual", dt, (R, d))
-    if mx8:
+    if mx8 and out is None:
         moe_mx8_size(1, R, d)   # checks the sizes
     _same_device(dev, "weight residual", weight, residual)
     key = ("rmsnorm", R, d, dt, dev, residual is not None, bool(want_y), bool(mx8))
-    with _On(dev, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
             res = Result.of(key, h=on.empty((R, d), dt) if residual is not None else None,
                             y=on.empty((R, d), dt) if want_y else None, y8=Mx8._empty(on, (R, d)) if mx8 else None,
                             rstd=on.empty((R,), torch.float32))
         else:
             res = _lent_result(out, key, "rmsnorm")
-            for t in res._bound[1].values():
-                on.lent(t)
         if on.other is not None:
-            for t in (x, weight, residual):
+            for t in (*res._bound[1].values(), x, weight, residual):
                 on.lent(t)
         t = res._bound[1]
         moe_rmsnorm(x, residual, weight, eps, R, d, dtype, t["h"], t["y"], t["y8"], t["rstd"], on.stream)
@@ -1073,17 +1113,15 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, out=None, stream=None):
     _require(rstd, "rstd", torch.float32, (R,))
     _same_device(dev, "h weight rstd dh", h, weight, rstd, dh)
     key = ("rmsnorm_backward", R, d, dt, dev)
-    with _On(dev, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
             nbytes = moe_rmsnorm_backward_workspace_size(R, d, dtype)
             res = Result.of(key, dh=on.empty((R, d), dt), dweight=on.empty((d,), dt),
                             workspace=on.empty((max(nbytes, 1),), torch.uint8))
         else:
             res = _lent_result(out, key, "rmsnorm_backward")
-            for t in res._bound[1].values():
-                on.lent(t)
         if on.other is not None:
-            for t in (dy, h, weight, rstd, dh):
+            for t in (*res._bound[1].values(), dy, h, weight, rstd, dh):
                 on.lent(t)
         t = res._bound[1]
         moe_rmsnorm_backward(dy, h, weight, rstd, dh, R, d, dtype, t["dh"], t["dweight"], t["workspace"],
@@ -1118,25 +1156,22 @@ def experts_mx8(x, topk_idx, topk_w, W_gate, W_up, W_down, residual, cf, out=Non
     _require(topk_w, "topk_w", torch.float32, (T, k))
     _same_device(dev, "topk_idx topk_w W_gate W_up W_down residual", topk_idx, topk_w, W_gate, W_up, W_down, residual)
     key = ("experts_mx8", T, d, d_ff, E, k, cf, dt, dev)
-    with _On(dev, stream) as on:
+    with _on(dev, stream) as on:
         if out is None:
             nbytes = moe_experts_mx8_workspace_size(T, d, d_ff, E, k, cf, dtype)
             i32 = torch.int32
             res = Result.of(key, out=on.empty((T, d), dt), slot=on.empty((T, k), i32), routed_count=on.empty((E,), i32),
                             kept_count=on.empty((E,), i32), workspace=on.empty((max(nbytes, 1),), torch.uint8))
             if T == 0:   # nothing will be launched: the counts of no tokens
-                with torch.cuda.stream(on.stream):
-                    for name in ("routed_count", "kept_count"):
-                        res[name].zero_()
+                for name in ("routed_count", "kept_count"):
+                    on.zero(res[name])
         else:
             res = _lent_result(out, key, "experts_mx8")
-            for t in res._bound[1].values():
-                on.lent(t)
         if on.other is not None:
-            for t in (x, topk_idx, topk_w, W_gate, W_up, W_down, residual):
+            for t in (*res._bound[1].values(), x, topk_idx, topk_w, W_gate, W_up, W_down, residual):
                 on.lent(t)
         t = res._bound[1]
-        stats = {n: t[n] for n in ("slot", "routed_count", "kept_count")}
+        stats = {"slot": t["slot"], "routed_count": t["routed_count"], "kept_count": t["kept_count"]}
         moe_experts_mx8(x, residual, topk_idx, topk_w, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, dtype, t["out"], stats,
                         t["workspace"], t["workspace"].numel(), on.stream)
     return res

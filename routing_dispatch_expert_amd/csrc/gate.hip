@@ -35,16 +35,75 @@ __device__ inline V shfl_xor64(V v, int off) {
 
 __device__ inline double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-__device__ inline double wave_sum(double v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += shfl_xor64(v, off);
-  return v;
+// A word of the lane that many places below (or, from the last two, of the last
+// lane of the rows below); 0 where there is none. Register moves, without LDS: a
+// wave's reductions here are chains of them, and one through LDS takes ten times
+// as long.
+template <int CTRL, int ROWS>
+__device__ inline uint32_t below(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ inline double below(double v) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
+  return __longlong_as_double(static_cast<int64_t>(static_cast<uint64_t>(below<CTRL, ROWS>(static_cast<uint32_t>(u >> 32))) << 32 |
+                                                   below<CTRL, ROWS>(static_cast<uint32_t>(u))));
+}
+template <int CTRL, int ROWS>
+__device__ inline float below(float v) {
+  return __uint_as_float(below<CTRL, ROWS>(__float_as_uint(v)));
 }
 
-__device__ inline double wave_max(double v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmax(v, shfl_xor64(v, off));
-  return v;
+__device__ inline uint32_t lane_word(uint32_t v, int lane) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
+__device__ inline uint64_t lane_word(uint64_t v, int lane) {
+  return static_cast<uint64_t>(lane_word(static_cast<uint32_t>(v >> 32), lane)) << 32 | lane_word(static_cast<uint32_t>(v), lane);
+}
+__device__ inline double lane_word(double v, int lane) {
+  return __longlong_as_double(static_cast<int64_t>(lane_word(static_cast<uint64_t>(__double_as_longlong(v)), lane)));
+}
+__device__ inline float lane_word(float v, int lane) { return __uint_as_float(lane_word(__float_as_uint(v), lane)); }
+
+// Reductions over the wave, the same in every lane: shifts by 1, 2, 4, 8 within
+// rows of 16 lanes, then the rows' last lanes onto the rows above.
+template <typename V, typename F>
+__device__ inline V wave_reduce(V v, F f) {
+  v = f(v, below<0x111, 0xf>(v));
+  v = f(v, below<0x112, 0xf>(v));
+  v = f(v, below<0x114, 0xf>(v));
+  v = f(v, below<0x118, 0xf>(v));
+  v = f(v, below<0x142, 0xa>(v));
+  v = f(v, below<0x143, 0xc>(v));
+  return lane_word(v, 63);
+}
+// Maxima as integers in the numbers' order, of which 0 is below all.
+__device__ inline uint32_t wave_max(uint32_t v) {
+  return wave_reduce(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ inline uint64_t wave_max(uint64_t v) {
+  const uint32_t hi = static_cast<uint32_t>(v >> 32), top = wave_max(hi);
+  return static_cast<uint64_t>(top) << 32 | wave_max(hi == top ? static_cast<uint32_t>(v) : 0u);
+}
+template <typename V>
+__device__ inline V wave_sum(V v) {
+  return wave_reduce(v, [](V a, V b) { return a + b; });
+}
+// The same over lanes 0 .. k - 1, one after the other.
+__device__ inline double first_sum(double v, int k) {
+  double sum = 0;
+  for (int j = 0; j < k; ++j) sum += lane_word(v, j);
+  return sum;
+}
+__device__ inline double first_max(double v, int k) {
+  double m = -INFINITY;
+  for (int j = 0; j < k; ++j) m = fmax(m, lane_word(v, j));
+  return m;
+}
+
+// The order's inverse, for numbers.
+__device__ inline double number_of(uint64_t key) {
+  return __longlong_as_double(static_cast<int64_t>(key >> 63 ? key & ~(uint64_t{1} << 63) : ~key));
 }
 
 // Lanes that share a group's experts when its value is formed: 64 over the
@@ -73,8 +132,8 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
     top = l[0];
 #pragma unroll
     for (int i = 1; i < NE; ++i) top = fmax(top, l[i]);
-    top = wave_max(top);
-    if (top == -INFINITY) top = 0;  // every expert masked: all scores are 0
+    top = number_of(wave_max(order_of(top)));
+    if (!(top > -INFINITY)) top = 0;  // every expert masked: all scores are 0
     total = 0;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
@@ -127,7 +186,7 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
     const uint64_t value = order_of(g.best > 1 ? a + b : a);
     int ahead = 0;  // groups that are better, or as good and before this one
     for (int o = 0; o < g.groups; ++o) {
-      const uint64_t ov = __shfl(value, o * lpg, 64);
+      const uint64_t ov = lane_word(value, o * lpg);
       ahead += (ov > value || (ov == value && o < mine)) ? 1 : 0;
     }
     const uint64_t kept = __ballot(mine < g.groups && ahead < g.top_groups);
@@ -140,32 +199,34 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
   int my_e = 0;  // lane j < k: the j-th choice
   double my_l = 0;
   for (int j = 0; j < k; ++j) {
-    uint64_t best = 0;
+    uint64_t best = 0;  // of this lane's; a NaN's key is 0 too
     int be = INT_MAX;
     double bl = 0;
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (!((taken >> i) & 1) && (be == INT_MAX || key[i] > best)) {
-        best = key[i];
-        be = lane + 64 * i;
-        bl = l[i];
-      }
-    int win = lane;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-      const uint64_t ok = shfl_xor64(best, off);
-      const int oe = shfl_xor64(be, off), ow = shfl_xor64(win, off);
-      if (be == INT_MAX ? oe != INT_MAX : (oe != INT_MAX && (ok > best || (ok == best && oe < be)))) {
-        best = ok;
-        be = oe;
-        win = ow;
-      }
+    for (int i = 0; i < NE; ++i) {
+      const bool better = !((taken >> i) & 1) && (be == INT_MAX || key[i] > best);
+      best = better ? key[i] : best;
+      be = better ? lane + 64 * i : be;
+      bl = better ? l[i] : bl;
     }
-    bl = __shfl(bl, win, 64);
-    if (lane == be % 64) taken |= uint64_t{1} << (be / 64);
+    // two lanes' bests seldom share the upper half; of equal ones the lowest expert
+    const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
+    const uint32_t top_hi = wave_max(hi);
+    uint64_t like = __ballot(be != INT_MAX && hi == top_hi);
+    if (like & (like - 1)) {
+      const bool in = (like >> lane) & 1;
+      const uint32_t top_lo = wave_max(in ? lo : 0u);
+      const bool tie = in && lo == top_lo;
+      const uint32_t first = ~wave_max(tie ? ~static_cast<uint32_t>(be) : 0u);
+      like = __ballot(tie && static_cast<uint32_t>(be) == first);
+    }
+    const int win = __builtin_ctzll(like);
+    const int e = static_cast<int>(lane_word(static_cast<uint32_t>(be), win));
+    const double el = lane_word(bl, win);
+    if (lane == win) taken |= uint64_t{1} << (e / 64);
     if (lane == j) {
-      my_e = be;
-      my_l = bl;
+      my_e = e;
+      my_l = el;
     }
   }
   // weights of the chosen
@@ -174,13 +235,13 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
   if (g.sigmoid) {
     z = in ? sigmoid64(my_l) : 0;
   } else if (g.renormalize) {  // a softmax over the chosen
-    const double m = wave_max(in ? my_l : -INFINITY);
+    const double m = first_max(my_l, k);
     z = in && m > -INFINITY ? exp(my_l - m) : 0;
   } else {
     z = in ? exp(my_l - top) / total : 0;
   }
   if (g.renormalize) {
-    const double sum = wave_sum(z);
+    const double sum = first_sum(z, k);
     z = sum > 0 ? z / sum : 0;
   }
   if (in) {
@@ -228,12 +289,12 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const float* __restr
     if (g.sigmoid) {
       z = in ? sigmoid64(l_j) : 0;
     } else {
-      const double m = wave_max(in ? l_j : -INFINITY);
+      const double m = first_max(in ? l_j : -INFINITY, k);
       z = in && m > -INFINITY ? exp(l_j - m) : 0;
     }
-    const double sum = wave_sum(z);
+    const double sum = first_sum(z, k);
     const double r = sum > 0 ? z / sum : 0;
-    const double D = wave_sum(q_j * r);
+    const double D = first_sum(q_j * r, k);
     term = r * (q_j - D) * (g.sigmoid ? sigmoid64(-l_j) : 1.0);
   } else {
     term = g.sigmoid ? q_j * sigmoid64(l_j) * sigmoid64(-l_j) : q_j;
@@ -266,8 +327,9 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const float* __restr
       float m = l[0];
 #pragma unroll
       for (int i = 1; i < NE; ++i) m = fmaxf(m, l[i]);
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, shfl_xor64(m, off));
+      const uint32_t mu = __float_as_uint(m + 0.f);
+      const uint32_t mk = wave_max(mu >> 31 ? ~mu : mu | 0x80000000u);
+      m = __uint_as_float(mk >> 31 ? mk & 0x7fffffffu : ~mk);
       float p[NE], sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
@@ -275,11 +337,8 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const float* __restr
         sum += p[i];
         dot += p[i] * ds[i];
       }
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) {
-        sum += shfl_xor64(sum, off);
-        dot += shfl_xor64(dot, off);
-      }
+      sum = wave_sum(sum);
+      dot = wave_sum(dot);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
       dot *= inv;
 #pragma unroll
