@@ -59,9 +59,10 @@ struct ExpertsMx8 {
   int E, k;
   bool bf16;       // residual, y and out
   void* out;
-  int32_t *slot, *routed, *kept;  // routed and kept may be NULL
+  int32_t *slot, *routed, *kept;
   // workspace
   ExpertLists ls;
+  int32_t *tile_cnt, *tile_off;  // [ceil(T / kTileTokens)][E]
   Mx8Ptr h;        // rows [T k][f]
   void* y;         // [T k][d]
 };

@@ -1503,7 +1503,7 @@ namespace {
 struct ExpertsPlan {
   moe::ExpertLists ls;
   moe::Mx8Ptr h;
-  int32_t* slot;
+  int32_t *slot, *routed, *kept, *tile_cnt, *tile_off;
   void* y;
   size_t bytes;
 };
@@ -1518,6 +1518,11 @@ ExpertsPlan plan_experts_mx8(void* ws, int64_t T, int64_t d, int64_t d_ff, int32
   p.ls.act = c.take<int32_t>(std::min<size_t>(E, n));
   p.ls.copy = c.take<int32_t>(n);
   p.slot = c.take<int32_t>(n);
+  p.routed = c.take<int32_t>(E);
+  p.kept = c.take<int32_t>(E);
+  const size_t counts = static_cast<size_t>(moe::ceil_div(T, moe::kTileTokens)) * E;
+  p.tile_cnt = c.take<int32_t>(counts);
+  p.tile_off = c.take<int32_t>(counts);
   p.h.codes = c.take<uint8_t>(n * d_ff);
   p.h.scale = c.take<uint32_t>(mx8_scale_bytes(1, n, d_ff) / 4);
   p.y = c.take<char>(n * d * eb);
@@ -1597,9 +1602,11 @@ int moe_experts_mx8(const moe_mx8_t* x, const void* residual, const int32_t* top
   L.bf16 = dtype == MOE_DTYPE_BF16;
   L.out = out;
   L.slot = pick(S.slot, p.slot);
-  L.routed = S.routed_count;
-  L.kept = S.kept_count;
+  L.routed = pick(S.routed_count, p.routed);
+  L.kept = pick(S.kept_count, p.kept);
   L.ls = p.ls;
+  L.tile_cnt = p.tile_cnt;
+  L.tile_off = p.tile_off;
   L.h = p.h;
   L.y = p.y;
   MOE_HIP_TRY(moe::launch_experts_mx8(L, static_cast<hipStream_t>(stream)), "8-bit experts");

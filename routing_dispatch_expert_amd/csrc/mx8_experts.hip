@@ -36,6 +36,9 @@ namespace {
 // expert's running count: token order, nothing depends on arrival.
 // ---------------------------------------------------------------------------
 constexpr int kPlanCounts = 16384;  // counts of a round's waves: waves * E
+// With more copies the layer's own launches, 24 us for any number of them, replace
+// the one work-group (8192 copies: 23 - 27 us; 16384 53, 98304 272).
+constexpr int64_t kPlanCopies = 8192;
 
 // Exclusive prefix sum over the block's 1024 values; the total goes to *total.
 __device__ inline int block_prefix(int v, int* sums, int* total) {
@@ -57,6 +60,40 @@ __device__ inline int block_prefix(int v, int* sums, int* total) {
   }
   *total = all;
   return before + s - v;
+}
+
+// Rows, row tiles of bt rows and places among the experts that have rows, as prefix
+// sums over the experts' counts by one work-group; count [E] becomes the experts'
+// first rows.
+__device__ inline void list_experts(int32_t* count, int E, int64_t C, int bt, int32_t* routed, int32_t* kept,
+                                    const ExpertLists& ls, int* sums) {
+  const int tid = threadIdx.x;
+  int rows0 = 0, tiles0 = 0, act0 = 0;
+  for (int e0 = 0; e0 < E; e0 += 1024) {
+    const int e = e0 + tid;
+    const int all = e < E ? count[e] : 0;
+    const int mine = static_cast<int>(min(static_cast<int64_t>(all), C));
+    int rows, tiles, act;
+    const int at = rows0 + block_prefix(mine, sums, &rows);
+    const int tile = tiles0 + block_prefix((mine + bt - 1) / bt, sums, &tiles);
+    const int place = act0 + block_prefix(mine > 0 ? 1 : 0, sums, &act);
+    if (e < E) {
+      if (routed) routed[e] = all;
+      if (kept) kept[e] = mine;
+      count[e] = at;
+      ls.off[e] = at;
+      ls.tile[e] = tile;
+      if (mine > 0) ls.act[place] = e;
+    }
+    rows0 += rows;
+    tiles0 += tiles;
+    act0 += act;
+  }
+  if (tid == 0) {
+    ls.off[E] = rows0;
+    ls.tile[E] = tiles0;
+    *ls.n_act = act0;
+  }
 }
 
 __global__ __launch_bounds__(1024) void experts_plan_kernel(const int32_t* __restrict__ idx, int64_t T, int k, int E,
@@ -108,33 +145,7 @@ __global__ __launch_bounds__(1024) void experts_plan_kernel(const int32_t* __res
     }
     __syncthreads();
   }
-  // rows, row tiles and places among the experts that have rows, as prefix sums over the experts
-  int rows0 = 0, tiles0 = 0, act0 = 0;
-  for (int e0 = 0; e0 < E; e0 += 1024) {
-    const int e = e0 + tid;
-    const int all = e < E ? cnt[e] : 0;
-    const int mine = static_cast<int>(min(static_cast<int64_t>(all), C));
-    int rows, tiles, act;
-    const int at = rows0 + block_prefix(mine, sums, &rows);
-    const int tile = tiles0 + block_prefix((mine + bt - 1) / bt, sums, &tiles);
-    const int place = act0 + block_prefix(mine > 0 ? 1 : 0, sums, &act);
-    if (e < E) {
-      if (routed) routed[e] = all;
-      if (kept) kept[e] = mine;
-      cnt[e] = at;
-      ls.off[e] = at;
-      ls.tile[e] = tile;
-      if (mine > 0) ls.act[place] = e;
-    }
-    rows0 += rows;
-    tiles0 += tiles;
-    act0 += act;
-  }
-  if (tid == 0) {
-    ls.off[E] = rows0;
-    ls.tile[E] = tiles0;
-    *ls.n_act = act0;
-  }
+  list_experts(cnt, E, C, bt, routed, kept, ls, sums);
   __syncthreads();
   // every thread places the copies whose slots it wrote
   for (int64_t c0 = 0; c0 < n; c0 += 64 * W) {
@@ -144,6 +155,24 @@ __global__ __launch_bounds__(1024) void experts_plan_kernel(const int32_t* __res
       if (s >= 0) ls.copy[cnt[idx[i]] + s] = static_cast<int32_t>(i);
     }
   }
+}
+
+// The same for many copies, after the layer's histogram, scan and slots over tiles of
+// tokens: the experts' lists from the kept counts, then the copies' places.
+__global__ __launch_bounds__(1024) void list_experts_kernel(int32_t* kept, int E, int64_t C, int bt, ExpertLists ls) {
+  __shared__ int cnt[4096];
+  __shared__ int sums[16];
+  for (int e = threadIdx.x; e < E; e += 1024) cnt[e] = kept[e];
+  __syncthreads();
+  list_experts(cnt, E, C, bt, nullptr, nullptr, ls, sums);
+}
+
+__global__ __launch_bounds__(256) void place_copies_kernel(const int32_t* __restrict__ idx,
+                                                           const int32_t* __restrict__ slot, int64_t n, ExpertLists ls) {
+  const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+  if (i >= n) return;
+  const int s = slot[i];
+  if (s >= 0) ls.copy[ls.off[idx[i]] + s] = static_cast<int32_t>(i);
 }
 
 // ---------------------------------------------------------------------------
@@ -408,8 +437,20 @@ Mx8 view(const Mx8Ptr& p) { return {p.codes, p.scale}; }
 }  // namespace
 
 hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
-  experts_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.idx, L.T, L.k, L.E, L.C, mx8_tile_rows(), L.slot, L.routed, L.kept, L.ls);
   const int64_t copies = L.T * L.k, act = std::min<int64_t>(L.E, copies);
+  hipError_t e = hipSuccess;
+  if (copies <= kPlanCopies) {
+    experts_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.idx, L.T, L.k, L.E, L.C, mx8_tile_rows(), L.slot, L.routed, L.kept, L.ls);
+  } else {
+    if ((e = launch_tile_hist(L.idx, L.T, L.k, L.E, L.tile_cnt, s, L.slot)) != hipSuccess ||
+        (e = launch_scan(L.tile_cnt, ceil_div(L.T, kTileTokens), L.E, L.C, 1, 0, L.k, L.T, L.tile_off, L.routed, L.kept,
+                         nullptr, nullptr, 0, nullptr, nullptr, s)) != hipSuccess ||
+        (e = launch_slots_from_ranks(L.idx, L.slot, L.tile_off, L.T, L.k, L.E, L.C, nullptr, nullptr, s)) != hipSuccess)
+      return e;
+    list_experts_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.kept, L.E, L.C, mx8_tile_rows(), L.ls);
+    place_copies_kernel<<<dim3(static_cast<unsigned>(ceil_div(copies, 256))), dim3(256), 0, s>>>(L.idx, L.slot, copies, L.ls);
+  }
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   Mx8Gemm a;
   a.a0 = view(L.gate);
   a.a1 = view(L.up);
@@ -435,7 +476,7 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
     few_rows_kernel<GU, GU ? 4 : 2, 4><<<dim3(static_cast<unsigned>(act * strips)), dim3(256), 0, s>>>(g, strips);
     return hipGetLastError();
   };
-  hipError_t e = many ? launch_mx8_tiles(a, true, L.E, tiles, s) : few(std::true_type{}, a);
+  e = many ? launch_mx8_tiles(a, true, L.E, tiles, s) : few(std::true_type{}, a);
   if (e != hipSuccess) return e;
   Mx8Gemm b = a;
   b.a0 = b.a1 = view(L.down);

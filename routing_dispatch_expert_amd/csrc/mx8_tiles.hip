@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 namespace moe {
 namespace {
@@ -30,6 +31,25 @@ __device__ inline __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
 
 // s_waitcnt: everything of this wave's loads, and its LDS reads.
 __device__ inline __attribute__((unused)) void wait_all() { __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (0 << 8)); }
+
+// A stage half's schedule: NM products with NR reads of LDS and NV loads spread
+// among them. Left to itself the compiler reads an operand right before its
+// product and waits.
+template <int I, int NM, int NR, int NV>
+__device__ inline void interleave_one() {
+  constexpr int R = NR * (I + 1) / NM - NR * I / NM, V = NV * (I + 1) / NM - NV * I / NM;
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  if constexpr (R > 0) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+  if constexpr (V > 0) __builtin_amdgcn_sched_group_barrier(0x020, V, 0);
+}
+template <int NM, int NR, int NV, int... I>
+__device__ inline void interleave_all(std::integer_sequence<int, I...>) {
+  (interleave_one<I, NM, NR, NV>(), ...);
+}
+template <int NM, int NR, int NV>
+__device__ inline void interleave() {
+  interleave_all<NM, NR, NV>(std::make_integer_sequence<int, NM>{});
+}
 
 constexpr int kFeatureGroup = 8;  // feature tiles that go through an expert's row tiles together (shared in L2)
 
@@ -91,32 +111,27 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   const int wm = wave / WN, wn = wave % WN, lr = lane & 31, lq = lane >> 5;
   const int64_t K = a.K, N = a.N, steps = ceil_div(K, 128);
 
-  // row r of the block's A operand: feature and matrix
-  auto feature = [&](int r) {
-    const int w = r / (TM * 32), i = r / 32 % TM, in = r & 31;
-    return min(n0 + w * FW + (GU ? i % (TM / 2) : i) * 32 + in, N - 1);  // past the matrix: the last one again
-  };
+  // Row r of the block's A operand is this feature of this matrix. Rows past the matrix read as zeros, with some other
+  // row's scales: what becomes of their features is not stored.
+  auto feature = [&](int r) { return n0 + r / (TM * 32) * FW + (GU ? r / 32 % TM % (TM / 2) : r / 32 % TM) * 32 + (r & 31); };
   auto is_up = [&](int r) { return GU && r / 32 % TM >= TM / 2; };
   const int64_t span = N * K;
   const auto ra0 = rsrc(a.a0.codes + e * span, span), ra1 = rsrc(a.a1.codes + e * span, span);
-  // GU reads the tokens' rows (all of x), else the lists' rows from the expert's first
+  // GU reads the tokens' rows (all of x), else the lists' rows from the tile's first
   const int64_t xbase = GU ? 0 : first, xrows = GU ? a.R : rows;
   const auto rx = rsrc(a.x.codes + xbase * K, xrows * K);
   auto x_row = [&](int r) {
     const int at = first + min(r, rows - 1);  // past the last row: it again
     return GU ? static_cast<int64_t>(a.ls.copy[at] / a.k) : static_cast<int64_t>(at);
   };
-  uint32_t va[PA], vx[PX];
+  // the piece at this lane's position of the 8 rows of an even or odd DMA instruction, in bytes of the row's 128
+  const int piece[2] = {16 * ((lane & 7) ^ (lane >> 4)), 16 * ((lane & 7) ^ (4 + (lane >> 4)))};
+  const uint32_t va = static_cast<uint32_t>((lane >> 3) * K);
+  uint32_t vx[PX];
 #pragma unroll
-  for (int i = 0; i < PA; ++i) {
-    const int r = (wave * PA + i) * 8 + (lane >> 3);
-    va[i] = static_cast<uint32_t>(feature(r) * K + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
-  }
-#pragma unroll
-  for (int i = 0; i < PX; ++i) {
-    const int r = (wave * PX + i) * 8 + (lane >> 3);
-    vx[i] = static_cast<uint32_t>((x_row(r) - xbase) * K + 16 * ((lane & 7) ^ ((r >> 1) & 7)));
-  }
+  for (int i = 0; i < PX; ++i)
+    vx[i] = static_cast<uint32_t>((x_row((wave * PX + i) * 8 + (lane >> 3)) - xbase) * K + piece[i & 1]);
+  static_assert(PA % 2 == 0 && PX % 2 == 0, "a wave's DMA instructions begin with an even one");
   // the scales: rows 64 (PS wave + i) + lane of A's (of one matrix: TM % 4 == 0), then of x's
   static_assert(!GU || TM % 4 == 0, "64 rows of A are of one matrix");
   const int64_t sbytes = steps * N * 4;
@@ -130,20 +145,19 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   }
   auto dma = [&](uint4* as, uint4* xs, uint32_t* sc, int64_t s) {
     const int k0 = static_cast<int>(s * 128);
-    const bool tail = k0 + 128 > K;  // pieces past the last column: zero (an offset past the buffer)
+    // pieces past the last column: zero (an offset past the buffer)
+    const bool in[2] = {k0 + piece[0] < K, k0 + piece[1] < K};
+    const uint32_t v[2] = {in[0] ? va + piece[0] : 0x80000000u, in[1] ? va + piece[1] : 0x80000000u};
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
       const int r = (wave * PA + i) * 8;
-      uint32_t v = va[i];
-      if (tail && k0 + 16 * ((lane & 7) ^ (((r + (lane >> 3)) >> 1) & 7)) >= K) v = 0x80000000u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_up(r) ? ra1 : ra0, MOE_LDS(as + r * 8), 16, v, k0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_up(r) ? ra1 : ra0, MOE_LDS(as + r * 8), 16, v[i & 1],
+                                               static_cast<int>(feature(r) * K) + k0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < PX; ++i) {
       const int r = (wave * PX + i) * 8;
-      uint32_t v = vx[i];
-      if (tail && k0 + 16 * ((lane & 7) ^ (((r + (lane >> 3)) >> 1) & 7)) >= K) v = 0x80000000u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MOE_LDS(xs + r * 8), 16, v, k0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, MOE_LDS(xs + r * 8), 16, in[i & 1] ? vx[i] : 0x80000000u, k0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < PS; ++i) {
@@ -183,16 +197,26 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
         for (int j = 0; j < TX; ++j) fx[slot][j] = read(xs, (wn * TN + j) * 32 + lr, h);
       }
     };
-    // byte 0 of a scale operand is that of the first 64 columns' block lq, byte 2 of the second's
-    auto sload = [&](const uint32_t* sc, int64_t s) {
+    // the stage's scales as they lie, and made ready: byte 0 of an operand is that of the first 64 columns' block lq,
+    // byte 2 of the second's
+    uint32_t ra[TM], rx_[TN];
+    auto sload = [&](const uint32_t* sc) {
+      if constexpr (TX > 0) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) ra[i] = sc[(wm * TM + i) * 32 + lr];
+#pragma unroll
+        for (int j = 0; j < TX; ++j) rx_[j] = sc[MA + (wn * TN + j) * 32 + lr];
+      }
+    };
+    auto sready = [&](int64_t s) {
       if constexpr (TX > 0) {
         const int64_t groups = ceil_div(K - s * 128, 32);  // with columns; bytes past them may be anything
         const uint32_t mask = groups >= 4 ? ~0u : (1u << (8 * groups)) - 1;
         auto fix = [&](uint32_t v) { return ((v & mask) | (0x7f7f7f7fu & ~mask)) >> (8 * lq); };
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] = fix(sc[(wm * TM + i) * 32 + lr]);
+        for (int i = 0; i < TM; ++i) sa[i] = fix(ra[i]);
 #pragma unroll
-        for (int j = 0; j < TX; ++j) sx[j] = fix(sc[MA + (wn * TN + j) * 32 + lr]);
+        for (int j = 0; j < TX; ++j) sx[j] = fix(rx_[j]);
       }
     };
     auto multiply = [&](auto half) {
@@ -211,8 +235,10 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
     // compiler keep the accumulators twice.
     auto stage = [&](auto next, auto next2, uint4* as, uint4* xs, uint32_t* sc, uint4* an, uint4* xn, uint32_t* sn,
                      int64_t s) {
+      constexpr int READS = 2 * (TM + TX), PRODUCTS = TM * TX;
       fload(as, xs, 1, 1);
       multiply(Half0{});
+      if constexpr (TX > 0) interleave<PRODUCTS, READS, 0>();
       if constexpr (decltype(next)::value) {
         __builtin_amdgcn_sched_barrier(0);
         wait_all();                    // own share of stage s + 1 landed, reads of stage s done ...
@@ -220,9 +246,12 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (decltype(next2)::value) dma(as, xs, sc, s + 2);
         fload(an, xn, 0, 0);
+        sload(sn);
       }
       multiply(Half1{});
-      if constexpr (decltype(next)::value) sload(sn, s + 1);
+      if constexpr (TX > 0 && decltype(next)::value)
+        interleave<PRODUCTS, READS + TM + TX, decltype(next2)::value ? PA + PX + PS : 0>();
+      if constexpr (decltype(next)::value) sready(s + 1);
     };
     using Yes = std::true_type;
     using No = std::false_type;
@@ -232,7 +261,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
       wait_all();
       __builtin_amdgcn_s_barrier();
       fload(As0, Xs0, 0, 0);
-      sload(Sc0, 0);
+      sload(Sc0);
+      sready(0);
       stage(No{}, No{}, As0, Xs0, Sc0, As1, Xs1, Sc1, 0);
       wait_all();
       __builtin_amdgcn_s_barrier();
@@ -243,7 +273,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
       __builtin_amdgcn_s_barrier();
       dma(As1, Xs1, Sc1, s + 1);
       fload(As0, Xs0, 0, 0);
-      sload(Sc0, s);
+      sload(Sc0);
+      sready(s);
       for (; s + 2 < steps; s += 2) {
         stage(Yes{}, Yes{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
         stage(Yes{}, Yes{}, As1, Xs1, Sc1, As0, Xs0, Sc0, s + 1);

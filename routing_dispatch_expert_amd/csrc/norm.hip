@@ -144,9 +144,9 @@ __global__ __launch_bounds__(THR > 256 ? THR : 256) void rmsnorm_kernel(
   }
 }
 
-// Gradient of rows blockIdx, blockIdx + gridDim, ...; a block's (THR = 64: a
-// wave's) sum of dweight's terms stays in registers and becomes row `part` of
-// parts [shares][d].
+// Gradient of the rows that the block (THR = 64: each of its four waves) takes in
+// turn; its sum of dweight's terms stays in registers until the end and becomes a
+// row of parts [gridDim][d]. 8192 x 4096 bf16 with dh_in: 45 us (268 MB, 6 TB/s; with 1024 blocks 50).
 template <bool BF16, int THR, int U>
 __global__ __launch_bounds__(THR > 256 ? THR : 256) void rmsnorm_backward_kernel(
     const uint4* dy, const uint4* h, const uint4* __restrict__ weight, const float* __restrict__ rstd,
@@ -209,32 +209,63 @@ __global__ __launch_bounds__(THR > 256 ? THR : 256) void rmsnorm_backward_kernel
       store_stream(dh + r * V + v, pack<BF16>(o));
     }
   }
+  if constexpr (THR == 64) {  // the waves' sums, in their order, as one row
+    __shared__ float4 sums[4][U * P / 4][64];
+    const int wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < P; i += 4)
+        sums[wave][(u * P + i) / 4][tid] = float4{dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]};
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < P; i += 4) {
+          const float4 o = sums[w][(u * P + i) / 4][tid];
+          dw[u][i] += o.x;
+          dw[u][i + 1] += o.y;
+          dw[u][i + 2] += o.z;
+          dw[u][i + 3] += o.w;
+        }
+  }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t v = tid + THR * u;
     if (v >= V) continue;
 #pragma unroll
     for (int i = 0; i < P; i += 4)
-      *reinterpret_cast<float4*>(parts + part * d + v * P + i) = float4{dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]};
+      *reinterpret_cast<float4*>(parts + blockIdx.x * d + v * P + i) = float4{dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]};
   }
 }
 
-// dweight = the parts' sums, 16 slices of the parts side by side.
+// dweight = the parts' sums: a block has 32 columns, 32 slices of the parts side by
+// side, each with eight loads on their way (one at a time, over 64 columns and 16
+// slices, 1024 x 4096 parts took 17 us).
 template <bool BF16>
 __global__ __launch_bounds__(1024) void dweight_kernel(const float* __restrict__ parts, int64_t shares, int64_t d,
                                                        void* __restrict__ out) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
-  const int64_t c = blockIdx.x * 64ll + lane;
+  __shared__ float red[32][32];
+  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int64_t c = blockIdx.x * 32ll + col;
   float sum = 0.f;
   if (c < d)
-    for (int64_t p = slice; p < shares; p += 16) sum += parts[p * d + c];
-  red[slice][lane] = sum;
+    for (int64_t p0 = slice; p0 < shares; p0 += 32 * 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = p0 + 32 * i < shares ? parts[(p0 + 32 * i) * d + c] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i];
+    }
+  red[slice][col] = sum;
   __syncthreads();
   if (slice || c >= d) return;
   sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sum += red[i][lane];
+  for (int i = 0; i < 32; ++i) sum += red[i][col];
   if (BF16)
     static_cast<bf16_t*>(out)[c] = f32_to_bf16(sum);
   else
@@ -292,12 +323,12 @@ hipError_t launch_rmsnorm(const void* x, const void* residual, const void* weigh
   return ok ? hipGetLastError() : hipErrorInvalidValue;
 }
 
-// Blocks' (waves') partial sums of dweight: by the sizes alone, so that results do
-// not depend on the card's state.
+// Blocks, and with them partial sums of dweight: by the sizes alone, so that
+// results do not depend on the card's state.
 int64_t rmsnorm_shares(int64_t R, int64_t d, bool bf16) {
   const int64_t V = d / (bf16 ? 8 : 4);
-  if (V <= 256) return ceil_div(std::min<int64_t>(R, 2048), 4) * 4;
-  return std::min<int64_t>(R, V <= 2048 ? 1024 : 256);
+  if (V <= 256) return std::min<int64_t>(ceil_div(R, 4), 512);
+  return std::min<int64_t>(R, V <= 2048 ? 512 : 256);
 }
 
 hipError_t launch_rmsnorm_backward(const void* dy, const void* h, const void* weight, const float* rstd,
@@ -311,7 +342,7 @@ hipError_t launch_rmsnorm_backward(const void* dy, const void* h, const void* we
   auto* ov = static_cast<uint4*>(dh);
   const bool ok = R == 0 || norm_shape(V, [&](auto thr, auto u) {
     constexpr int T = decltype(thr)::value, U = decltype(u)::value;
-    const dim3 grid(static_cast<unsigned>(T == 64 ? shares / 4 : shares));
+    const dim3 grid(static_cast<unsigned>(shares));
     if (bf16)
       rmsnorm_backward_kernel<true, T, U><<<grid, dim3(T == 64 ? 256 : T), 0, s>>>(gv, hv, wv, rstd, rv, R, d, ov, parts);
     else
@@ -320,7 +351,7 @@ hipError_t launch_rmsnorm_backward(const void* dy, const void* h, const void* we
   if (!ok) return hipErrorInvalidValue;
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(ceil_div(d, 64)));
+  const dim3 grid(static_cast<unsigned>(ceil_div(d, 32)));
   if (bf16)
     dweight_kernel<true><<<grid, dim3(1024), 0, s>>>(parts, shares, d, dweight);
   else
