@@ -1175,3 +1175,71 @@ def experts_mx8(x, topk_idx, topk_w, W_gate, W_up, W_down, residual, cf, out=Non
         moe_experts_mx8(x, residual, topk_idx, topk_w, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, dtype, t["out"], stats,
                         t["workspace"], t["workspace"].numel(), on.stream)
     return res
+
+
+def forward_mx8(x, norm_weight, W_router, W_gate, W_up, W_down, k, cf, residual=None, eps=1e-6, score="softmax", bias=None,
+                groups=1, top_groups=0, group_best=1, renormalize=True, scale=1.0, out=None, stream=None):
+    """The layer as it stands in a transformer block, with 8-bit experts, for rows
+    x [T, d] (bf16 or fp32):
+      h = x + residual;  y = rmsnorm(h) norm_weight, also in 8 bits
+      topk_idx, topk_w = gate(y W_router^T)        (score .. scale as for gate())
+      out = h + the experts' outputs for the 8-bit y (as experts_mx8())
+    W_router [E, d] and norm_weight [d] of x's dtype, W_gate, W_up, W_down an Mx8
+    each. Returns a dict out, h (x without a residual), y, logits, topk_idx, topk_w,
+    slot, routed_count, kept_count. out: the result of an earlier call with the same
+    sizes, whose tensors and workspaces this call writes. Runs on torch's current
+    stream unless one is given."""
+    import torch
+    for q, n in ((W_gate, "W_gate"), (W_up, "W_up"), (W_down, "W_down")):
+        if not isinstance(q, Mx8) or len(q.shape) != 3:
+            raise ValueError(f"{n}: need an Mx8 of 3 dimensions")
+    if x.dim() != 2:
+        raise ValueError(f"x: need [T, d], got {tuple(x.shape)}")
+    T, d = x.shape
+    E, d_ff = W_gate.shape[:2]
+    dt, dev = x.dtype, x.device
+    dtype = _dtype(dt)
+    for q, n, s in ((W_gate, "W_gate", (E, d_ff, d)), (W_up, "W_up", (E, d_ff, d)), (W_down, "W_down", (E, d, d_ff))):
+        if q.shape != s:
+            raise ValueError(f"{n}: need 8-bit weights of shape {s}, got {q.shape}")
+    _require(x, "x", dt, (T, d))
+    _require(norm_weight, "norm_weight", dt, (d,))
+    _require(W_router, "W_router", dt, (E, d))
+    if residual is not None:
+        _require(residual, "residual", dt, (T, d))
+    if bias is not None:
+        _require(bias, "bias", torch.float32, (E,))
+    rule = _gate_rule(score, groups, top_groups, group_best, renormalize, scale)
+    _same_device(dev, "norm_weight W_router W_gate W_up W_down residual bias", norm_weight, W_router, W_gate, W_up, W_down,
+                 residual, bias)
+    key = ("forward_mx8", T, d, d_ff, E, k, cf, dt, dev, residual is not None)
+    with _on(dev, stream) as on:
+        if out is None:
+            nbytes = moe_experts_mx8_workspace_size(T, d, d_ff, E, k, cf, dtype)
+            rbytes = moe_router_workspace_size(T, d, E, dtype)
+            i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+            res = Result.of(key, out=on.empty((T, d), dt), h=on.empty((T, d), dt) if residual is not None else None,
+                            y=on.empty((T, d), dt), y8=Mx8._empty(on, (T, d)), logits=on.empty((T, E), f32),
+                            top=on.empty((2, max(T, 1)), i32), topk_idx=on.empty((T, k), i32), topk_w=on.empty((T, k), f32),
+                            slot=on.empty((T, k), i32), routed_count=on.empty((E,), i32), kept_count=on.empty((E,), i32),
+                            router_workspace=on.empty((max(rbytes, 1),), u8), workspace=on.empty((max(nbytes, 1),), u8))
+            if T == 0:   # nothing will be launched: the counts of no tokens
+                for name in ("routed_count", "kept_count"):
+                    on.zero(res[name])
+        else:
+            res = _lent_result(out, key, "forward_mx8")
+        t = res._bound[1]
+        if on.other is not None:
+            for v in (*t.values(), x, norm_weight, W_router, W_gate, W_up, W_down, residual, bias):
+                on.lent(v)
+        h = x if residual is None else t["h"]
+        moe_rmsnorm(x, residual, norm_weight, eps, T, d, dtype, t["h"], t["y"], t["y8"], None, on.stream)
+        if T:   # the scores, with one best expert a token that nothing reads
+            moe_router(t["y"], W_router, None, T, d, E, 1, 1, 0, dtype, t["top"][0], t["top"][1], t["logits"],
+                       t["router_workspace"], t["router_workspace"].numel(), on.stream)
+        moe_gate(t["logits"], bias, rule, T, E, k, t["topk_idx"], t["topk_w"], on.stream)
+        stats = {"slot": t["slot"], "routed_count": t["routed_count"], "kept_count": t["kept_count"]}
+        moe_experts_mx8(t["y8"], h, t["topk_idx"], t["topk_w"], W_gate, W_up, W_down, T, d, d_ff, E, k, cf, dtype, t["out"],
+                        stats, t["workspace"], t["workspace"].numel(), on.stream)
+    res["h"] = h
+    return res
