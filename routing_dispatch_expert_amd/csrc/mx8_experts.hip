@@ -186,7 +186,8 @@ __global__ __launch_bounds__(256) void place_copies_kernel(const int32_t* __rest
 // instruction, and rotated into place (operands()).
 // ---------------------------------------------------------------------------
 // A range of memory for loads at an offset that is the same for all lanes plus a
-// lane's own; a lane past the end gets 0 and touches nothing.
+// lane's own. A lane whose own offset is past the end gets 0 and touches nothing;
+// the common offset is not checked, so what it adds must stay in the range.
 struct Range {
   const void* base;
   uint32_t bytes;
@@ -218,14 +219,14 @@ __device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int st
   const int quad = lane >> 4, half = (lane >> 3) & 1, col = lane & 15;
   const int K = static_cast<int>(a.K), N = static_cast<int>(a.N), steps = (K + 127) / 128, n0 = strip * 16 * FT;
   const uint32_t span = static_cast<uint32_t>(N) * K, sspan = static_cast<uint32_t>(steps) * N * 4;
-  // Rows past the matrix read as zeros, with some other row's scales: what becomes of their features is not stored.
+  // Rows past the matrix are its last ones again (N is a multiple of 16): what becomes of their features is not stored.
   const Range w0 = {a.a0.codes + static_cast<int64_t>(e) * span, span}, w1 = {a.a1.codes + static_cast<int64_t>(e) * span, span};
   const Range s0 = {a.a0.scale + static_cast<int64_t>(e) * steps * N, sspan}, s1 = {a.a1.scale + static_cast<int64_t>(e) * steps * N, sspan};
   // x's rows: the tokens' (of all) with GU, else the lists' from row0 on
   const int64_t xbase = GU ? 0 : row0;
   const Range x = {a.x.codes + xbase * K, static_cast<uint32_t>((GU ? a.R : n) * K)};
   const Range xs = {a.x.scale, static_cast<uint32_t>(steps * a.R * 4)};
-  const uint32_t wv = static_cast<uint32_t>(n0 + (lane & 7)) * K + 16 * (quad + 4 * half), sv = 4 * (n0 + col);
+  const uint32_t wv = static_cast<uint32_t>(lane & 7) * K + 16 * (quad + 4 * half), sv = 4 * col;
   uint32_t xv[NT], xsv[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -247,11 +248,12 @@ __device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int st
     const uint32_t ca = tail && k0 + 16 * (quad + 4 * half) >= static_cast<uint32_t>(K) ? kNowhere : wv;
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-      const uint32_t at = k0 + 16 * (i % FT) * K;
+      const int row = min(n0 + 16 * (i % FT), N - 16);
+      const uint32_t at = static_cast<uint32_t>(row) * K + k0;
       const Range& w = GU && i >= FT ? w1 : w0;
       b.lo[i] = w.load16<true>(ca, at);
       b.hi[i] = w.load16<true>(ca, at + 8 * K);
-      b.sa[i] = (GU && i >= FT ? s1 : s0).load4(sv, 4 * (s * N + 16 * (i % FT)));
+      b.sa[i] = (GU && i >= FT ? s1 : s0).load4(sv, 4 * (s * N + row));
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {

@@ -117,9 +117,13 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   const int wm = wave / WN, wn = wave % WN, lr = lane & 31, lq = lane >> 5;
   const int64_t K = a.K, N = a.N, steps = ceil_div(K, 128);
 
-  // Row r of the block's A operand is this feature of this matrix. Rows past the matrix read as zeros, with some other
-  // row's scales: what becomes of their features is not stored.
-  auto feature = [&](int r) { return n0 + r / (TM * 32) * FW + (GU ? r / 32 % TM % (TM / 2) : r / 32 % TM) * 32 + (r & 31); };
+  // Row r of the block's A operand is this feature of this matrix. Past the matrix its last 16 rows stand in (N is a
+  // multiple of 16, so eight rows that are loaded together are all in it or all past it): a load's common offset is
+  // not checked against the buffer's size, and what becomes of those features is not stored.
+  auto feature = [&](int r) {
+    const int64_t f = n0 + r / (TM * 32) * FW + (GU ? r / 32 % TM % (TM / 2) : r / 32 % TM) * 32 + (r & 31);
+    return f < N ? f : N - 16 + (r & 15);
+  };
   auto is_up = [&](int r) { return GU && r / 32 % TM >= TM / 2; };
   const int64_t span = N * K;
   const auto ra0 = rsrc(a.a0.codes + e * span, span), ra1 = rsrc(a.a1.codes + e * span, span);
