@@ -170,6 +170,7 @@ def _ptr(a):
     return a.data_ptr() or None
 
 
+@functools.lru_cache(maxsize=16)
 def _dtype(dt) -> int:
     if isinstance(dt, int):
         return dt
@@ -420,12 +421,12 @@ def moe_mx8_size(E, N, K) -> tuple[int, int]:
     return a.value, b.value
 
 
-def _mx8(q) -> "ctypes.POINTER(moe_mx8_t) | None":
+def _mx8(q):
     """q: None, an Mx8, or (codes, scale)."""
     if q is None:
         return None
     codes, scale = (q._codes, q._scale) if isinstance(q, Mx8) else q
-    return ctypes.pointer(moe_mx8_t(_ptr(codes), _ptr(scale)))
+    return ctypes.byref(moe_mx8_t(_ptr(codes), _ptr(scale)))
 
 
 def moe_mx8_quantize(W, E, N, K, dtype, q, stream=None):
@@ -895,6 +896,11 @@ def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None,
 
 # ---------------------------------------------------- the gate
 
+def _need(t, name, dtype, shape):
+    """_require, for calls that take a few microseconds in all."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _require(t, name, dtype, shape)
+
 def _gate_rule(score, groups, top_groups, group_best, renormalize, scale):
     if score not in SCORES:
         raise ValueError(f"score: need one of {sorted(SCORES)}, got {score!r}")
@@ -937,9 +943,9 @@ def gate(logits, k, score="softmax", bias=None, groups=1, top_groups=0, group_be
     if logits.dim() != 2:
         raise ValueError(f"logits: need [T, E], got {tuple(logits.shape)}")
     T, E = logits.shape
-    _require(logits, "logits", torch.float32, (T, E))
+    _need(logits, "logits", torch.float32, (T, E))
     if bias is not None:
-        _require(bias, "bias", torch.float32, (E,))
+        _need(bias, "bias", torch.float32, (E,))
     rule = _gate_rule(score, groups, top_groups, group_best, renormalize, scale)
     dev = logits.device
     _same_device(dev, "bias", bias)
@@ -968,11 +974,11 @@ def gate_backward(logits, topk_idx, d_topk_w, score="softmax", renormalize=True,
         raise ValueError("logits, topk_idx: need [T, E] and [T, k]")
     T, E = logits.shape
     k = topk_idx.shape[1]
-    _require(logits, "logits", torch.float32, (T, E))
-    _require(topk_idx, "topk_idx", torch.int32, (T, k))
-    _require(d_topk_w, "d_topk_w", torch.float32, (T, k))
+    _need(logits, "logits", torch.float32, (T, E))
+    _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _need(d_topk_w, "d_topk_w", torch.float32, (T, k))
     if d_scores is not None:
-        _require(d_scores, "d_scores", torch.float32, (T, E))
+        _need(d_scores, "d_scores", torch.float32, (T, E))
     rule = _gate_rule(score, 1, 1, 1, renormalize, scale)
     dev = logits.device
     _same_device(dev, "topk_idx d_topk_w d_scores out", topk_idx, d_topk_w, d_scores, out)
@@ -980,7 +986,7 @@ def gate_backward(logits, topk_idx, d_topk_w, score="softmax", renormalize=True,
         if out is None:
             out = on.empty((T, E), torch.float32)
         else:
-            _require(out, "out", torch.float32, (T, E))
+            _need(out, "out", torch.float32, (T, E))
             on.lent(out)
         if on.other is not None:
             for t in (logits, topk_idx, d_topk_w, d_scores):
@@ -1004,8 +1010,8 @@ class Mx8:
             raise ValueError(f"codes: need [E, N, K] or [R, K], got {tuple(codes.shape)}")
         lead, (N, K) = tuple(codes.shape[:-2]), codes.shape[-2:]
         moe_mx8_size(*lead or (1,), N, K)   # checks the sizes
-        _require(codes, "codes", torch.float8_e4m3fn, tuple(codes.shape))
-        _require(scale, "scale", torch.uint8, (*lead, -(-K // 128), N, 4))
+        _need(codes, "codes", torch.float8_e4m3fn, tuple(codes.shape))
+        _need(scale, "scale", torch.uint8, (*lead, -(-K // 128), N, 4))
         if scale.device != codes.device:
             raise ValueError("codes and scale must be on one device")
         self._set(codes.detach(), scale.detach())
@@ -1036,7 +1042,7 @@ def quantize_mx8(W, stream=None):
     if W.dim() not in (2, 3):
         raise ValueError(f"W: need [E, N, K] or [R, K], got {tuple(W.shape)}")
     shape = tuple(W.shape)
-    _require(W, "W", W.dtype, shape)
+    _need(W, "W", W.dtype, shape)
     dt = _dtype(W.dtype)
     E, N, K = shape if len(shape) == 3 else (1, *shape)
     moe_mx8_size(E, N, K)   # checks the sizes
@@ -1071,10 +1077,10 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, want_y=True, mx8=False, out=None
     R, d = x.shape
     dt, dev = x.dtype, x.device
     dtype = _dtype(dt)
-    _require(x, "x", dt, (R, d))
-    _require(weight, "weight", dt, (d,))
+    _need(x, "x", dt, (R, d))
+    _need(weight, "weight", dt, (d,))
     if residual is not None:
-        _require(residual, "residual", dt, (R, d))
+        _need(residual, "residual", dt, (R, d))
     if mx8 and out is None:
         moe_mx8_size(1, R, d)   # checks the sizes
     _same_device(dev, "weight residual", weight, residual)
@@ -1109,8 +1115,8 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, out=None, stream=None):
     dtype = _dtype(dt)
     for t, n, s in ((dy, "dy", (R, d)), (h, "h", (R, d)), (weight, "weight", (d,)), (dh, "dh", (R, d))):
         if t is not None:
-            _require(t, n, dt, s)
-    _require(rstd, "rstd", torch.float32, (R,))
+            _need(t, n, dt, s)
+    _need(rstd, "rstd", torch.float32, (R,))
     _same_device(dev, "h weight rstd dh", h, weight, rstd, dh)
     key = ("rmsnorm_backward", R, d, dt, dev)
     with _on(dev, stream) as on:
@@ -1151,9 +1157,9 @@ def experts_mx8(x, topk_idx, topk_w, W_gate, W_up, W_down, residual, cf, out=Non
             raise ValueError(f"{n}: need 8-bit weights of shape {s}, got {q.shape}")
     dt, dev = residual.dtype, x.device
     dtype = _dtype(dt)
-    _require(residual, "residual", dt, (T, d))
-    _require(topk_idx, "topk_idx", torch.int32, (T, k))
-    _require(topk_w, "topk_w", torch.float32, (T, k))
+    _need(residual, "residual", dt, (T, d))
+    _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _need(topk_w, "topk_w", torch.float32, (T, k))
     _same_device(dev, "topk_idx topk_w W_gate W_up W_down residual", topk_idx, topk_w, W_gate, W_up, W_down, residual)
     key = ("experts_mx8", T, d, d_ff, E, k, cf, dt, dev)
     with _on(dev, stream) as on:
@@ -1202,13 +1208,13 @@ def forward_mx8(x, norm_weight, W_router, W_gate, W_up, W_down, k, cf, residual=
     for q, n, s in ((W_gate, "W_gate", (E, d_ff, d)), (W_up, "W_up", (E, d_ff, d)), (W_down, "W_down", (E, d, d_ff))):
         if q.shape != s:
             raise ValueError(f"{n}: need 8-bit weights of shape {s}, got {q.shape}")
-    _require(x, "x", dt, (T, d))
-    _require(norm_weight, "norm_weight", dt, (d,))
-    _require(W_router, "W_router", dt, (E, d))
+    _need(x, "x", dt, (T, d))
+    _need(norm_weight, "norm_weight", dt, (d,))
+    _need(W_router, "W_router", dt, (E, d))
     if residual is not None:
-        _require(residual, "residual", dt, (T, d))
+        _need(residual, "residual", dt, (T, d))
     if bias is not None:
-        _require(bias, "bias", torch.float32, (E,))
+        _need(bias, "bias", torch.float32, (E,))
     rule = _gate_rule(score, groups, top_groups, group_best, renormalize, scale)
     _same_device(dev, "norm_weight W_router W_gate W_up W_down residual bias", norm_weight, W_router, W_gate, W_up, W_down,
                  residual, bias)

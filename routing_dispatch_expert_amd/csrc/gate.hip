@@ -21,11 +21,11 @@
 namespace moe {
 namespace {
 
-// Monotone map of a double to uint64; NaN lies below every number.
+// Monotone map of a double to uint64; NaN lies below every number, and 0 below NaN.
 __device__ inline uint64_t order_of(double v) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));  // -0 as 0
   const uint64_t key = (u >> 63) ? ~u : (u | (uint64_t{1} << 63));
-  return v != v ? 0 : key;
+  return v != v ? 1 : key;
 }
 
 template <typename V>
@@ -149,15 +149,12 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
     for (int i = 0; i < NE; ++i) s[i] = sigmoid64(l[i]);
   }
   uint64_t key[NE];
+  int ex[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    const int e = lane + 64 * i;
+    const int e = ex[i] = lane + 64 * i;
     key[i] = e < E ? order_of(bias ? s[i] + static_cast<double>(bias[e]) : l[i]) : 0;
   }
-  uint64_t taken = 0;  // bit i: expert lane + 64 i is chosen already or not allowed (NE <= 64)
-#pragma unroll
-  for (int i = 0; i < NE; ++i)
-    if (lane + 64 * i >= E) taken |= uint64_t{1} << i;
   if (g.groups > 1) {
     const int per = E / g.groups, lpg = lanes_of_group(g.groups), sub = lane % lpg, mine = lane / lpg;
     double* v = smem + wave * E;
@@ -193,26 +190,42 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const int e = lane + 64 * i;
-      if (e < E && !((kept >> (e / per * lpg)) & 1)) taken |= uint64_t{1} << i;
+      if (e < E && !((kept >> (e / per * lpg)) & 1)) key[i] = 0;
     }
   }
-  int my_e = 0;  // lane j < k: the j-th choice
-  double my_l = 0;
-  for (int j = 0; j < k; ++j) {
-    uint64_t best = 0;  // of this lane's; a NaN's key is 0 too
-    int be = INT_MAX;
-    double bl = 0;
+  // Each lane's keys in order, of equal ones the lower expert first: a choice is then the best of the lanes' heads.
+  // (Beyond eight a lane, a search of the lane's keys for each choice takes fewer steps.)
+  constexpr bool SORTED = NE <= 8;
+  if constexpr (SORTED) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const bool better = !((taken >> i) & 1) && (be == INT_MAX || key[i] > best);
-      best = better ? key[i] : best;
-      be = better ? lane + 64 * i : be;
-      bl = better ? l[i] : bl;
+    for (int a = NE - 1; a > 0; --a)
+#pragma unroll
+      for (int i = 0; i < a; ++i) {
+        const bool swap = key[i] < key[i + 1];
+        const uint64_t hi = swap ? key[i + 1] : key[i], lo = swap ? key[i] : key[i + 1];
+        const int he = swap ? ex[i + 1] : ex[i], le = swap ? ex[i] : ex[i + 1];
+        key[i] = hi;
+        key[i + 1] = lo;
+        ex[i] = he;
+        ex[i + 1] = le;
+      }
+  }
+  int my_e = 0;  // lane j < k: the j-th choice
+  for (int j = 0; j < k; ++j) {
+    uint64_t best = key[0];
+    int be = ex[0];
+    if constexpr (!SORTED) {
+#pragma unroll
+      for (int i = 1; i < NE; ++i) {
+        const bool better = key[i] > best;
+        best = better ? key[i] : best;
+        be = better ? ex[i] : be;
+      }
     }
     // two lanes' bests seldom share the upper half; of equal ones the lowest expert
     const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
     const uint32_t top_hi = wave_max(hi);
-    uint64_t like = __ballot(be != INT_MAX && hi == top_hi);
+    uint64_t like = __ballot(hi == top_hi);
     if (like & (like - 1)) {
       const bool in = (like >> lane) & 1;
       const uint32_t top_lo = wave_max(in ? lo : 0u);
@@ -222,13 +235,23 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
     }
     const int win = __builtin_ctzll(like);
     const int e = static_cast<int>(lane_word(static_cast<uint32_t>(be), win));
-    const double el = lane_word(bl, win);
-    if (lane == win) taken |= uint64_t{1} << (e / 64);
-    if (lane == j) {
-      my_e = e;
-      my_l = el;
+    if (lane == j) my_e = e;
+    if (lane == win) {
+      if constexpr (SORTED) {
+#pragma unroll
+        for (int i = 0; i + 1 < NE; ++i) {
+          key[i] = key[i + 1];
+          ex[i] = ex[i + 1];
+        }
+        key[NE - 1] = 0;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+          if (ex[i] == e) key[i] = 0;
+      }
     }
   }
+  const double my_l = lane < k ? static_cast<double>(logits[t * E + my_e]) : 0;
   // weights of the chosen
   const bool in = lane < k;
   double z;
