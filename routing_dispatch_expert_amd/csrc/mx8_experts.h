@@ -40,9 +40,9 @@ struct Mx8Gemm {
   bool y_bf16;
 };
 
-// Many rows an expert (mx8_tiles.hip): row tiles of mx8_tile_rows() rows, listed in
-// ls.tile. Grid: at most `tiles` of them.
-int mx8_tile_rows();
-hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, hipStream_t s);
+// Many rows an expert (mx8_tiles.hip): row tiles of mx8_tile_rows() rows, by the rows
+// that the experts have on average, listed in ls.tile. Grid: at most `tiles` of them.
+int mx8_tile_rows(int64_t copies, int64_t experts);
+hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, int tile_rows, hipStream_t s);
 
 }  // namespace moe

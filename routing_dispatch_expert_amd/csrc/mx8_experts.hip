@@ -440,16 +440,17 @@ Mx8 view(const Mx8Ptr& p) { return {p.codes, p.scale}; }
 
 hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   const int64_t copies = L.T * L.k, act = std::min<int64_t>(L.E, copies);
+  const int tile_rows = mx8_tile_rows(copies, act);
   hipError_t e = hipSuccess;
   if (copies <= kPlanCopies) {
-    experts_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.idx, L.T, L.k, L.E, L.C, mx8_tile_rows(), L.slot, L.routed, L.kept, L.ls);
+    experts_plan_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.idx, L.T, L.k, L.E, L.C, tile_rows, L.slot, L.routed, L.kept, L.ls);
   } else {
     if ((e = launch_tile_hist(L.idx, L.T, L.k, L.E, L.tile_cnt, s, L.slot)) != hipSuccess ||
         (e = launch_scan(L.tile_cnt, ceil_div(L.T, kTileTokens), L.E, L.C, 1, 0, L.k, L.T, L.tile_off, L.routed, L.kept,
                          nullptr, nullptr, 0, nullptr, nullptr, s)) != hipSuccess ||
         (e = launch_slots_from_ranks(L.idx, L.slot, L.tile_off, L.T, L.k, L.E, L.C, nullptr, nullptr, s)) != hipSuccess)
       return e;
-    list_experts_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.kept, L.E, L.C, mx8_tile_rows(), L.ls);
+    list_experts_kernel<<<dim3(1), dim3(1024), 0, s>>>(L.kept, L.E, L.C, tile_rows, L.ls);
     place_copies_kernel<<<dim3(static_cast<unsigned>(ceil_div(copies, 256))), dim3(256), 0, s>>>(L.idx, L.slot, copies, L.ls);
   }
   if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -467,18 +468,18 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   a.H = copies;
   a.y = nullptr;
   a.y_bf16 = L.bf16;
-  // Row tiles from 28 rows an expert on, where both take the same time (d = 4096, d_ff = 14336, 8 experts with 32
-  // rows each: 527 us by strips, 541 by tiles; d = 2048, d_ff = 1408, 64 experts: 24 rows 167 and 238, 48 rows 304
-  // and 244). 16 columns of x where an expert has that few rows, else 32: with 16 alone the second case takes 267 us.
-  const bool many = copies > 28 * act;
-  const int64_t tiles = copies / mx8_tile_rows() + act;
+  // Row tiles from 20 rows an expert on: by strips and by tiles of 128 rows, 8 experts of d = 4096, d_ff = 14336 take
+  // 319 and 380 us with 16 rows each, 522 and 411 - 447 with 32; 256 of d = 7168, d_ff = 2048 2.52 and 2.40 ms with 16,
+  // 3.75 and 2.58 with 32; 64 of d = 2048, d_ff = 1408 166 and 163 us with 24, 298 and 186 with 48.
+  const bool many = copies > 20 * act;
+  const int64_t tiles = copies / tile_rows + act;
   auto few = [&](auto gu, const Mx8Gemm& g) {
     constexpr bool GU = decltype(gu)::value;
     const int strips = static_cast<int>(ceil_div(g.N, 32));
     few_rows_kernel<GU, GU ? 4 : 2, 4><<<dim3(static_cast<unsigned>(act * strips)), dim3(256), 0, s>>>(g, strips);
     return hipGetLastError();
   };
-  e = many ? launch_mx8_tiles(a, true, L.E, tiles, s) : few(std::true_type{}, a);
+  e = many ? launch_mx8_tiles(a, true, L.E, tiles, tile_rows, s) : few(std::true_type{}, a);
   if (e != hipSuccess) return e;
   Mx8Gemm b = a;
   b.a0 = b.a1 = view(L.down);
@@ -487,7 +488,7 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   b.x = view(L.h);
   b.R = copies;
   b.y = L.y;
-  e = many ? launch_mx8_tiles(b, false, L.E, tiles, s) : few(std::false_type{}, b);
+  e = many ? launch_mx8_tiles(b, false, L.E, tiles, tile_rows, s) : few(std::false_type{}, b);
   if (e != hipSuccess) return e;
   const int64_t V = L.d / (L.bf16 ? 8 : 4), blocks = ceil_div(V, 256);
   const dim3 grid(static_cast<unsigned>(L.T * blocks));

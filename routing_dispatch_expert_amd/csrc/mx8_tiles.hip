@@ -1,6 +1,6 @@
 // The experts' products with 8-bit rows and weights where an expert has many rows
-// (gfx950): blocks of 256 weight rows by 256 rows of x, brought into LDS by the
-// buffer unit, two stages of 128 columns (a row's stage is a 128-byte line).
+// (gfx950): blocks of 256 weight rows by 256 (or 128) rows of x, brought into LDS by
+// the buffer unit, two (three) stages of 128 columns: a row's stage is a 128-byte line.
 //
 // As in mx8_experts.hip the weights are the A operand: lane l of a 32 x 32 x 64
 // instruction holds, of row l % 32, the bytes 16 (l / 32) .. + 15 and 32 + 16 (l /
@@ -29,8 +29,12 @@ __device__ inline __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
                                            0x00020000);
 }
 
-// s_waitcnt: all of this wave's loads, and its LDS reads.
-__device__ inline __attribute__((unused)) void wait_all() { __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (0 << 8)); }
+// s_waitcnt: this wave's loads but the last VM of them, and its LDS reads.
+template <int VM>
+__device__ inline void wait_loads() {
+  static_assert(VM < 64, "vmcnt has six bits");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | (0 << 8) | ((VM >> 4) << 14));
+}
 
 // A stage half's schedule: NM products with NR reads of LDS and NV loads spread
 // among them. Left to itself the compiler reads an operand right before its
@@ -87,7 +91,8 @@ __device__ inline bool tile_of_block(const ExpertLists& ls, int E, int row_tile,
   return true;
 }
 
-// WM x WN waves of TM x TN tiles of 32 x 32: 2 x 2 of 4 x 4. A stage is 32 products
+// WM x WN waves of TM x TN tiles of 32 x 32, NS slots for stages: 2 x 2 of 4 x 4 and
+// two slots, or of 4 x 2 and three. The former's stage is 32 products
 // a wave (2048 clocks), 128 KiB of LDS read and 66 written, which together with
 // its loads' way through the L2 bounds it: 1.9 us a stage where the products alone
 // take 1.0 at the clock that they leave (4.25 PFLOP/s in registers). Mixtral-shaped,
@@ -95,7 +100,7 @@ __device__ inline bool tile_of_block(const ExpertLists& ls, int E, int row_tile,
 // Measured and dropped: 2 x 4 waves of 4 x 2 tiles (256 registers do not hold them:
 // twice the time), 128 features a block (down 0.81 ms), a word of each weight line
 // asked for two stages before (down 0.61 ms, but 64 rows an expert 12% more).
-template <bool GU, int WM, int WN, int TM, int TN>
+template <bool GU, int WM, int WN, int TM, int TN, int NS>
 __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM* WN / 4, WM* WN / 4))) void mx8_tile_kernel(
     Mx8Gemm a, int E) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass has no scaled matrix instruction and would drop the kernel without a word
@@ -104,8 +109,11 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   constexpr int FB = WM * FW;                          // and of the block
   constexpr int PA = MA / 8 / NW, PX = MX / 8 / NW;    // 8-row DMA pieces of a wave
   constexpr int SETS = (MA + MX) / 64, PS = (SETS + NW - 1) / NW;  // sets of 64 scales, and a wave's
-  __shared__ uint4 As0[MA * 8], As1[MA * 8], Xs0[MX * 8], Xs1[MX * 8];
-  __shared__ uint32_t Sc0[MA + MX], Sc1[MA + MX];
+  static_assert(NS == 2 || NS == 3, "two or three slots");
+  constexpr int THIRD = NS == 3;
+  // a slot's arrays each by themselves, so that the compiler tells the stages apart
+  __shared__ uint4 As0[MA * 8], As1[MA * 8], As2[THIRD ? MA * 8 : 1], Xs0[MX * 8], Xs1[MX * 8], Xs2[THIRD ? MX * 8 : 1];
+  __shared__ uint32_t Sc0[MA + MX], Sc1[MA + MX], Sc2[THIRD ? MA + MX : 1];
 
   Tile tl;
   if (!tile_of_block(a.ls, E, MX, FB, a.N, &tl)) return;
@@ -240,57 +248,74 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
     };
     using Half0 = std::integral_constant<int, 0>;
     using Half1 = std::integral_constant<int, 1>;
-    // stage s is in (as, xs, sc), its first half's operands in slot 0; stage s + 1 is on its way into the other.
-    // Whether there are stages s + 1 and s + 2 is known here: a branch around the matrix work instead made the
-    // compiler keep the accumulators twice.
-    auto stage = [&](auto next, auto next2, uint4* as, uint4* xs, uint32_t* sc, uint4* an, uint4* xn, uint32_t* sn,
-                     int64_t s) {
+    // Stage s is in (as, xs, sc), its first half's operands in slot 0 of the registers; the stages after it are on
+    // their way into the other slots. Half way through, stage s + 1 has landed (of the loads under way the last `later`
+    // may be out), and stage s + NS is asked for in this one's place.
+    // What follows a stage is known here: a branch around the matrix work instead made the compiler keep the
+    // accumulators twice.
+    constexpr int LOADS = PA + PX + PS;
+    auto stage = [&](auto next, auto refill, auto later, uint4* as, uint4* xs, uint32_t* sc, uint4* an, uint4* xn,
+                     uint32_t* sn, int64_t s) {
       constexpr int READS = 2 * (TM + TX), PRODUCTS = TM * TX;
       fload(as, xs, 1, 1);
       multiply(Half0{});
       if constexpr (TX > 0) interleave<PRODUCTS, READS, 0>();
       if constexpr (decltype(next)::value) {
         __builtin_amdgcn_sched_barrier(0);
-        wait_all();                    // own share of stage s + 1 landed, reads of stage s done ...
-        __builtin_amdgcn_s_barrier();  // ... and everyone's
+        wait_loads<decltype(later)::value>();  // own share of stage s + 1 landed, reads of stage s done ...
+        __builtin_amdgcn_s_barrier();          // ... and everyone's
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (decltype(next2)::value) dma(as, xs, sc, s + 2);
+        if constexpr (decltype(refill)::value) dma(as, xs, sc, s + NS);
         fload(an, xn, 0, 0);
         sload(sn);
       }
       multiply(Half1{});
       if constexpr (TX > 0 && decltype(next)::value)
-        interleave<PRODUCTS, READS + TM + TX, decltype(next2)::value ? PA + PX + PS : 0>();
+        interleave<PRODUCTS, READS + TM + TX, decltype(refill)::value ? LOADS : 0>();
       if constexpr (decltype(next)::value) sready(s + 1);
     };
     using Yes = std::true_type;
     using No = std::false_type;
-    int64_t s = steps & 1;
-    if (s) {  // an odd number of stages: one by itself, then pairs
-      dma(As0, Xs0, Sc0, 0);
-      wait_all();
+    using None = std::integral_constant<int, 0>;
+    using Later = std::integral_constant<int, (NS - 2) * LOADS>;
+    int64_t s = 0;
+    for (; s < steps % NS; ++s) {  // what does not fill all slots: one stage after the other
+      dma(As0, Xs0, Sc0, s);
+      wait_loads<0>();
       __builtin_amdgcn_s_barrier();
       fload(As0, Xs0, 0, 0);
       sload(Sc0);
-      sready(0);
-      stage(No{}, No{}, As0, Xs0, Sc0, As1, Xs1, Sc1, 0);
-      wait_all();
+      sready(s);
+      stage(No{}, No{}, None{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
+      wait_loads<0>();
       __builtin_amdgcn_s_barrier();
     }
     if (s < steps) {
       dma(As0, Xs0, Sc0, s);
-      wait_all();
-      __builtin_amdgcn_s_barrier();
       dma(As1, Xs1, Sc1, s + 1);
+      if constexpr (NS == 3) dma(As2, Xs2, Sc2, s + 2);
+      wait_loads<(NS - 1) * LOADS>();
+      __builtin_amdgcn_s_barrier();
       fload(As0, Xs0, 0, 0);
       sload(Sc0);
       sready(s);
-      for (; s + 2 < steps; s += 2) {
-        stage(Yes{}, Yes{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
-        stage(Yes{}, Yes{}, As1, Xs1, Sc1, As0, Xs0, Sc0, s + 1);
+      if constexpr (NS == 2) {
+        for (; s + 2 < steps; s += 2) {
+          stage(Yes{}, Yes{}, Later{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
+          stage(Yes{}, Yes{}, Later{}, As1, Xs1, Sc1, As0, Xs0, Sc0, s + 1);
+        }
+        stage(Yes{}, No{}, None{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
+        stage(No{}, No{}, None{}, As1, Xs1, Sc1, As0, Xs0, Sc0, s + 1);
+      } else {
+        for (; s + 3 < steps; s += 3) {
+          stage(Yes{}, Yes{}, Later{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
+          stage(Yes{}, Yes{}, Later{}, As1, Xs1, Sc1, As2, Xs2, Sc2, s + 1);
+          stage(Yes{}, Yes{}, Later{}, As2, Xs2, Sc2, As0, Xs0, Sc0, s + 2);
+        }
+        stage(Yes{}, No{}, Later{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
+        stage(Yes{}, No{}, None{}, As1, Xs1, Sc1, As2, Xs2, Sc2, s + 1);
+        stage(No{}, No{}, None{}, As2, Xs2, Sc2, As0, Xs0, Sc0, s + 2);
       }
-      stage(Yes{}, No{}, As0, Xs0, Sc0, As1, Xs1, Sc1, s);
-      stage(No{}, No{}, As1, Xs1, Sc1, As0, Xs0, Sc0, s + 1);
     }
   };
   if (live == TN)
@@ -368,21 +393,28 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
 #endif
 }
 
-template <bool GU>
+template <bool GU, int WM, int WN, int TM, int TN, int NS>
 hipError_t launch(const Mx8Gemm& a, int E, int64_t tiles, hipStream_t s) {
-  constexpr int WM = 2, WN = 2, TM = 4, TN = 4;
   const int64_t ft = ceil_div(a.N, WM * (GU ? TM / 2 : TM) * 32);
   const dim3 grid(static_cast<unsigned>(ceil_div(tiles * ft, 8) * 8));
-  mx8_tile_kernel<GU, WM, WN, TM, TN><<<grid, dim3(WM * WN * 64), 0, s>>>(a, E);
+  mx8_tile_kernel<GU, WM, WN, TM, TN, NS><<<grid, dim3(WM * WN * 64), 0, s>>>(a, E);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int mx8_tile_rows() { return 256; }
+// With few rows an expert the weights' way from memory bounds the products, and what
+// counts is how much of it is asked for at once: 128 rows leave room for three
+// slots, two stages under way (the same weights: 64 rows an expert of d = 7168,
+// d_ff = 2048 2.8 ms instead of 3.0, 32 rows 2.6 instead of 3.0; 96 rows of d = 4096,
+// d_ff = 14336 437 us instead of 491, 128 rows, which half the experts exceed, 537
+// instead of 497).
+int mx8_tile_rows(int64_t copies, int64_t experts) { return copies > 96 * experts ? 256 : 128; }
 
-hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, hipStream_t s) {
-  return gate_up ? launch<true>(a, E, tiles, s) : launch<false>(a, E, tiles, s);
+hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, int tile_rows, hipStream_t s) {
+  if (tile_rows == 256)
+    return gate_up ? launch<true, 2, 2, 4, 4, 2>(a, E, tiles, s) : launch<false, 2, 2, 4, 4, 2>(a, E, tiles, s);
+  return gate_up ? launch<true, 2, 2, 4, 2, 3>(a, E, tiles, s) : launch<false, 2, 2, 4, 2, 3>(a, E, tiles, s);
 }
 
 }  // namespace moe
