@@ -1045,8 +1045,7 @@ def quantize_mx8(W, stream=None):
     _need(W, "W", W.dtype, shape)
     dt = _dtype(W.dtype)
     E, N, K = shape if len(shape) == 3 else (1, *shape)
-    moe_mx8_size(E, N, K)   # checks the sizes
-    with _on(W.device, stream) as on:
+    with _on(W.device, stream) as on:   # the call checks the sizes
         q = Mx8._empty(on, shape)
         moe_mx8_quantize(on.lent(W), E, N, K, dt, q, on.stream)
     return q
