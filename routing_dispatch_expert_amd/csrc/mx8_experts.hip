@@ -393,11 +393,10 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(Mx8Gemm a, int str
 // out[t] = residual[t] + sum_j w y[t, j] over the kept copies, j ascending, in
 // fp32; a token without a kept copy passes bit for bit.
 template <bool BF16>
-__global__ __launch_bounds__(256) void experts_combine_kernel(const uint4* __restrict__ residual,
-                                                              const uint4* __restrict__ y,
+__global__ __launch_bounds__(256) void experts_combine_kernel(const uint4* residual, const uint4* __restrict__ y,
                                                               const float* __restrict__ w,
                                                               const int32_t* __restrict__ slot, int k, int64_t V,
-                                                              int64_t blocks, uint4* __restrict__ out) {
+                                                              int64_t blocks, uint4* out) {  // out may be residual
   constexpr int P = BF16 ? 8 : 4;
   const int64_t t = blockIdx.x / blocks, v = blockIdx.x % blocks * 256 + threadIdx.x;
   if (v >= V) return;

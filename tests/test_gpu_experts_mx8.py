@@ -123,6 +123,29 @@ def test_experts(T, d, f, E, k, cf, ints):
     run_case(T, d, f, E, k, cf, ints=ints)
 
 
+# rows an expert on both sides of the rules for strips, tiles of 128 rows and of 256; one to seven 128-column steps, whole and not
+STEPS = [(50, 128, 128, 2, 2, 1.0), (100, 768, 384, 4, 2, 2.0), (90, 640, 896, 4, 2, 2.0), (60, 400, 272, 3, 1, 3.0),
+         (400, 512, 896, 2, 1, 2.0), (300, 128, 768, 2, 1, 2.0), (384, 144, 656, 4, 1, 4.0), (388, 656, 144, 4, 1, 4.0),
+         (80, 256, 528, 4, 1, 4.0), (84, 528, 256, 4, 1, 4.0), (16, 272, 4112, 1, 1, 1.0), (25, 2064, 48, 1, 1, 1.0)]
+
+
+@pytest.mark.parametrize("ints", [True, False], ids=["whole", "gauss"])
+@pytest.mark.parametrize("T,d,f,E,k,cf", STEPS)
+def test_steps_and_rules(T, d, f, E, k, cf, ints):
+    run_case(T, d, f, E, k, cf, ints=ints)
+
+
+@pytest.mark.parametrize("T,E", [(100, 64), (33, 64), (300, 4), (700, 8)])
+def test_one_expert_with_many_rows_among_experts_with_few(T, E):
+    """Strips take such an expert 32 rows at a time, tiles by more of them."""
+    rng = np.random.default_rng(T)
+    idx = np.full((T, 1), E // 2, np.int32)
+    few = rng.permutation(T)[:E // 2]
+    idx[few, 0] = np.arange(E // 2)
+    run_case(T, 144, 80, E, 1, float(E), idx=idx)
+    run_case(T, 144, 80, E, 1, float(E), idx=idx, ints=False)
+
+
 @pytest.mark.parametrize("ints", [True, False], ids=["whole", "gauss"])
 @pytest.mark.parametrize("T,d,f,E,k,cf", [(2, 144, 80, 4, 2, 2.0), (40, 256, 96, 2, 2, 1.0), (400, 272, 176, 2, 1, 2.0)])
 def test_experts_fp32(T, d, f, E, k, cf, ints):
