@@ -422,6 +422,30 @@ int moe_gate(const float* logits, const float* bias, const moe_gate_t* gate, int
 int moe_gate_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, const float* d_scores,
                       const moe_gate_t* gate, int64_t T, int32_t E, int32_t k, float* dlogits, void* stream);
 
+/* ---- The layer with a given routing ----
+ *
+ * moe_layer_forward with the caller's routing (moe_gate's or any other) and
+ * residual, as in a transformer block:
+ *   out[t] = residual[t] + sum_j [slot >= 0] topk_w[t,j] * y[topk_idx[t,j], slot[t,j]]
+ * for the experts' outputs y of x; slots, capacity, drops, arguments, checks, stats
+ * (topk_idx and topk_w NULL) and workspace as there. A topk_idx entry outside [0,
+ * E) is dropped. out must not overlap x or residual, which may be one array.
+ * moe_layer_backward_routed: from dout [T, d], dx [T, d] of the experts' path alone
+ * (residual's gradient is dout), d_topk_w [T, k] fp32 = <dout[t], y[t,j]> (0 for a
+ * dropped copy, and where topk_w is 0, where the experts' gradients hold no trace of
+ * it), dW_gate, dW_up, dW_down. saved: NULL, or the stats of the forward on the
+ * same inputs that kept buckets, g, u and h (then not recomputed). Else as
+ * moe_layer_backward; workspace: moe_backward_workspace_size() bytes. */
+int moe_layer_forward_routed(const void* x, const void* residual, const int32_t* topk_idx, const float* topk_w,
+                             const void* W_gate, const void* W_up, const void* W_down, int64_t T, int64_t d,
+                             int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P, moe_dtype_t dtype, void* out,
+                             moe_stats_t* stats, void* workspace, size_t workspace_bytes, void* stream);
+int moe_layer_backward_routed(const void* x, const int32_t* topk_idx, const float* topk_w, const void* W_gate,
+                              const void* W_up, const void* W_down, const void* dout, int64_t T, int64_t d,
+                              int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P, moe_dtype_t dtype,
+                              const moe_stats_t* saved, void* dx, float* d_topk_w, void* dW_gate, void* dW_up,
+                              void* dW_down, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- 8-bit matrices ----
  *
  * A stack of matrices [E, N, K], or rows [R, K] (E = 1, N = R), in 8 bits: e4m3

@@ -33,7 +33,7 @@ EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_layer_forward", "moe_backw
            "moe_permute_workspace_size", "moe_permute", "moe_permute_static", "moe_grouped_gemm_workspace_size",
            "moe_grouped_gemm", "moe_combine", "moe_q4_size", "moe_q4_quantize", "moe_q4_dequantize",
            "moe_q4_matvec_workspace_size", "moe_q4_matvec", "moe_few_workspace_size", "moe_layer_forward_few",
-           "moe_layer_forward_few_q4", "moe_gate", "moe_gate_backward", "moe_mx8_size",
+           "moe_layer_forward_few_q4", "moe_gate", "moe_gate_backward", "moe_layer_forward_routed", "moe_layer_backward_routed", "moe_mx8_size",
            "moe_mx8_quantize", "moe_mx8_dequantize", "moe_rmsnorm", "moe_rmsnorm_backward_workspace_size",
            "moe_rmsnorm_backward", "moe_experts_mx8_workspace_size", "moe_experts_mx8", "moe_set_stage_events", "moe_stage_ran", "moe_status_string", "moe_last_error")
 STAGES = ("router", "route", "slots", "scatter", "gate_up", "down", "combine")
@@ -110,6 +110,10 @@ _SIGS = {
                                  ctypes.c_int, _P, ctypes.POINTER(moe_stats_t), _P, _SZ, _P],
     "moe_gate": [_P, _P, ctypes.POINTER(moe_gate_t), _I64, _I32, _I32, _P, _P, _P],
     "moe_gate_backward": [_P, _P, _P, _P, ctypes.POINTER(moe_gate_t), _I64, _I32, _I32, _P, _P],
+    "moe_layer_forward_routed": [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _F32, _I32, ctypes.c_int, _P,
+                                 ctypes.POINTER(moe_stats_t), _P, _SZ, _P],
+    "moe_layer_backward_routed": [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _F32, _I32, ctypes.c_int,
+                                  ctypes.POINTER(moe_stats_t), _P, _P, _P, _P, _P, _P, _SZ, _P],
     "moe_mx8_size": [_I32, _I64, _I64, _P, _P],
     "moe_mx8_quantize": [_P, _I32, _I64, _I64, ctypes.c_int, ctypes.POINTER(moe_mx8_t), _P],
     "moe_mx8_dequantize": [ctypes.POINTER(moe_mx8_t), _I32, _I64, _I64, ctypes.c_int, _P, _P],
@@ -412,6 +416,22 @@ def moe_gate(logits, bias, gate, T, E, k, topk_idx, topk_w, stream=None):
 def moe_gate_backward(logits, topk_idx, d_topk_w, d_scores, gate, T, E, k, dlogits, stream=None):
     _check(lib().moe_gate_backward(_ptr(logits), _ptr(topk_idx), _ptr(d_topk_w), _ptr(d_scores), _gate(gate), T, E, k,
                                    _ptr(dlogits), _stream(stream)), "moe_gate_backward")
+
+
+def moe_layer_forward_routed(x, residual, topk_idx, topk_w, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, dtype, out,
+                             stats, workspace, workspace_bytes, stream=None):
+    _check(lib().moe_layer_forward_routed(_ptr(x), _ptr(residual), _ptr(topk_idx), _ptr(topk_w), _ptr(W_gate), _ptr(W_up),
+                                          _ptr(W_down), T, d, d_ff, E, k, cf, P, _dtype(dtype), _ptr(out), _stats(stats),
+                                          _ptr(workspace), workspace_bytes, _stream(stream)), "moe_layer_forward_routed")
+
+
+def moe_layer_backward_routed(x, topk_idx, topk_w, W_gate, W_up, W_down, dout, T, d, d_ff, E, k, cf, P, dtype, saved, dx,
+                              d_topk_w, dW_gate, dW_up, dW_down, workspace, workspace_bytes, stream=None):
+    """saved: None, or the stats dict of a moe_layer_forward_routed call that kept buckets, g, u and h."""
+    _check(lib().moe_layer_backward_routed(_ptr(x), _ptr(topk_idx), _ptr(topk_w), _ptr(W_gate), _ptr(W_up), _ptr(W_down),
+                                           _ptr(dout), T, d, d_ff, E, k, cf, P, _dtype(dtype), _stats(saved), _ptr(dx),
+                                           _ptr(d_topk_w), _ptr(dW_gate), _ptr(dW_up), _ptr(dW_down), _ptr(workspace),
+                                           workspace_bytes, _stream(stream)), "moe_layer_backward_routed")
 
 
 def moe_mx8_size(E, N, K) -> tuple[int, int]:
@@ -916,7 +936,7 @@ def _lent_result(out, key, what):
 
 
 class Result(dict):
-    """What gate, rmsnorm, rmsnorm_backward, experts_mx8 and forward_mx8 return.
+    """What gate, rmsnorm, experts_mx8, forward_mx8, forward_routed and their like return.
     Passed to a later call as `out` it lends that call the outputs and workspace
     that it was made with, and shows them again whatever became of its entries."""
 
@@ -993,6 +1013,97 @@ def gate_backward(logits, topk_idx, d_topk_w, score="softmax", renormalize=True,
                 on.lent(t)
         moe_gate_backward(logits, topk_idx, d_topk_w, d_scores, rule, T, E, k, out, on.stream)
     return out
+
+
+def _routed_shapes(x, topk_idx, topk_w, W_gate, W_up, W_down, others):
+    import torch
+    if x.dim() != 2 or topk_idx.dim() != 2 or W_gate.dim() != 3:
+        raise ValueError("x, topk_idx, W_gate: need [T, d], [T, k] and [E, d_ff, d]")
+    T, d = x.shape
+    E, d_ff = W_gate.shape[:2]
+    k = topk_idx.shape[1]
+    dt = x.dtype
+    for t, n, s in ((x, "x", (T, d)), (W_gate, "W_gate", (E, d_ff, d)), (W_up, "W_up", (E, d_ff, d)),
+                    (W_down, "W_down", (E, d, d_ff)), *((t, n, (T, d)) for n, t in others.items())):
+        _need(t, n, dt, s)
+    _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _need(topk_w, "topk_w", torch.float32, (T, k))
+    _same_device(x.device, "topk_idx topk_w W_gate W_up W_down " + " ".join(others), topk_idx, topk_w, W_gate, W_up, W_down,
+                 *others.values())
+    return T, d, d_ff, E, k
+
+
+def forward_routed(x, topk_idx, topk_w, W_gate, W_up, W_down, cf, residual=None, P=1, keep_activations=False, out=None,
+                   stream=None):
+    """The layer (bf16 or fp32) with a given routing, gate()'s or any other, and the
+    residual of a transformer block: out = residual + the experts' outputs for x
+    (residual None: x). Returns a dict out, slot [T, k], routed_count, kept_count,
+    send_count [P], totals, workspace; with keep_activations also buckets and g, u, h,
+    which backward_routed(..., saved=result) takes instead of recomputing them. out:
+    the result of an earlier call with the same sizes, whose tensors this call writes."""
+    import torch
+    if residual is None:
+        residual = x
+    T, d, d_ff, E, k = _routed_shapes(x, topk_idx, topk_w, W_gate, W_up, W_down, {"residual": residual})
+    dt, dev = x.dtype, x.device
+    key = ("forward_routed", T, d, d_ff, E, k, cf, P, dt, dev, bool(keep_activations))
+    with _on(dev, stream) as on:
+        if out is None:
+            nbytes, C, i32 = moe_workspace_size(T, d, d_ff, E, k, cf, P, dt), moe_capacity(T, E, k, cf), torch.int32
+            kept = dict(buckets=on.empty((E, C, d), dt), **{n: on.empty((E, C, d_ff), dt) for n in "guh"}) if keep_activations else {}
+            res = Result.of(key, C=C, out=on.empty((T, d), dt), slot=on.empty((T, k), i32), routed_count=on.empty((E,), i32),
+                            kept_count=on.empty((E,), i32), send_count=on.empty((P,), i32), totals=on.empty((4,), torch.int64),
+                            workspace=on.empty((max(nbytes, 1),), torch.uint8), **kept)
+            if T == 0:   # nothing will be launched: the counts of no tokens
+                for name in ("routed_count", "kept_count", "send_count", "totals"):
+                    on.zero(res[name])
+        else:
+            res = _lent_result(out, key, "forward_routed")
+        t = res._bound[1]
+        if on.other is not None:
+            for v in (*t.values(), x, topk_idx, topk_w, W_gate, W_up, W_down, residual):
+                if not isinstance(v, int):
+                    on.lent(v)
+        if T:
+            moe_layer_forward_routed(x, residual, topk_idx, topk_w, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, dt,
+                                     t["out"], t, t["workspace"], t["workspace"].numel(), on.stream)
+    return res
+
+
+def backward_routed(x, topk_idx, topk_w, W_gate, W_up, W_down, dout, cf, P=1, saved=None, out=None, stream=None):
+    """Gradients of forward_routed() for dout [T, d]: a dict dx (of the experts' path
+    alone: residual's gradient is dout itself), d_topk_w fp32 [T, k] (for
+    gate_backward()), dW_gate, dW_up, dW_down, workspace. saved: the result of
+    forward_routed(..., keep_activations=True) on the same inputs. out: the result of
+    an earlier call with the same sizes, whose tensors this call writes."""
+    import torch
+    T, d, d_ff, E, k = _routed_shapes(x, topk_idx, topk_w, W_gate, W_up, W_down, {"dout": dout})
+    dt, dev = x.dtype, x.device
+    if saved is not None and (not isinstance(saved, Result) or
+                              saved._bound[0] != ("forward_routed", T, d, d_ff, E, k, cf, P, dt, dev, True)):
+        raise ValueError("saved: need the result of forward_routed(..., keep_activations=True) with the same sizes")
+    key = ("backward_routed", T, d, d_ff, E, k, cf, P, dt, dev)
+    with _on(dev, stream) as on:
+        if out is None:
+            nbytes = moe_backward_workspace_size(T, d, d_ff, E, k, cf, P, dt)
+            res = Result.of(key, dx=on.empty((T, d), dt), d_topk_w=on.empty((T, k), torch.float32),
+                            dW_gate=on.empty((E, d_ff, d), dt), dW_up=on.empty((E, d_ff, d), dt),
+                            dW_down=on.empty((E, d, d_ff), dt), workspace=on.empty((max(nbytes, 1),), torch.uint8))
+        else:
+            res = _lent_result(out, key, "backward_routed")
+        t, state = res._bound[1], None if saved is None else saved._bound[1]
+        if on.other is not None:
+            for v in (*t.values(), *(state or {}).values(), x, topk_idx, topk_w, W_gate, W_up, W_down, dout):
+                if not isinstance(v, int):
+                    on.lent(v)
+        if T:
+            moe_layer_backward_routed(x, topk_idx, topk_w, W_gate, W_up, W_down, dout, T, d, d_ff, E, k, cf, P, dt,
+                                      state and {n: state[n] for n in ("buckets", "g", "u", "h")}, t["dx"], t["d_topk_w"],
+                                      t["dW_gate"], t["dW_up"], t["dW_down"], t["workspace"], t["workspace"].numel(), on.stream)
+        else:   # nothing will be launched: the gradients of no tokens
+            for name in ("dW_gate", "dW_up", "dW_down"):
+                on.zero(t[name])
+    return res
 
 
 # ---------------------------------------------------- 8-bit matrices, the norm

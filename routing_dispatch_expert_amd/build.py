@@ -21,7 +21,7 @@ ARCH = "gfx950"
 
 SOURCES = ["moe_api.hip", "router.hip", "permute.hip", "grouped_gemm.hip", "combine.hip", "backward.hip",
            "few.hip", "q4.hip", "gate.hip", "mx8.hip",
-           "norm.hip", "mx8_experts.hip", "mx8_tiles.hip"]
+           "norm.hip", "mx8_experts.hip", "mx8_tiles.hip", "routed.hip"]
 
 
 def hipcc() -> str:

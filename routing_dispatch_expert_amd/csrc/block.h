@@ -68,4 +68,12 @@ struct ExpertsMx8 {
 };
 hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s);
 
+// ---- the layer with a given routing (routed.hip) ----
+hipError_t launch_zero(float* p, int64_t n, hipStream_t s);
+// dw = q / w (0 where w is 0).
+hipError_t launch_weight_grad(const float* q, const float* w, int64_t n, float* dw, hipStream_t s);
+// dx[t] = sum_j [slot >= 0] dX[idx, slot].
+hipError_t launch_gather_copies(const void* dX, const int32_t* idx, const int32_t* slot, int64_t T, int64_t d, int k,
+                                int64_t C, bool bf16, void* dx, hipStream_t s);
+
 }  // namespace moe

@@ -429,20 +429,34 @@ int moe_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k,
   return MOE_OK;
 }
 
-int moe_layer_forward(const void* x, const void* W_router, const float* router_bias,
-                      const void* W_gate, const void* W_up, const void* W_down, int64_t T,
-                      int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P,
-                      int32_t max_ranks, moe_dtype_t dtype, void* out, moe_stats_t* stats,
-                      void* workspace, size_t workspace_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// A routing from outside: topk_idx, topk_w [T, k], and where the weights' gradients go.
+struct Routing {
+  const int32_t* idx;
+  const float* w;
+  float* dw;
+};
+
+// The layer; with `given` the routing is the caller's, and the rows that the
+// experts' outputs are added to are `residual`.
+int layer_forward(const void* x, const void* residual, const Routing* given, const void* W_router,
+                  const float* router_bias, const void* W_gate, const void* W_up, const void* W_down, int64_t T,
+                  int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P, int32_t max_ranks,
+                  moe_dtype_t dtype, void* out, moe_stats_t* stats, void* workspace, size_t workspace_bytes,
+                  void* stream) {
   int64_t C;
   int st = check_layer_shape(T, d, d_ff, E, k, cf, P, dtype, &C);
   if (st != MOE_OK) return st;
   if ((st = check_rank_limit(E, k, P, max_ranks)) != MOE_OK) return st;
-  if (!x || !W_router || !W_gate || !W_up || !W_down || !out)
+  if (!x || !residual || (given ? !given->idx || !given->w : !W_router) || !W_gate || !W_up || !W_down || !out)
     return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
   const int eb = elem_bytes(dtype);
-  if (overlaps(x, static_cast<size_t>(T * d * eb), out, static_cast<size_t>(T * d * eb)))
-    return fail(MOE_ERR_INVALID_ARG, "out overlaps x");
+  for (const void* in : {x, residual})
+    if (overlaps(in, static_cast<size_t>(T * d * eb), out, static_cast<size_t>(T * d * eb)))
+      return fail(MOE_ERR_INVALID_ARG, "out overlaps x or residual");
   if (T == 0) return MOE_OK;
   const LayerPlan need = plan_layer(nullptr, T, d, d_ff, E, k, C, P, eb);
   if (!workspace || workspace_bytes < need.bytes || reinterpret_cast<uintptr_t>(workspace) % kAlign)
@@ -451,8 +465,8 @@ int moe_layer_forward(const void* x, const void* W_router, const float* router_b
   moe_stats_t none;
   std::memset(&none, 0, sizeof(none));
   const moe_stats_t& S = stats ? *stats : none;
-  int32_t* idx = pick(S.topk_idx, p.idx);
-  float* w = pick(S.topk_w, p.w);
+  int32_t* idx = given ? const_cast<int32_t*>(given->idx) : pick(S.topk_idx, p.idx);  // a given routing is only read
+  float* w = given ? const_cast<float*>(given->w) : pick(S.topk_w, p.w);
   int32_t* slot = pick(S.slot, p.slot);
   int32_t* routed = pick(S.routed_count, p.routed);
   int32_t* kept = pick(S.kept_count, p.kept);
@@ -465,22 +479,24 @@ int moe_layer_forward(const void* x, const void* W_router, const float* router_b
   const int bm = moe::grouped_gemm_bm_down(bf16, C, d_ff);
 
   const int splits = moe::router_splits(T, d, E, bf16);
-  MOE_HIP_TRY(stage_mark(MOE_STAGE_ROUTER, false, s), "event");
-  MOE_HIP_TRY(moe::launch_router_logits(x, W_router, T, d, E, bf16, splits, p.logits, s), "router logits");
-  MOE_HIP_TRY(stage_mark(MOE_STAGE_ROUTER, true, s), "event");
-  MOE_HIP_TRY(stage_mark(MOE_STAGE_ROUTE, false, s), "event");
-  const bool fused_hist = moe::route_builds_histogram(k, E, T);
+  MOE_HIP_TRY(stage_mark(MOE_STAGE_ROUTER, false, s, given != nullptr), "event");
+  if (!given)
+    MOE_HIP_TRY(moe::launch_router_logits(x, W_router, T, d, E, bf16, splits, p.logits, s), "router logits");
+  MOE_HIP_TRY(stage_mark(MOE_STAGE_ROUTER, true, s, given != nullptr), "event");
+  MOE_HIP_TRY(stage_mark(MOE_STAGE_ROUTE, false, s, given != nullptr), "event");
+  const bool fused_hist = !given && moe::route_builds_histogram(k, E, T);
   const int64_t nt = moe::ceil_div(T, moe::kTileTokens);
   // short tile histograms: the scan runs beside the slots and the row copies,
   // which count fully dropped tokens into totals[1], zeroed by the histogram's kernel
   const bool one_pass = moe::slot_scatter_fits(T, k, E);
   int64_t* zero_t1 = one_pass ? totals + 1 : nullptr;
   // the tile histogram comes with each copy's rank within its tile, kept in slot
-  MOE_HIP_TRY(moe::launch_route(p.logits, splits, router_bias, T, E, k, nullptr, idx, w,
-                                fused_hist ? p.tile_cnt : nullptr, P, max_ranks, s, fused_hist ? slot : nullptr,
-                                fused_hist ? zero_t1 : nullptr),
-              "route");
-  MOE_HIP_TRY(stage_mark(MOE_STAGE_ROUTE, true, s), "event");
+  if (!given)
+    MOE_HIP_TRY(moe::launch_route(p.logits, splits, router_bias, T, E, k, nullptr, idx, w,
+                                  fused_hist ? p.tile_cnt : nullptr, P, max_ranks, s, fused_hist ? slot : nullptr,
+                                  fused_hist ? zero_t1 : nullptr),
+                "route");
+  MOE_HIP_TRY(stage_mark(MOE_STAGE_ROUTE, true, s, given != nullptr), "event");
   // the scan also writes the counts, totals and both GEMMs' row-tile maps;
   // slots are the tile offsets plus the ranks
   const int bm_gu = moe::grouped_gemm_bm_gate_up(bf16, C, d);
@@ -539,9 +555,33 @@ int moe_layer_forward(const void* x, const void* W_router, const float* router_b
               "grouped gemm (down)");
   MOE_HIP_TRY(stage_mark(MOE_STAGE_DOWN, true, s), "event");
   MOE_HIP_TRY(stage_mark(MOE_STAGE_COMBINE, false, s), "event");
-  MOE_HIP_TRY(moe::launch_combine(x, p.y, idx, w, slot, T, d, k, E, C, bf16, out, s), "combine");
+  MOE_HIP_TRY(moe::launch_combine(residual, p.y, idx, w, slot, T, d, k, E, C, bf16, out, s), "combine");
   MOE_HIP_TRY(stage_mark(MOE_STAGE_COMBINE, true, s), "event");
   return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_layer_forward(const void* x, const void* W_router, const float* router_bias,
+                      const void* W_gate, const void* W_up, const void* W_down, int64_t T,
+                      int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P,
+                      int32_t max_ranks, moe_dtype_t dtype, void* out, moe_stats_t* stats,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  return layer_forward(x, x, nullptr, W_router, router_bias, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, max_ranks,
+                       dtype, out, stats, workspace, workspace_bytes, stream);
+}
+
+int moe_layer_forward_routed(const void* x, const void* residual, const int32_t* topk_idx, const float* topk_w,
+                             const void* W_gate, const void* W_up, const void* W_down, int64_t T, int64_t d,
+                             int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P, moe_dtype_t dtype, void* out,
+                             moe_stats_t* stats, void* workspace, size_t workspace_bytes, void* stream) {
+  if (stats && (stats->topk_idx || stats->topk_w))
+    return fail(MOE_ERR_INVALID_ARG, "the routing is given: stats takes no topk_idx and topk_w");
+  const Routing given = {topk_idx, topk_w, nullptr};
+  return layer_forward(x, residual, &given, nullptr, nullptr, W_gate, W_up, W_down, T, d, d_ff, E, k, cf, P, 0, dtype,
+                       out, stats, workspace, workspace_bytes, stream);
 }
 
 int moe_backward_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P,
@@ -560,7 +600,9 @@ namespace {
 
 // The backward; with `saved` (a kept forward state) the routing, buckets and
 // activations are taken from it instead of being recomputed.
-int layer_backward(const void* x, const void* W_router, const float* router_bias, const void* W_gate,
+// With `given` the routing is the caller's: dx has the experts' part alone, and the
+// router's gradients are not taken.
+int layer_backward(const void* x, const Routing* given, const void* W_router, const float* router_bias, const void* W_gate,
                    const void* W_up, const void* W_down, const void* dout, int64_t T, int64_t d, int64_t d_ff,
                    int32_t E, int32_t k, float cf, int32_t P, int32_t max_ranks, moe_dtype_t dtype,
                    const moe_stats_t* saved, void* dx, void* dW_router, float* d_bias, void* dW_gate, void* dW_up,
@@ -569,10 +611,10 @@ int layer_backward(const void* x, const void* W_router, const float* router_bias
   int st = check_layer_shape(T, d, d_ff, E, k, cf, P, dtype, &C);
   if (st != MOE_OK) return st;
   if ((st = check_rank_limit(E, k, P, max_ranks)) != MOE_OK) return st;
-  if (!x || !W_router || !W_gate || !W_up || !W_down || !dout || !dx || !dW_router || !dW_gate || !dW_up ||
-      !dW_down)
+  if (!x || !W_gate || !W_up || !W_down || !dout || !dx || !dW_gate || !dW_up || !dW_down ||
+      (given ? !given->idx || !given->w || !given->dw : !W_router || !dW_router))
     return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
-  if (saved && (!saved->topk_idx || !saved->topk_w || !saved->buckets || !saved->g || !saved->u || !saved->h))
+  if (saved && ((!given && (!saved->topk_idx || !saved->topk_w)) || !saved->buckets || !saved->g || !saved->u || !saved->h))
     return fail(MOE_ERR_INVALID_ARG, "saved state needs topk_idx, topk_w, buckets, g, u and h");
   const int eb = elem_bytes(dtype);
   const size_t row_bytes = static_cast<size_t>(T * d * eb);
@@ -598,15 +640,15 @@ int layer_backward(const void* x, const void* W_router, const float* router_bias
   // 1. the forward again: routing, buckets X, g, u, h (y is not needed: the
   //    gate gradients come from dh and h, step 4); with a kept state only the
   //    counts, slots and per-expert copy lists, from its routing
-  int32_t* idx = saved ? saved->topk_idx : p.idx;
-  float* w = saved ? saved->topk_w : p.w;
+  int32_t* idx = given ? const_cast<int32_t*>(given->idx) : saved ? saved->topk_idx : p.idx;  // given: only read
+  float* w = given ? const_cast<float*>(given->w) : saved ? saved->topk_w : p.w;
   void* X = saved ? saved->buckets : p.buckets;
   void* g = saved ? saved->g : b.g;
   void* u = saved ? saved->u : b.u;
   void* h = saved ? saved->h : p.h;
   const int splits = moe::router_splits(T, d, E, bf16);
-  const bool fused_hist = !saved && moe::route_builds_histogram(k, E, T);
-  if (!saved) {
+  const bool fused_hist = !given && !saved && moe::route_builds_histogram(k, E, T);
+  if (!given && !saved) {
     MOE_HIP_TRY(moe::launch_router_logits(x, W_router, T, d, E, bf16, splits, p.logits, s), "router logits");
     MOE_HIP_TRY(moe::launch_route(p.logits, splits, router_bias, T, E, k, nullptr, idx, w,
                                   fused_hist ? p.tile_cnt : nullptr, P, max_ranks, s),
@@ -677,13 +719,21 @@ int layer_backward(const void* x, const void* W_router, const float* router_bias
                 "gemm dX");
   }
   //    the gate gradients: q_j = <dh_j, h_j> = w_j <dout, y_j>, dl_j = q_j - w_j sum_i q_i
-  MOE_HIP_TRY(moe::launch_gate_grad(b.dh, h, idx, w, p.slot, T, F, k, C, bf16, b.dl, s), "gate gradients");
+  //    (with a given routing q_j itself, as with weights of 0, over w_j; dx then sums the expert paths alone)
+  if (given) MOE_HIP_TRY(moe::launch_zero(p.w, T * k, s), "zero");
+  MOE_HIP_TRY(moe::launch_gate_grad(b.dh, h, idx, given ? p.w : w, p.slot, T, F, k, C, bf16, b.dl, s),
+              "gate gradients");
+  if (given) {
+    MOE_HIP_TRY(moe::launch_weight_grad(b.dl, w, T * k, given->dw, s), "weights' gradients");
+    MOE_HIP_TRY(moe::launch_gather_copies(b.dX, idx, p.slot, T, d, k, C, bf16, dx, s), "gather dx");
+  } else {
   // 5. router gradients, then dx = dout + the expert paths + the router path
   MOE_HIP_TRY(moe::launch_router_wgrad(x, idx, b.dl, T, k, E, d, bf16, b.rpart, dW_router, d_bias, s, p.routed,
                                        b.route_off, b.lcopy, b.ltok),
               "router wgrad");
   MOE_HIP_TRY(moe::launch_gather_dx(dout, b.dX, W_router, idx, b.dl, p.slot, T, d, k, C, bf16, dx, s),
               "gather dx");
+  }
   // 6. weight gradients over each expert's kept rows: dWd = dy^T h, dWg = dg^T X,
   //    dWu = du^T X. bf16: both operands read K-major straight from the
   //    buckets, each expert contracting over its own kept rows.
@@ -731,7 +781,7 @@ int moe_layer_backward(const void* x, const void* W_router, const float* router_
                        int32_t E, int32_t k, float cf, int32_t P, int32_t max_ranks, moe_dtype_t dtype, void* dx,
                        void* dW_router, float* d_bias, void* dW_gate, void* dW_up, void* dW_down,
                        void* workspace, size_t workspace_bytes, void* stream) {
-  return layer_backward(x, W_router, router_bias, W_gate, W_up, W_down, dout, T, d, d_ff, E, k, cf, P, max_ranks,
+  return layer_backward(x, nullptr, W_router, router_bias, W_gate, W_up, W_down, dout, T, d, d_ff, E, k, cf, P, max_ranks,
                         dtype, nullptr, dx, dW_router, d_bias, dW_gate, dW_up, dW_down, workspace, workspace_bytes,
                         stream);
 }
@@ -743,9 +793,19 @@ int moe_layer_backward_saved(const void* x, const void* W_router, const float* r
                              void* dW_gate, void* dW_up, void* dW_down, void* workspace, size_t workspace_bytes,
                              void* stream) {
   if (!saved) return fail(MOE_ERR_INVALID_ARG, "saved is NULL");
-  return layer_backward(x, W_router, router_bias, W_gate, W_up, W_down, dout, T, d, d_ff, E, k, cf, P, max_ranks,
+  return layer_backward(x, nullptr, W_router, router_bias, W_gate, W_up, W_down, dout, T, d, d_ff, E, k, cf, P, max_ranks,
                         dtype, saved, dx, dW_router, d_bias, dW_gate, dW_up, dW_down, workspace, workspace_bytes,
                         stream);
+}
+
+int moe_layer_backward_routed(const void* x, const int32_t* topk_idx, const float* topk_w, const void* W_gate,
+                              const void* W_up, const void* W_down, const void* dout, int64_t T, int64_t d,
+                              int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P, moe_dtype_t dtype,
+                              const moe_stats_t* saved, void* dx, float* d_topk_w, void* dW_gate, void* dW_up,
+                              void* dW_down, void* workspace, size_t workspace_bytes, void* stream) {
+  const Routing given = {topk_idx, topk_w, d_topk_w};
+  return layer_backward(x, &given, nullptr, nullptr, W_gate, W_up, W_down, dout, T, d, d_ff, E, k, cf, P, 0, dtype,
+                        saved, dx, nullptr, nullptr, dW_gate, dW_up, dW_down, workspace, workspace_bytes, stream);
 }
 
 int moe_replica_plan(const int32_t* routed_count, int32_t E, int32_t extra, int32_t* replicas) {
