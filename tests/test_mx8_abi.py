@@ -79,7 +79,7 @@ def back(**kw):
     (dict(dy=None), INVALID), (dict(h=None), INVALID), (dict(weight=None), INVALID), (dict(rstd=None), INVALID), (dict(dh=None), INVALID),
     (dict(dweight=None), INVALID), (dict(dy=FAKE + 8), INVALID), (dict(dh=FAKE * 6 + 8), INVALID), (dict(dh=FAKE + 128), INVALID),
     (dict(dh=FAKE * 2 + 128), INVALID), (dict(dh=FAKE * 5 + 128), INVALID), (dict(workspace=None), WORKSPACE),
-    (dict(workspace_bytes=1000), WORKSPACE), (dict(workspace=FAKE * 8 + 128), WORKSPACE), (dict(R=1 << 26), UNSUPPORTED)])
+    (dict(workspace_bytes=255), WORKSPACE), (dict(workspace=FAKE * 8 + 128), WORKSPACE), (dict(R=1 << 26), UNSUPPORTED)])
 def test_norm_backward_refusals(kw, status):
     refused(status, lambda: back(**kw))
 
