@@ -82,6 +82,22 @@ def test_scores_that_fp32_cannot_tell_apart():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("step", [2.0 ** -e for e in (27, 24, 22, 21, 20, 19, 18, 17, 16, 14)])
+def test_scores_that_lie_close(step, score):
+    """Values in random order, steps apart that fp32 cannot, can hardly and can tell: the order is that of 64 bits."""
+    rng = np.random.default_rng(8)
+    l = (0.5 * rng.standard_normal((40, 256))).astype(np.float32)
+    s = ref.scores(l[:1], score)
+    for level in (0.5, 40.0):
+        bias = (level + step * rng.permutation(256) - s[0]).astype(np.float32)   # the first row's values: level + steps
+        for kw in ({}, dict(groups=8, top_groups=4, group_best=2), dict(groups=16, top_groups=3)):
+            check(l, 8, bias, score=score, scale=1.5, **kw)
+    near = (np.round(l / step) * step).astype(np.float32)
+    check(near, 8, score=score)
+    check(near, 8, score=score, groups=8, top_groups=2, group_best=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_masked_rows_and_large_logits(score, renormalize):
     rng = np.random.default_rng(6)
