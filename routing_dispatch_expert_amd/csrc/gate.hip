@@ -28,11 +28,6 @@ __device__ inline uint64_t order_of(double v) {
   return v != v ? 1 : key;
 }
 
-template <typename V>
-__device__ inline V shfl_xor64(V v, int off) {
-  return __shfl_xor(v, off, 64);
-}
-
 __device__ inline double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
 // A word of the lane that many places below (or, from the last two, of the last
@@ -101,20 +96,37 @@ __device__ inline double first_max(double v, int k) {
   return m;
 }
 
+// The two largest (a >= b) of a lane's and another's.
+template <int CTRL>
+__device__ inline void join_two(double& a, double& b) {
+  const double oa = below<CTRL, 0xf>(a), ob = below<CTRL, 0xf>(b);
+  b = fmax(fmin(a, oa), fmax(b, ob));
+  a = fmax(a, oa);
+}
+
 // The order's inverse, for numbers.
 __device__ inline double number_of(uint64_t key) {
   return __longlong_as_double(static_cast<int64_t>(key >> 63 ? key & ~(uint64_t{1} << 63) : ~key));
 }
 
-// Lanes that share a group's experts when its value is formed: 64 over the
-// groups, rounded down to a power of two.
-__device__ inline int lanes_of_group(int groups) { return 1 << (31 - __clz(64 / groups)); }
+// What the host divides for the kernel (a division by a number known only at run
+// time takes some 30 instructions a wave; 8192 tokens, 8 groups of 32: 16.2 -> 15.0
+// us without them): the experts of a group, the logarithm of
+// the lanes that form a group's value (64 over the groups, rounded down to a power
+// of two) and 1 / per.
+struct GroupSplit {
+  int per, log_lanes;
+  float inv_per;
+  // The group of expert e: (e + 1/2) / per lies 1 / (2 per) or more from a whole
+  // number, and is off by less than 2^-21 E / per.
+  __device__ int of(int e) const { return static_cast<int>((e + 0.5f) * inv_per); }
+};
 
 // NE: scores a lane holds (E <= 64 NE). LDS: [waves][E] doubles with groups.
 template <int NE>
 __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
-                                                   GateRule g, int64_t T, int E, int k, int32_t* __restrict__ idx,
-                                                   float* __restrict__ w) {
+                                                   GateRule g, GroupSplit gs, int64_t T, int E, int k,
+                                                   int32_t* __restrict__ idx, float* __restrict__ w) {
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 6) + wave;
@@ -156,7 +168,7 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
     key[i] = e < E ? order_of(bias ? s[i] + static_cast<double>(bias[e]) : l[i]) : 0;
   }
   if (g.groups > 1) {
-    const int per = E / g.groups, lpg = lanes_of_group(g.groups), sub = lane % lpg, mine = lane / lpg;
+    const int per = gs.per, lpg = 1 << gs.log_lanes, sub = lane & (lpg - 1), mine = lane >> gs.log_lanes;
     double* v = smem + wave * E;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
@@ -175,22 +187,27 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
           b = x;
         }
       }
-    for (int off = 1; off < lpg; off <<= 1) {
-      const double oa = shfl_xor64(a, off), ob = shfl_xor64(b, off);
+    // joined over 2, 4, 8, 16 lanes: each with a lane of the other half, whose lanes agree (pairs, quads, mirrors)
+    if (lpg > 1) join_two<0xb1>(a, b);
+    if (lpg > 2) join_two<0x4e>(a, b);
+    if (lpg > 4) join_two<0x141>(a, b);
+    if (lpg > 8) join_two<0x140>(a, b);
+    if (lpg > 16) {
+      const double oa = __shfl_xor(a, 16, 64), ob = __shfl_xor(b, 16, 64);
       b = fmax(fmin(a, oa), fmax(b, ob));
       a = fmax(a, oa);
     }
     const uint64_t value = order_of(g.best > 1 ? a + b : a);
     int ahead = 0;  // groups that are better, or as good and before this one
     for (int o = 0; o < g.groups; ++o) {
-      const uint64_t ov = lane_word(value, o * lpg);
+      const uint64_t ov = lane_word(value, o << gs.log_lanes);
       ahead += (ov > value || (ov == value && o < mine)) ? 1 : 0;
     }
     const uint64_t kept = __ballot(mine < g.groups && ahead < g.top_groups);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const int e = lane + 64 * i;
-      if (e < E && !((kept >> (e / per * lpg)) & 1)) key[i] = 0;
+      if (e < E && !((kept >> (gs.of(e) << gs.log_lanes)) & 1)) key[i] = 0;
     }
   }
   // Each lane's keys in order, of equal ones the lower expert first: a choice is then the best of the lanes' heads.
@@ -398,8 +415,10 @@ hipError_t launch_gate(const float* logits, const float* bias, const GateRule& g
                        float* w, hipStream_t s) {
   const int waves = E <= 1024 ? 4 : 1;  // at most 32 KiB of LDS
   const dim3 grid(static_cast<unsigned>(ceil_div(T, waves)));
+  const int per = E / g.groups;
+  const GroupSplit gs{per, 31 - __builtin_clz(64 / g.groups), 1.f / per};
   const size_t lds = g.groups > 1 ? waves * static_cast<size_t>(E) * sizeof(double) : 0;
-#define MOE_CALL(NE) gate_kernel<NE><<<grid, dim3(64 * waves), lds, s>>>(logits, bias, g, T, E, k, idx, w)
+#define MOE_CALL(NE) gate_kernel<NE><<<grid, dim3(64 * waves), lds, s>>>(logits, bias, g, gs, T, E, k, idx, w)
   MOE_GATE_BY_E(MOE_CALL);
 #undef MOE_CALL
   return hipGetLastError();

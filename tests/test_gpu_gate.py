@@ -81,6 +81,21 @@ def test_scores_that_fp32_cannot_tell_apart():
     assert r["topk_idx"].cpu().tolist() == [list(range(63, 55, -1))]
 
 
+@pytest.mark.parametrize("G,E", [(2, 64), (2, 8), (2, 130), (3, 48), (4, 64), (5, 80), (8, 64), (9, 72), (16, 64), (32, 64)])
+def test_the_two_largest_of_a_group_wherever_they_lie(G, E):
+    """One token per pair of places: group 1 wins by the sum of exactly these two, group 0 has the one largest."""
+    per = E // G
+    pairs = [(a, c) for a in range(per) for c in range(a)]
+    l = np.full((len(pairs), E), -2.0, np.float32)
+    l[:, 0] = 2.0                             # sigmoid: 0.881 + 0.119 in group 0
+    for t, (a, c) in enumerate(pairs):
+        l[t, per + a], l[t, per + c] = 1.0, 0.5   # 0.731 + 0.622 in group 1
+    r = check(l, 2, score="sigmoid", groups=G, top_groups=1, group_best=2)
+    assert np.array_equal(r["topk_idx"].cpu().numpy(), [[per + a, per + c] for a, c in pairs])
+    r = check(l, 2, score="sigmoid", groups=G, top_groups=1)   # by the largest alone
+    assert np.all(r["topk_idx"].cpu().numpy()[:, 0] == 0)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("step", [2.0 ** -e for e in (27, 24, 22, 21, 20, 19, 18, 17, 16, 14)])
 def test_scores_that_lie_close(step, score):
