@@ -65,7 +65,10 @@ struct ExpertsMx8 {
   int32_t *tile_cnt, *tile_off;  // [ceil(T / kTileTokens)][E]
   Mx8Ptr h;        // rows [T k][f]
   void* y;         // [T k][d]
+  float* parts;    // mx8_parts_bytes(T k, min(E, T k), f), or NULL
 };
+// Sums of down's split tiles (mx8_tiles.hip); 0 where none can be.
+int64_t mx8_parts_bytes(int64_t copies, int64_t experts, int64_t K);
 hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s);
 
 // ---- the layer with a given routing (routed.hip) ----

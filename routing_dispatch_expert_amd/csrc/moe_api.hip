@@ -1565,6 +1565,7 @@ struct ExpertsPlan {
   moe::Mx8Ptr h;
   int32_t *slot, *routed, *kept, *tile_cnt, *tile_off;
   void* y;
+  float* parts;
   size_t bytes;
 };
 
@@ -1586,6 +1587,9 @@ ExpertsPlan plan_experts_mx8(void* ws, int64_t T, int64_t d, int64_t d_ff, int32
   p.h.codes = c.take<uint8_t>(n * d_ff);
   p.h.scale = c.take<uint32_t>(mx8_scale_bytes(1, n, d_ff) / 4);
   p.y = c.take<char>(n * d * eb);
+  const int64_t parts = n ? moe::mx8_parts_bytes(n, std::min<int64_t>(E, n), d_ff) : 0;
+  p.parts = c.take<float>(parts / 4);
+  if (!parts) p.parts = nullptr;
   p.bytes = align_up(c.off);
   return p;
 }
@@ -1669,6 +1673,7 @@ int moe_experts_mx8(const moe_mx8_t* x, const void* residual, const int32_t* top
   L.tile_off = p.tile_off;
   L.h = p.h;
   L.y = p.y;
+  L.parts = p.parts;
   MOE_HIP_TRY(moe::launch_experts_mx8(L, static_cast<hipStream_t>(stream)), "8-bit experts");
   return MOE_OK;
 }

@@ -38,10 +38,12 @@ struct Mx8Gemm {
   int64_t H;
   void* y;            // else: [copies][N]
   bool y_bf16;
+  float* parts;       // or NULL: of down's tiles of 256 rows that are split over K
 };
 
 // Many rows an expert (mx8_tiles.hip): row tiles of mx8_tile_rows() rows, by the rows
 // that the experts have on average, listed in ls.tile. Grid: at most `tiles` of them.
+// parts: as mx8_parts_bytes() says (block.h).
 int mx8_tile_rows(int64_t copies, int64_t experts);
 hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, int tile_rows, hipStream_t s);
 

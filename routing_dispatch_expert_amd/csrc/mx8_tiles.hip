@@ -57,17 +57,44 @@ __device__ inline void interleave() {
 
 constexpr int kFeatureGroup = 8;  // feature tiles that go through an expert's row tiles together (shared in L2)
 
-// Block b of the live tiles: XCD b % 8 takes a contiguous eighth of them.
+// XCD x takes the x-th contiguous eighth of the live tiles. Its units take 32 of them
+// at a time (a block has a unit's LDS to itself), and the rest of them leaves units
+// idle for a whole tile: with many columns each of the rest is split over K between
+// `parts` blocks, which leave fp32 sums for join_parts_kernel. In turn on one card,
+// d = 4096, d_ff = 14336, 2 of 8 experts: 4096 tokens (72 tiles an XCD, the last 8 in
+// four parts) 1685 -> 1600 us in all, 512 tokens 470 -> 423.
+struct Split {
+  int64_t per, whole;  // tiles of an XCD; those before `whole` are not split
+  int parts;
+};
+constexpr int kUnits = 32;       // of an XCD
+constexpr int kPartFloats = 256 * 256;
+
+// A part has 16 stages of 128 columns or more, and is 32 shorter than the tile at
+// least (60 us; what it writes and what the join reads take 20 to 25).
+__host__ __device__ inline Split split_of(int64_t live, int64_t steps) {
+  Split s{(live + 7) / 8, (live + 7) / 8, 1};
+  const int64_t rest = s.per % kUnits;
+  if (rest == 0) return s;
+  const int64_t parts = kUnits / rest < steps / 16 ? kUnits / rest : steps / 16;
+  if (parts < 2 || steps - (steps + parts - 1) / parts < 32) return s;
+  s.whole = s.per - rest;
+  s.parts = static_cast<int>(parts);
+  return s;
+}
+
 struct Tile {
   int e, row0, rows;  // rows of the expert's list
   int64_t n0;
 };
 
-__device__ inline bool tile_of_block(const ExpertLists& ls, int E, int row_tile, int feature_tile, int64_t N, Tile* t) {
+__device__ inline int64_t live_tiles(const ExpertLists& ls, int E, int feature_tile, int64_t N) {
+  return static_cast<int64_t>(ls.tile[E]) * ((N + feature_tile - 1) / feature_tile);
+}
+
+__device__ inline bool tile_at(const ExpertLists& ls, int E, int feature_tile, int64_t N, int64_t id, Tile* t) {
   const int ft = static_cast<int>((N + feature_tile - 1) / feature_tile);
-  const int64_t live = static_cast<int64_t>(ls.tile[E]) * ft, per = (live + 7) / 8;
-  const int64_t at = blockIdx.x / 8, id = blockIdx.x % 8 * per + at;
-  if (at >= per || id >= live) return false;
+  if (id >= static_cast<int64_t>(ls.tile[E]) * ft) return false;
   const int rt = static_cast<int>(id / ft);
   int lo = 0, hi = E;  // tile[lo] <= rt < tile[hi]
   while (hi - lo > 1) {
@@ -96,7 +123,8 @@ __device__ inline bool tile_of_block(const ExpertLists& ls, int E, int row_tile,
 // a wave (2048 clocks), 128 KiB of LDS read and 66 written, which together with
 // its loads' way through the L2 bounds it: 1.9 us a stage where the products alone
 // take 1.0 at the clock that they leave (4.25 PFLOP/s in registers). Mixtral-shaped,
-// 4096 tokens: gate and up 1.07 - 1.12 ms (1.92 TFLOP: 1.75 PFLOP/s), down 0.65.
+// 4096 tokens: gate and up 1.07 - 1.12 ms (1.92 TFLOP: 1.75 PFLOP/s), down 0.51
+// - 0.55 and 0.016 for the join of its split tiles (0.65 without the split).
 // Measured and dropped: 2 x 4 waves of 4 x 2 tiles (256 registers do not hold them:
 // twice the time), 128 features a block (down 0.81 ms), a word of each weight line
 // asked for two stages before (down 0.61 ms, but 64 rows an expert 12% more).
@@ -115,15 +143,31 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   __shared__ uint4 As0[MA * 8], As1[MA * 8], As2[THIRD ? MA * 8 : 1], Xs0[MX * 8], Xs1[MX * 8], Xs2[THIRD ? MX * 8 : 1];
   __shared__ uint32_t Sc0[MA + MX], Sc1[MA + MX], Sc2[THIRD ? MA + MX : 1];
 
+  constexpr bool SPLIT = !GU && MA == 256 && MX == 256;
+  const int64_t xcd = blockIdx.x % 8, all_steps = ceil_div(a.K, 128), live_all = live_tiles(a.ls, E, FB, a.N);
+  int64_t at = blockIdx.x / 8, first_step = 0, end_step = all_steps;
+  int part_slot = -1;
+  Split sp{(live_all + 7) / 8, (live_all + 7) / 8, 1};
+  if constexpr (SPLIT) {
+    if (a.parts) sp = split_of(live_all, all_steps);
+    if (at >= sp.whole && sp.parts > 1) {
+      const int64_t o = at - sp.whole, p = o % sp.parts;
+      if (o >= (sp.per - sp.whole) * sp.parts) return;
+      at = sp.whole + o / sp.parts;
+      part_slot = __builtin_amdgcn_readfirstlane(static_cast<int>(xcd * kUnits + o));
+      first_step = __builtin_amdgcn_readfirstlane(static_cast<int>(all_steps * p / sp.parts));
+      end_step = __builtin_amdgcn_readfirstlane(static_cast<int>(all_steps * (p + 1) / sp.parts));
+    }
+  }
   Tile tl;
-  if (!tile_of_block(a.ls, E, MX, FB, a.N, &tl)) return;
+  if (at >= sp.per || !tile_at(a.ls, E, FB, a.N, xcd * sp.per + at, &tl)) return;
   const int e = __builtin_amdgcn_readfirstlane(tl.e);
   const int rows = __builtin_amdgcn_readfirstlane(tl.rows);
   const int first = __builtin_amdgcn_readfirstlane(a.ls.off[e] + tl.row0);  // row of the lists
   const int64_t n0 = __builtin_amdgcn_readfirstlane(static_cast<int>(tl.n0));
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN, lr = lane & 31, lq = lane >> 5;
-  const int64_t K = a.K, N = a.N, steps = ceil_div(K, 128);
+  const int64_t K = a.K, N = a.N, steps = end_step - first_step;  // stages are counted from the block's first
 
   // Row r of the block's A operand is this feature of this matrix. Past the matrix its last 16 rows stand in (N is a
   // multiple of 16, so eight rows that are loaded together are all in it or all past it): a load's common offset is
@@ -152,9 +196,9 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   static_assert(PA % 2 == 0 && PX % 2 == 0, "a wave's DMA instructions begin with an even one");
   // the scales: rows 64 (PS wave + i) + lane of A's (of one matrix: TM % 4 == 0), then of x's
   static_assert(!GU || TM % 4 == 0, "64 rows of A are of one matrix");
-  const int64_t sbytes = steps * N * 4;
-  const auto rs0 = rsrc(a.a0.scale + e * steps * N, sbytes), rs1 = rsrc(a.a1.scale + e * steps * N, sbytes);
-  const auto rsx = rsrc(a.x.scale, steps * a.R * 4);
+  const int64_t sbytes = all_steps * N * 4;
+  const auto rs0 = rsrc(a.a0.scale + e * all_steps * N, sbytes), rs1 = rsrc(a.a1.scale + e * all_steps * N, sbytes);
+  const auto rsx = rsrc(a.x.scale, all_steps * a.R * 4);
   uint32_t vs[PS];
 #pragma unroll
   for (int i = 0; i < PS; ++i) {
@@ -162,6 +206,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
     vs[i] = static_cast<uint32_t>(4 * (r < MA ? feature(r + lane) : x_row(r + lane - MA)));
   }
   auto dma = [&](uint4* as, uint4* xs, uint32_t* sc, int64_t s) {
+    s += first_step;
     const int k0 = static_cast<int>(s * 128);
     // pieces past the last column: zero (an offset past the buffer)
     const bool in[2] = {k0 + piece[0] < K, k0 + piece[1] < K};
@@ -228,7 +273,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
     };
     auto sready = [&](int64_t s) {
       if constexpr (TX > 0) {
-        const int64_t groups = ceil_div(K - s * 128, 32);  // with columns; bytes past them may be anything
+        const int64_t groups = ceil_div(K - (first_step + s) * 128, 32);  // with columns; bytes past them may be anything
         const uint32_t mask = groups >= 4 ? ~0u : (1u << (8 * groups)) - 1;
         auto fix = [&](uint32_t v) { return ((v & mask) | (0x7f7f7f7fu & ~mask)) >> (8 * lq); };
 #pragma unroll
@@ -327,6 +372,19 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   else
     loop(std::integral_constant<int, 0>{});
 
+  if constexpr (SPLIT)
+    if (part_slot >= 0) {
+      f32x4* p = reinterpret_cast<f32x4*>(a.parts + static_cast<int64_t>(part_slot) * kPartFloats) + wave * TM * TN * 256 + lane;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        if ((wn * TN + j) * 32 < rows)
+#pragma unroll
+          for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              p[((i * TN + j) * 4 + g) * 64] = f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+      return;
+    }
   const int64_t nw = n0 + wm * FW;  // the wave's first feature
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
@@ -393,10 +451,39 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
 #endif
 }
 
+// The split tiles' rows of y: their parts' sums, in order. Sixteen blocks a tile, of
+// the XCD whose L2 has the parts.
+__global__ __launch_bounds__(256) void join_parts_kernel(Mx8Gemm a, int E) {
+  const int64_t xcd = blockIdx.x % 8, r = blockIdx.x / 8 / 16, chunk = blockIdx.x / 8 % 16;
+  const Split sp = split_of(live_tiles(a.ls, E, 256, a.N), ceil_div(a.K, 128));
+  Tile tl;
+  if (sp.parts < 2 || r >= sp.per - sp.whole || !tile_at(a.ls, E, 256, a.N, xcd * sp.per + sp.whole + r, &tl)) return;
+  const f32x4* parts = reinterpret_cast<const f32x4*>(a.parts + (xcd * kUnits + r * sp.parts) * kPartFloats);
+  const int first = a.ls.off[tl.e] + tl.row0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    // as the product's waves (two by two of 4 x 4 tiles) left them
+    const int v = static_cast<int>(chunk * 1024) + q * 256 + threadIdx.x;
+    const int lane = v & 63, g = v >> 6 & 3, j = v >> 8 & 3, i = v >> 10 & 3, wave = v >> 12;
+    const int c = ((wave & 1) * 4 + j) * 32 + (lane & 31);
+    const int64_t f = tl.n0 + (wave >> 1) * 128 + 32 * i + 8 * g + 4 * (lane >> 5);
+    if (c >= tl.rows || f >= a.N) continue;
+    f32x4 sum = parts[v];
+    for (int p = 1; p < sp.parts; ++p) sum += parts[static_cast<int64_t>(p) * (kPartFloats / 4) + v];
+    const int64_t at = static_cast<int64_t>(a.ls.copy[first + c]) * a.N + f;
+    if (a.y_bf16)
+      *reinterpret_cast<uint2*>(static_cast<bf16_t*>(a.y) + at) =
+          uint2{f32_to_bf16(sum[0]) | static_cast<uint32_t>(f32_to_bf16(sum[1])) << 16,
+                f32_to_bf16(sum[2]) | static_cast<uint32_t>(f32_to_bf16(sum[3])) << 16};
+    else
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = sum;
+  }
+}
+
 template <bool GU, int WM, int WN, int TM, int TN, int NS>
 hipError_t launch(const Mx8Gemm& a, int E, int64_t tiles, hipStream_t s) {
   const int64_t ft = ceil_div(a.N, WM * (GU ? TM / 2 : TM) * 32);
-  const dim3 grid(static_cast<unsigned>(ceil_div(tiles * ft, 8) * 8));
+  const dim3 grid(static_cast<unsigned>((ceil_div(tiles * ft, 8) + (a.parts ? kUnits : 0)) * 8));
   mx8_tile_kernel<GU, WM, WN, TM, TN, NS><<<grid, dim3(WM * WN * 64), 0, s>>>(a, E);
   return hipGetLastError();
 }
@@ -411,9 +498,21 @@ hipError_t launch(const Mx8Gemm& a, int E, int64_t tiles, hipStream_t s) {
 // instead of 497).
 int mx8_tile_rows(int64_t copies, int64_t experts) { return copies > 96 * experts ? 256 : 128; }
 
+int64_t mx8_parts_bytes(int64_t copies, int64_t experts, int64_t K) {
+  const int64_t steps = ceil_div(K, 128);
+  bool any = false;  // with some number of tiles
+  for (int rest = 1; rest <= kUnits; ++rest) any = any || split_of(8 * rest, steps).parts > 1;
+  return any && mx8_tile_rows(copies, experts) == 256 ? int64_t{8} * kUnits * kPartFloats * 4 : 0;
+}
+
 hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, int tile_rows, hipStream_t s) {
-  if (tile_rows == 256)
-    return gate_up ? launch<true, 2, 2, 4, 4, 2>(a, E, tiles, s) : launch<false, 2, 2, 4, 4, 2>(a, E, tiles, s);
+  if (tile_rows == 256) {
+    if (gate_up) return launch<true, 2, 2, 4, 4, 2>(a, E, tiles, s);
+    const hipError_t e = launch<false, 2, 2, 4, 4, 2>(a, E, tiles, s);
+    if (e != hipSuccess || !a.parts) return e;
+    join_parts_kernel<<<dim3(8 * 16 * (kUnits / 2)), dim3(256), 0, s>>>(a, E);
+    return hipGetLastError();
+  }
   return gate_up ? launch<true, 2, 2, 4, 2, 3>(a, E, tiles, s) : launch<false, 2, 2, 4, 2, 3>(a, E, tiles, s);
 }
 

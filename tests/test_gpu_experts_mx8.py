@@ -135,6 +135,53 @@ def test_steps_and_rules(T, d, f, E, k, cf, ints):
     run_case(T, d, f, E, k, cf, ints=ints)
 
 
+# down's tiles split over K: 48 steps (the fewest) to 65, whole and not, in two to four parts; rows that end inside a tile;
+# live tiles that are no multiple of eight
+DEEP = [(300, 272, 6160, 2, 1, 2.0, "bf16"), (220, 144, 6144, 1, 1, 1.0, "f32"), (700, 640, 8208, 4, 2, 0.7, "bf16"),
+        (260, 2064, 6400, 1, 1, 1.0, "f32"), (129, 528, 8192, 2, 2, 1.0, "bf16")]
+
+
+@pytest.mark.parametrize("ints", [True, False], ids=["whole", "gauss"])
+@pytest.mark.parametrize("T,d,f,E,k,cf,dtype", DEEP)
+def test_down_split_over_its_columns(T, d, f, E, k, cf, dtype, ints):
+    run_case(T, d, f, E, k, cf, dtype, ints=ints)
+
+
+@pytest.mark.parametrize("T", [4400, 4230])
+def test_whole_rounds_and_a_split_rest(T):
+    """288 and 272 tiles of down: 36 and 34 an XCD, of which 32 are whole. A sample of tokens against 64 bits, all of them
+    twice the same, and in a graph whose replays find other numbers in the workspace."""
+    d, f = 4096, 6144
+    rng = np.random.default_rng(T)
+    (xq, x), (gq, Wg), (uq, Wu), (dq, Wd) = (matrix(rng, s, True) for s in ((T, d), (1, f, d), (1, f, d), (1, d, f)))
+    idx = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    w = torch.full((T, 1), 0.5, device="cuda")
+    residual = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    run = lambda: moe.experts_mx8(xq, idx, w, gq, uq, dq, residual, 1.0)["out"]
+    say("experts, split rest", T, d, f)
+    out = run()
+    pick = np.unique(np.concatenate([rng.integers(0, T, 60), [0, 1, 255, 256, T - 257, T - 256, T - 2, T - 1]]))
+    g, u = x[pick] @ Wg[0].T, x[pick] @ Wu[0].T
+    h = g / (1 + np.exp(-g)) * u
+    either = np.abs(ref.values(h * (1 + 2.0 ** -21)) - ref.values(h * (1 - 2.0 ** -21)))
+    h = ref.values(h)
+    part, size, slack = (0.5 * v @ np.abs(Wd[0]).T if v is not h else 0.5 * h @ Wd[0].T for v in (h, np.abs(h), either))
+    off = (CUT + HALF["bf16"] + U * (1 + f / 64 + 8)) * (size + slack) + slack   # as run_case()
+    got = out.double().cpu().numpy()[pick]
+    bad = np.abs(got - part) > off + HALF["bf16"] * (np.abs(part) + off)
+    assert not bad.any(), f"{bad.sum()} of {bad.size}, first {np.argwhere(bad)[:5].tolist()}"
+    assert torch.equal(out, run())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = run()
+    for _ in range(3):
+        again.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, again)
+        run()
+
+
 @pytest.mark.parametrize("T,E", [(100, 64), (33, 64), (300, 4), (700, 8)])
 def test_one_expert_with_many_rows_among_experts_with_few(T, E):
     """Strips take such an expert 32 rows at a time, tiles by more of them."""
