@@ -38,12 +38,18 @@ struct Mx8Gemm {
   int64_t H;
   void* y;            // else: [copies][N]
   bool y_bf16;
-  float* parts;       // or NULL: of down's tiles of 256 rows that are split over K
+  float* parts;       // or NULL: of down's tiles that are split over K
 };
 
 // Many rows an expert (mx8_tiles.hip): row tiles of mx8_tile_rows() rows, by the rows
 // that the experts have on average, listed in ls.tile. Grid: at most `tiles` of them.
 // parts: as mx8_parts_bytes() says (block.h).
+// From 20 rows an expert on: by strips and by tiles of 128 rows, 8 experts of d = 4096,
+// d_ff = 14336 take 319 and 380 us with 16 rows each, 522 and 411 - 447 with 32; 256
+// of d = 7168, d_ff = 2048 2.52 and 2.40 ms with 16, 3.75 and 2.58 with 32; 64 of d =
+// 2048, d_ff = 1408 166 and 163 us with 24, 298 and 186 with 48 (before down's tiles
+// were split).
+inline bool mx8_many(int64_t copies, int64_t experts) { return copies > 20 * experts; }
 int mx8_tile_rows(int64_t copies, int64_t experts);
 hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, int tile_rows, hipStream_t s);
 

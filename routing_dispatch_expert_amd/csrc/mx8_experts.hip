@@ -468,10 +468,7 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   a.y = nullptr;
   a.y_bf16 = L.bf16;
   a.parts = nullptr;
-  // Row tiles from 20 rows an expert on: by strips and by tiles of 128 rows, 8 experts of d = 4096, d_ff = 14336 take
-  // 319 and 380 us with 16 rows each, 522 and 411 - 447 with 32; 256 of d = 7168, d_ff = 2048 2.52 and 2.40 ms with 16,
-  // 3.75 and 2.58 with 32; 64 of d = 2048, d_ff = 1408 166 and 163 us with 24, 298 and 186 with 48.
-  const bool many = copies > 20 * act;
+  const bool many = mx8_many(copies, act);
   const int64_t tiles = copies / tile_rows + act;
   auto few = [&](auto gu, const Mx8Gemm& g) {
     constexpr bool GU = decltype(gu)::value;

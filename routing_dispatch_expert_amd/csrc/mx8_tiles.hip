@@ -62,13 +62,14 @@ constexpr int kFeatureGroup = 8;  // feature tiles that go through an expert's r
 // idle for a whole tile: with many columns each of the rest is split over K between
 // `parts` blocks, which leave fp32 sums for join_parts_kernel. In turn on one card,
 // d = 4096, d_ff = 14336, 2 of 8 experts: 4096 tokens (72 tiles an XCD, the last 8 in
-// four parts) 1685 -> 1600 us in all, 512 tokens 470 -> 423.
+// four parts) 1700 -> 1610 us in all, 512 tokens 471 -> 425; with tiles of 128 rows
+// 256 tokens (16 tiles an XCD in two parts) 410 -> 363, 128 tokens 397 -> 347.
 struct Split {
   int64_t per, whole;  // tiles of an XCD; those before `whole` are not split
   int parts;
 };
 constexpr int kUnits = 32;       // of an XCD
-constexpr int kPartFloats = 256 * 256;
+constexpr int kPartFloats = 256 * 256;  // or half of them
 
 // A part has 16 stages of 128 columns or more, and is 32 shorter than the tile at
 // least (60 us; what it writes and what the join reads take 20 to 25).
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   __shared__ uint4 As0[MA * 8], As1[MA * 8], As2[THIRD ? MA * 8 : 1], Xs0[MX * 8], Xs1[MX * 8], Xs2[THIRD ? MX * 8 : 1];
   __shared__ uint32_t Sc0[MA + MX], Sc1[MA + MX], Sc2[THIRD ? MA + MX : 1];
 
-  constexpr bool SPLIT = !GU && MA == 256 && MX == 256;
+  constexpr bool SPLIT = !GU;
   const int64_t xcd = blockIdx.x % 8, all_steps = ceil_div(a.K, 128), live_all = live_tiles(a.ls, E, FB, a.N);
   int64_t at = blockIdx.x / 8, first_step = 0, end_step = all_steps;
   int part_slot = -1;
@@ -451,10 +452,13 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
 #endif
 }
 
-// The split tiles' rows of y: their parts' sums, in order. Sixteen blocks a tile, of
-// the XCD whose L2 has the parts.
+// The split tiles' rows of y: their parts' sums, in order. A block takes a sixteenth
+// of 256 rows' tile, on the XCD whose L2 has the parts. TN: 32-row blocks of a wave.
+template <int TN>
 __global__ __launch_bounds__(256) void join_parts_kernel(Mx8Gemm a, int E) {
-  const int64_t xcd = blockIdx.x % 8, r = blockIdx.x / 8 / 16, chunk = blockIdx.x / 8 % 16;
+  static_assert(TN == 2 || TN == 4, "tiles of 128 or 256 rows");
+  constexpr int CHUNKS = 4 * TN;
+  const int64_t xcd = blockIdx.x % 8, r = blockIdx.x / 8 / CHUNKS, chunk = blockIdx.x / 8 % CHUNKS;
   const Split sp = split_of(live_tiles(a.ls, E, 256, a.N), ceil_div(a.K, 128));
   Tile tl;
   if (sp.parts < 2 || r >= sp.per - sp.whole || !tile_at(a.ls, E, 256, a.N, xcd * sp.per + sp.whole + r, &tl)) return;
@@ -462,10 +466,10 @@ __global__ __launch_bounds__(256) void join_parts_kernel(Mx8Gemm a, int E) {
   const int first = a.ls.off[tl.e] + tl.row0;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    // as the product's waves (two by two of 4 x 4 tiles) left them
+    // as the product's waves (two by two of 4 x TN tiles) left them
     const int v = static_cast<int>(chunk * 1024) + q * 256 + threadIdx.x;
-    const int lane = v & 63, g = v >> 6 & 3, j = v >> 8 & 3, i = v >> 10 & 3, wave = v >> 12;
-    const int c = ((wave & 1) * 4 + j) * 32 + (lane & 31);
+    const int lane = v & 63, g = v >> 6 & 3, j = v / 256 % TN, i = v / (256 * TN) % 4, wave = v / (1024 * TN);
+    const int c = ((wave & 1) * TN + j) * 32 + (lane & 31);
     const int64_t f = tl.n0 + (wave >> 1) * 128 + 32 * i + 8 * g + 4 * (lane >> 5);
     if (c >= tl.rows || f >= a.N) continue;
     f32x4 sum = parts[v];
@@ -495,25 +499,26 @@ hipError_t launch(const Mx8Gemm& a, int E, int64_t tiles, hipStream_t s) {
 // slots, two stages under way (the same weights: 64 rows an expert of d = 7168,
 // d_ff = 2048 2.8 ms instead of 3.0, 32 rows 2.6 instead of 3.0; 96 rows of d = 4096,
 // d_ff = 14336 437 us instead of 491, 128 rows, which half the experts exceed, 537
-// instead of 497).
+// instead of 497; all before down's tiles were split).
 int mx8_tile_rows(int64_t copies, int64_t experts) { return copies > 96 * experts ? 256 : 128; }
 
 int64_t mx8_parts_bytes(int64_t copies, int64_t experts, int64_t K) {
   const int64_t steps = ceil_div(K, 128);
   bool any = false;  // with some number of tiles
   for (int rest = 1; rest <= kUnits; ++rest) any = any || split_of(8 * rest, steps).parts > 1;
-  return any && mx8_tile_rows(copies, experts) == 256 ? int64_t{8} * kUnits * kPartFloats * 4 : 0;
+  return any && mx8_many(copies, experts) ? int64_t{8} * kUnits * kPartFloats * 4 : 0;
 }
 
 hipError_t launch_mx8_tiles(const Mx8Gemm& a, bool gate_up, int E, int64_t tiles, int tile_rows, hipStream_t s) {
-  if (tile_rows == 256) {
-    if (gate_up) return launch<true, 2, 2, 4, 4, 2>(a, E, tiles, s);
-    const hipError_t e = launch<false, 2, 2, 4, 4, 2>(a, E, tiles, s);
-    if (e != hipSuccess || !a.parts) return e;
-    join_parts_kernel<<<dim3(8 * 16 * (kUnits / 2)), dim3(256), 0, s>>>(a, E);
-    return hipGetLastError();
-  }
-  return gate_up ? launch<true, 2, 2, 4, 2, 3>(a, E, tiles, s) : launch<false, 2, 2, 4, 2, 3>(a, E, tiles, s);
+  const bool tall = tile_rows == 256;
+  if (gate_up) return tall ? launch<true, 2, 2, 4, 4, 2>(a, E, tiles, s) : launch<true, 2, 2, 4, 2, 3>(a, E, tiles, s);
+  const hipError_t e = tall ? launch<false, 2, 2, 4, 4, 2>(a, E, tiles, s) : launch<false, 2, 2, 4, 2, 3>(a, E, tiles, s);
+  if (e != hipSuccess || !a.parts) return e;
+  if (tall)
+    join_parts_kernel<4><<<dim3(8 * 16 * (kUnits / 2)), dim3(256), 0, s>>>(a, E);
+  else
+    join_parts_kernel<2><<<dim3(8 * 8 * (kUnits / 2)), dim3(256), 0, s>>>(a, E);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -138,7 +138,10 @@ def test_steps_and_rules(T, d, f, E, k, cf, ints):
 # down's tiles split over K: 48 steps (the fewest) to 65, whole and not, in two to four parts; rows that end inside a tile;
 # live tiles that are no multiple of eight
 DEEP = [(300, 272, 6160, 2, 1, 2.0, "bf16"), (220, 144, 6144, 1, 1, 1.0, "f32"), (700, 640, 8208, 4, 2, 0.7, "bf16"),
-        (260, 2064, 6400, 1, 1, 1.0, "f32"), (129, 528, 8192, 2, 2, 1.0, "bf16")]
+        (260, 2064, 6400, 1, 1, 1.0, "f32"), (129, 528, 8192, 2, 2, 1.0, "bf16"),
+        # the same with tiles of 128 rows: 25 to 96 rows an expert
+        (50, 272, 6160, 2, 1, 2.0, "bf16"), (96, 144, 6144, 1, 1, 1.0, "f32"), (65, 640, 8208, 4, 2, 0.7, "bf16"),
+        (70, 2064, 6400, 2, 1, 2.0, "f32")]
 
 
 @pytest.mark.parametrize("ints", [True, False], ids=["whole", "gauss"])
