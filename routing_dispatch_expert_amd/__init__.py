@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from operator import index as _index
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_hip.so")
@@ -400,12 +401,18 @@ def moe_layer_forward_few_q4(x, W_router, router_bias, W_gate, W_up, W_down, T, 
 
 
 @functools.lru_cache(maxsize=64)
+def _gate_struct(score, groups, top_groups, group_best, renormalize, scale):
+    return ctypes.pointer(moe_gate_t(score, groups, top_groups, group_best, renormalize, scale))
+
+
 def _gate(gate) -> "ctypes.POINTER(moe_gate_t) | None":
-    """gate: None or (score, groups, top_groups, group_best, renormalize, scale)."""
+    """gate: None or (score, groups, top_groups, group_best, renormalize, scale). The
+    struct is remembered by plain numbers: a tensor is the same key whatever it holds."""
     if gate is None:
         return None
     score, groups, top_groups, group_best, renormalize, scale = gate
-    return ctypes.pointer(moe_gate_t(SCORES.get(score, score), groups, top_groups, group_best, int(renormalize), scale))
+    return _gate_struct(SCORES.get(score, score), _index(groups), _index(top_groups), _index(group_best), int(renormalize),
+                        float(scale))
 
 
 def moe_gate(logits, bias, gate, T, E, k, topk_idx, topk_w, stream=None):
