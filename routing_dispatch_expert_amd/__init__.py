@@ -888,6 +888,7 @@ def forward_few(x, W_router, W_gate, W_up, W_down, k, cf, P=1, router_bias=None,
     if router_bias is not None:
         _require(router_bias, "router_bias", torch.float32, (E,))
     _same_device(dev, "W_router W_gate W_up W_down router_bias", W_router, W_gate, W_up, W_down, router_bias)
+    k, cf, P = _index(k), float(cf), _index(P)   # as they are now: the key is held until a later call
     with _On(dev, stream) as on:
         key = (T, d, d_ff, E, k, cf, P, dt, q4, dev)
         if out is None:
@@ -976,6 +977,7 @@ def gate(logits, k, score="softmax", bias=None, groups=1, top_groups=0, group_be
     rule = _gate_rule(score, groups, top_groups, group_best, renormalize, scale)
     dev = logits.device
     _same_device(dev, "bias", bias)
+    k = _index(k)   # as it is now: the key is held until a later call
     key = ("gate", T, E, k, dev)
     with _on(dev, stream) as on:
         if out is None:
@@ -1049,6 +1051,7 @@ def forward_routed(x, topk_idx, topk_w, W_gate, W_up, W_down, cf, residual=None,
     which backward_routed(..., saved=result) takes instead of recomputing them. out:
     the result of an earlier call with the same sizes, whose tensors this call writes."""
     import torch
+    cf, P = float(cf), _index(P)   # as they are now: the key is held until a later call
     if residual is None:
         residual = x
     T, d, d_ff, E, k = _routed_shapes(x, topk_idx, topk_w, W_gate, W_up, W_down, {"residual": residual})
@@ -1084,6 +1087,7 @@ def backward_routed(x, topk_idx, topk_w, W_gate, W_up, W_down, dout, cf, P=1, sa
     forward_routed(..., keep_activations=True) on the same inputs. out: the result of
     an earlier call with the same sizes, whose tensors this call writes."""
     import torch
+    cf, P = float(cf), _index(P)
     T, d, d_ff, E, k = _routed_shapes(x, topk_idx, topk_w, W_gate, W_up, W_down, {"dout": dout})
     dt, dev = x.dtype, x.device
     if saved is not None and (not isinstance(saved, Result) or
@@ -1272,6 +1276,7 @@ def experts_mx8(x, topk_idx, topk_w, W_gate, W_up, W_down, residual, cf, out=Non
     for q, n, s in ((W_gate, "W_gate", (E, d_ff, d)), (W_up, "W_up", (E, d_ff, d)), (W_down, "W_down", (E, d, d_ff))):
         if q.shape != s:
             raise ValueError(f"{n}: need 8-bit weights of shape {s}, got {q.shape}")
+    cf = float(cf)   # as it is now: the key is held until a later call
     dt, dev = residual.dtype, x.device
     dtype = _dtype(dt)
     _need(residual, "residual", dt, (T, d))
@@ -1335,6 +1340,7 @@ def forward_mx8(x, norm_weight, W_router, W_gate, W_up, W_down, k, cf, residual=
     rule = _gate_rule(score, groups, top_groups, group_best, renormalize, scale)
     _same_device(dev, "norm_weight W_router W_gate W_up W_down residual bias", norm_weight, W_router, W_gate, W_up, W_down,
                  residual, bias)
+    k, cf = _index(k), float(cf)   # as they are now: the key is held until a later call
     key = ("forward_mx8", T, d, d_ff, E, k, cf, dt, dev, residual is not None)
     with _on(dev, stream) as on:
         if out is None:
