@@ -431,11 +431,11 @@ int moe_gate_backward(const float* logits, const int32_t* topk_idx, const float*
  * (topk_idx and topk_w NULL) and workspace as there. A topk_idx entry outside [0,
  * E) is dropped. out must not overlap x or residual, which may be one array.
  * moe_layer_backward_routed: from dout [T, d], dx [T, d] of the experts' path alone
- * (residual's gradient is dout), d_topk_w [T, k] fp32 = <dout[t], y[t,j]> (0 for a
- * dropped copy, and where topk_w is 0, where the experts' gradients hold no trace of
- * it), dW_gate, dW_up, dW_down. saved: NULL, or the stats of the forward on the
- * same inputs that kept buckets, g, u and h (then not recomputed). Else as
- * moe_layer_backward; workspace: moe_backward_workspace_size() bytes. */
+ * (residual's gradient is dout), d_topk_w [T, k] fp32 = <dout[t], y[t,j]>, whatever
+ * topk_w is (0 for a dropped copy), dW_gate, dW_up, dW_down. saved: NULL, or the
+ * stats of the forward on the same inputs that kept buckets, g, u and h (then not
+ * recomputed). Else as moe_layer_backward; workspace: moe_backward_workspace_size()
+ * bytes. */
 int moe_layer_forward_routed(const void* x, const void* residual, const int32_t* topk_idx, const float* topk_w,
                              const void* W_gate, const void* W_up, const void* W_down, int64_t T, int64_t d,
                              int64_t d_ff, int32_t E, int32_t k, float cf, int32_t P, moe_dtype_t dtype, void* out,

@@ -72,9 +72,11 @@ int64_t mx8_parts_bytes(int64_t copies, int64_t experts, int64_t K);
 hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s);
 
 // ---- the layer with a given routing (routed.hip) ----
-hipError_t launch_zero(float* p, int64_t n, hipStream_t s);
-// dw = q / w (0 where w is 0).
-hipError_t launch_weight_grad(const float* q, const float* w, int64_t n, float* dw, hipStream_t s);
+// The weights that dy = first dout is formed with: w, and 1 for weights of 0 and of unusual size.
+hipError_t launch_split_weights(const float* w, int64_t n, float* first, hipStream_t s);
+// dw = <dh, h> / first, 0 for a dropped copy; after it dh and dy have the whole weight.
+hipError_t launch_weight_grad(void* dh, const void* h, void* dy, const int32_t* idx, const float* w, const int32_t* slot,
+                              int64_t T, int64_t d, int64_t F, int k, int64_t C, bool bf16, float* dw, hipStream_t s);
 // dx[t] = sum_j [slot >= 0] dX[idx, slot].
 hipError_t launch_gather_copies(const void* dX, const int32_t* idx, const int32_t* slot, int64_t T, int64_t d, int k,
                                 int64_t C, bool bf16, void* dx, hipStream_t s);

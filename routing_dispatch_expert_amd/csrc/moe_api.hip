@@ -690,9 +690,14 @@ int layer_backward(const void* x, const Routing* given, const void* W_router, co
     MOE_HIP_TRY(moe::launch_swiglu_fwd(g, u, h, p.kept, E, C, F, bf16, s), "swiglu");
   }
 
-  // 2. combine backward: dy = w dout on kept rows
-  MOE_HIP_TRY(moe::launch_combine_bwd(dout, nullptr, idx, w, p.slot, T, d, k, C, bf16, b.dy, nullptr, s),
+  // 2. combine backward: dy = w dout on kept rows (with a given routing for weights of ordinary size, else dout)
+  if (given) MOE_HIP_TRY(moe::launch_split_weights(w, T * k, p.w, s), "weights");
+  MOE_HIP_TRY(moe::launch_combine_bwd(dout, nullptr, idx, given ? p.w : w, p.slot, T, d, k, C, bf16, b.dy, nullptr, s),
               "combine backward");
+  // a given routing's weights' gradients from dh, after which dh and dy are those of the whole weight
+  auto weight_grad = [&] {
+    return given ? moe::launch_weight_grad(b.dh, h, b.dy, idx, w, p.slot, T, d, F, k, C, bf16, given->dw, s) : hipSuccess;
+  };
   // 3. dh = dy Wd; dg, du. 4. dX = [dg | du] [Wg ; Wu]. Either straight from the
   //    weights (K-major B: Wd is [d][d_ff] = [K][N], Wg and Wu are [d_ff][d]),
   //    or through transposed copies (B = Wd^T [E][d_ff][d], [Wg^T | Wu^T] [E][d][2 d_ff]).
@@ -700,6 +705,7 @@ int layer_backward(const void* x, const Routing* given, const void* W_router, co
     MOE_HIP_TRY(moe::launch_gemm_kmajor_b(b.dy, p.kept, mtile_d_rows, W_down, nullptr, d, E, C, d, F, b.dh, s, sk,
                                           bm_d),
                 "gemm dh");
+    MOE_HIP_TRY(weight_grad(), "weights' gradients");
     MOE_HIP_TRY(moe::launch_swiglu_bwd(b.dh, g, u, b.dgu, p.kept, E, C, F, bf16, s), "swiglu backward");
     MOE_HIP_TRY(moe::launch_gemm_kmajor_b(b.dgu, p.kept, mtile_d_rows, W_gate, W_up, F, E, C, 2 * F, d, b.dX, s, sk,
                                           bm_d),
@@ -710,6 +716,7 @@ int layer_backward(const void* x, const Routing* given, const void* W_router, co
     MOE_HIP_TRY(moe::launch_gemm_down(b.dy, p.kept, mtile_d_rows, b.WdT, E, C, F, d, bf16, b.dh, s, nullptr, sk,
                                       bmo_d),
                 "gemm dh");
+    MOE_HIP_TRY(weight_grad(), "weights' gradients");
     MOE_HIP_TRY(moe::launch_swiglu_bwd(b.dh, g, u, b.dgu, p.kept, E, C, F, bf16, s), "swiglu backward");
     MOE_HIP_TRY(moe::launch_transpose(W_gate, b.WguT, E, F, d, d, 2 * F, 0, F, nullptr, F * d, d * 2 * F, bf16, s),
                 "transpose W_gate");
@@ -718,21 +725,17 @@ int layer_backward(const void* x, const Routing* given, const void* W_router, co
     MOE_HIP_TRY(moe::launch_gemm_down(b.dgu, p.kept, p.mtile, b.WguT, E, C, d, 2 * F, bf16, b.dX, s, nullptr, sk),
                 "gemm dX");
   }
-  //    the gate gradients: q_j = <dh_j, h_j> = w_j <dout, y_j>, dl_j = q_j - w_j sum_i q_i
-  //    (with a given routing q_j itself, as with weights of 0, over w_j; dx then sums the expert paths alone)
-  if (given) MOE_HIP_TRY(moe::launch_zero(p.w, T * k, s), "zero");
-  MOE_HIP_TRY(moe::launch_gate_grad(b.dh, h, idx, given ? p.w : w, p.slot, T, F, k, C, bf16, b.dl, s),
-              "gate gradients");
-  if (given) {
-    MOE_HIP_TRY(moe::launch_weight_grad(b.dl, w, T * k, given->dw, s), "weights' gradients");
+  if (given) {  // dx sums the expert paths alone
     MOE_HIP_TRY(moe::launch_gather_copies(b.dX, idx, p.slot, T, d, k, C, bf16, dx, s), "gather dx");
   } else {
-  // 5. router gradients, then dx = dout + the expert paths + the router path
-  MOE_HIP_TRY(moe::launch_router_wgrad(x, idx, b.dl, T, k, E, d, bf16, b.rpart, dW_router, d_bias, s, p.routed,
-                                       b.route_off, b.lcopy, b.ltok),
-              "router wgrad");
-  MOE_HIP_TRY(moe::launch_gather_dx(dout, b.dX, W_router, idx, b.dl, p.slot, T, d, k, C, bf16, dx, s),
-              "gather dx");
+    //  the gate gradients: q_j = <dh_j, h_j> = w_j <dout, y_j>, dl_j = q_j - w_j sum_i q_i
+    MOE_HIP_TRY(moe::launch_gate_grad(b.dh, h, idx, w, p.slot, T, F, k, C, bf16, b.dl, s), "gate gradients");
+    // 5. router gradients, then dx = dout + the expert paths + the router path
+    MOE_HIP_TRY(moe::launch_router_wgrad(x, idx, b.dl, T, k, E, d, bf16, b.rpart, dW_router, d_bias, s, p.routed,
+                                         b.route_off, b.lcopy, b.ltok),
+                "router wgrad");
+    MOE_HIP_TRY(moe::launch_gather_dx(dout, b.dX, W_router, idx, b.dl, p.slot, T, d, k, C, bf16, dx, s),
+                "gather dx");
   }
   // 6. weight gradients over each expert's kept rows: dWd = dy^T h, dWg = dg^T X,
   //    dWu = du^T X. bf16: both operands read K-major straight from the
