@@ -663,9 +663,10 @@ int layer_backward(const void* x, const Routing* given, const void* W_router, co
                                p.totals, bm, p.mtile, nullptr, s, nullptr, 0, nullptr, split.tick,
                                split.tick ? moe::kSplitUnits : 0),
               "scan");
-  MOE_HIP_TRY(moe::launch_exclusive_scan(p.routed, E, b.route_off, s), "routed offsets");
-  MOE_HIP_TRY(moe::launch_slots(idx, p.tile_off, T, k, E, C, p.slot, nullptr, p.totals, s, b.route_off, b.lcopy,
-                                b.ltok),
+  // the lists of each expert's routed copies are for the router's gradient
+  if (!given) MOE_HIP_TRY(moe::launch_exclusive_scan(p.routed, E, b.route_off, s), "routed offsets");
+  MOE_HIP_TRY(moe::launch_slots(idx, p.tile_off, T, k, E, C, p.slot, nullptr, p.totals, s,
+                                given ? nullptr : b.route_off, b.lcopy, b.ltok),
               "slots");
   if (!saved) MOE_HIP_TRY(moe::launch_scatter_rows(x, idx, p.slot, T, k, C, d * eb, X, s), "scatter");
   // g = X Wg^T and u = X Wu^T (the plain row-tile GEMM: N = d_ff, K = d). GEMMs
