@@ -400,8 +400,9 @@ int moe_layer_forward_few_q4(const void* x, const void* W_router, const float* r
  * topk_w[t, j] = scale * s_j, with renormalize divided by the sum of the chosen s
  * (0 where that sum is 0). Scores and order are evaluated in fp64, topk_w is
  * rounded to fp32. A NaN sorts below every number; the k experts are distinct
- * whatever the logits are. Limits (else MOE_ERR_UNSUPPORTED): E <= 4096, k <= 32,
- * T k < 2^31. */
+ * whatever the logits are. Weights are what the formulas give: where a softmax has a
+ * NaN or +infinity among the token's logits every weight is NaN, of a sigmoid's
+ * the NaN's own and, renormalized, all of a token that chose it. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 typedef struct {
   int32_t score;

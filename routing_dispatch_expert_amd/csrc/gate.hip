@@ -137,6 +137,12 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
     const int e = lane + 64 * i;
     l[i] = e < E ? static_cast<double>(logits[t * E + e]) : -INFINITY;
   }
+  bool nan = false;  // a NaN or an infinity makes every score NaN, which a softmax over the chosen alone does not see
+  if (!g.sigmoid && g.renormalize) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) nan = nan || !(l[i] < INFINITY);
+    nan = __ballot(nan) != 0;
+  }
   // the scores, where the choice needs them
   const bool scores = bias || (g.groups > 1 && g.best > 1) || (!g.sigmoid && !g.renormalize);
   double top = 0, total = 1;
@@ -277,12 +283,13 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
   } else if (g.renormalize) {  // a softmax over the chosen
     const double m = first_max(my_l, k);
     z = in && m > -INFINITY ? exp(my_l - m) : 0;
+    if (nan) z = NAN;
   } else {
     z = in ? exp(my_l - top) / total : 0;
   }
   if (g.renormalize) {
     const double sum = first_sum(z, k);
-    z = sum > 0 ? z / sum : 0;
+    z = sum == 0 ? 0 : z / sum;  // a NaN stays one
   }
   if (in) {
     idx[t * k + lane] = my_e;

@@ -1,0 +1,71 @@
+"""NaN and infinities among the gate's logits: what the formulas give, at every number of scores a lane holds."""
+import numpy as np
+import pytest
+
+import routing_dispatch_expert_amd as moe
+from tests import gate_reference as ref
+from tests.gpu_util import U, gpu_available, say
+from tests.test_gpu_gate import dev
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+SIZES = [8, 64, 65, 100, 256, 300, 700, 2000]   # 1, 2, 4, 8, 16 and 64 scores a lane
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    assert gpu_available(), "GPU tests need an MI355X; run them with -m gpu on a GPU host"
+    moe.lib()
+
+
+def rows(E):
+    """Rows with: no NaN; one at the end of the order; all but two; nothing else; one of the other sign; +inf; +inf twice;
+    one beside -inf; -inf alone."""
+    l = np.random.default_rng(E).standard_normal((9, E)).astype(np.float32)
+    l[1, E // 2] = np.nan
+    l[2, 2:] = np.nan
+    l[3] = np.nan
+    l[4, E - 1] = -np.float32(np.nan)
+    l[5, 3] = np.inf
+    l[6, 1:3] = np.inf
+    l[7] = -np.inf
+    l[7, E - 2] = np.nan
+    l[8] = -np.inf
+    return l
+
+
+def weights(l, idx, score, renormalize, scale):
+    """The chosen ones' weights as the formulas have them, in 64 bits."""
+    with np.errstate(all="ignore"):
+        l = l.astype(np.float64)
+        if score == "sigmoid":
+            s = 1 / (1 + np.exp(-l))
+        else:
+            m = l.max(1, keepdims=True)   # NaN where there is one
+            e = np.exp(l - np.where(np.isneginf(m), 0, m))
+            total = e.sum(1, keepdims=True)
+            s = e / np.where(total == 0, 1, total)
+        z = np.take_along_axis(s, idx.astype(np.int64), 1)
+        total = z.sum(1, keepdims=True)
+        return scale * (z / np.where(total == 0, 1, total) if renormalize else z)
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", SIZES)
+def test_weights(E, score, renormalize):
+    say("gate with NaN", E, score, renormalize)
+    l = rows(E)
+    for k in (1, 4):
+        for bias in (None, np.zeros(E, np.float32)):
+            r = moe.gate(dev(l), k, score=score, bias=dev(bias), renormalize=renormalize, scale=1.5)
+            idx, w = r["topk_idx"].cpu().numpy(), r["topk_w"].cpu().numpy()
+            if bias is None:   # in the order of the logits, NaN last
+                assert np.array_equal(idx, [ref._ranked(t)[:k] for t in l])
+            want = weights(l, idx, score, renormalize, 1.5)
+            assert np.array_equal(np.isnan(w), np.isnan(want)), (k, bias is None)
+            ok = ~np.isnan(want)
+            assert np.all(np.abs(w - want)[ok] <= U * (1 + 2.0 ** -20) * np.abs(want[ok]) + 2.0 ** -149)
+            nan = np.array([1, 2, 3, 4, 5, 6, 7])
+            assert np.isnan(w[nan]).all() if score == "softmax" else np.isnan(w[3]).all()
+            assert not w[8].any()
