@@ -402,7 +402,8 @@ int moe_layer_forward_few_q4(const void* x, const void* W_router, const float* r
  * rounded to fp32. A NaN sorts below every number; the k experts are distinct
  * whatever the logits are. Weights are what the formulas give: where a softmax has a
  * NaN or +infinity among the token's logits every weight is NaN, of a sigmoid's
- * the NaN's own and, renormalized, all of a token that chose it. */
+ * the NaN's own and, renormalized, all of a token that chose it. Limits (else
+ * MOE_ERR_UNSUPPORTED): E <= 4096, k <= 32, groups <= 64, T < 2^26 - 4, T k < 2^31. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 typedef struct {
   int32_t score;
