@@ -418,7 +418,9 @@ int moe_gate(const float* logits, const float* bias, const moe_gate_t* gate, int
 
 /* dlogits [T, E] of the gradients d_topk_w [T, k] of the weights of the chosen
  * topk_idx and, optionally, d_scores [T, E] of all scores s (a balance loss's);
- * the choice is held fixed, of `gate` score, renormalize and scale are used. An
+ * the choice is held fixed, of `gate` score, renormalize and scale are used. NaN
+ * scores give NaN: with d_scores or a softmax that is not renormalized the row's whole
+ * gradient where a softmax's scores are NaN, else that of the chosen alone. An
  * index that a row has twice counts twice; one outside [0, E) passes no gradient.
  * Written, not accumulated; dlogits must not overlap logits or d_scores. */
 int moe_gate_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, const float* d_scores,

@@ -318,6 +318,12 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const float* __restr
     l[i] = e < E ? logits[t * E + e] : -INFINITY;
     ds[i] = dscores && e < E ? dscores[t * E + e] : 0.f;
   }
+  bool nan = false;  // as in the forward: every score of a softmax is NaN
+  if (!g.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) nan = nan || !(l[i] < INFINITY);
+    nan = __ballot(nan) != 0;
+  }
   int e_j = -1;
   double l_j = 0, q_j = 0;
   if (lane < k) {
@@ -338,9 +344,10 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const float* __restr
     } else {
       const double m = first_max(in ? l_j : -INFINITY, k);
       z = in && m > -INFINITY ? exp(l_j - m) : 0;
+      if (in && nan) z = NAN;
     }
     const double sum = first_sum(z, k);
-    const double r = sum > 0 ? z / sum : 0;
+    const double r = sum == 0 ? 0 : z / sum;  // a NaN stays one
     const double D = first_sum(q_j * r, k);
     term = r * (q_j - D) * (g.sigmoid ? sigmoid64(-l_j) : 1.0);
   } else {
@@ -386,7 +393,7 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const float* __restr
       }
       sum = wave_sum(sum);
       dot = wave_sum(dot);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = nan ? NAN : sum > 0.f ? 1.f / sum : 0.f;  // 0: every expert masked
       dot *= inv;
 #pragma unroll
       for (int i = 0; i < NE; ++i) dl[i] += p[i] * inv * (ds[i] - dot);

@@ -69,3 +69,44 @@ def test_weights(E, score, renormalize):
             nan = np.array([1, 2, 3, 4, 5, 6, 7])
             assert np.isnan(w[nan]).all() if score == "softmax" else np.isnan(w[3]).all()
             assert not w[8].any()
+
+
+def gradients(l, idx, dw, dsc, score, renormalize, scale):
+    """Where the gradient is NaN, and the gradient of the rows without one, in 64 bits."""
+    T, E = l.shape
+    own = np.isnan(l)
+    bad = ~(l < np.inf).all(1) if score == "softmax" else np.zeros(T, bool)   # every score of the row is NaN
+    nan = np.zeros((T, E), bool)
+    for t in range(T):
+        if renormalize:   # the sum of the chosen ones' scores enters each of theirs
+            nan[t, idx[t]] = bad[t] or own[t, idx[t]].any()
+        elif score == "sigmoid":
+            nan[t, idx[t]] = own[t, idx[t]]
+        if dsc is not None or (score == "softmax" and not renormalize):
+            nan[t] |= own[t] if score == "sigmoid" else bad[t]
+    fine = ~(own.any(1) | bad)
+    want, mag = np.zeros((T, E)), np.zeros((T, E))
+    want[fine], mag[fine] = ref.gate_backward(l[fine], idx[fine], dw[fine], score, renormalize, scale, None if dsc is None else dsc[fine])
+    return nan, want, mag, fine
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", SIZES)
+def test_gradients(E, score, renormalize):
+    say("gate backward with NaN", E, score, renormalize)
+    rng = np.random.default_rng(E)
+    l = rows(E)
+    l[6, 1:3] = (-np.inf, 1.0)      # a row without NaN beside them
+    for chosen in (False, True):    # whether the NaN is among the chosen
+        order = [[e for e in ref._ranked(r) if chosen or np.isfinite(r[e])] for r in l]
+        idx = np.array([(o[0], o[-1]) if len(o) > 1 else (0, 1) for o in order], np.int32)
+        dw = rng.standard_normal(idx.shape).astype(np.float32)
+        for dsc in (None, rng.standard_normal(l.shape).astype(np.float32)):
+            got = moe.gate_backward(dev(l), dev(idx, np.int32), dev(dw), score=score, renormalize=renormalize, scale=1.5,
+                                    d_scores=dev(dsc)).cpu().numpy()
+            nan, want, mag, fine = gradients(l, idx, dw, dsc, score, renormalize, 1.5)
+            assert np.array_equal(np.isnan(got), nan), (chosen, dsc is not None)
+            steps = 2 * (E / 64 + 6 + 14)   # as in test_gpu_gate.py
+            assert np.all(np.abs(got - want)[fine] <= U * steps * mag[fine] + 1e-38)
+            assert not got[8].any()
