@@ -399,8 +399,9 @@ int moe_layer_forward_few_q4(const void* x, const void* W_router, const float* r
  * taken from the top_groups best groups (lower group first on a tie).
  * topk_w[t, j] = scale * s_j, with renormalize divided by the sum of the chosen s
  * (0 where that sum is 0). Scores and order are evaluated in fp64, topk_w is
- * rounded to fp32. A NaN sorts below every number; the k experts are distinct
- * whatever the logits are. Weights are what the formulas give: where a softmax has a
+ * rounded to fp32. A NaN sorts below every number, also as a group's value (with
+ * fewer numbers than group_best); the k experts are distinct whatever the logits are.
+ * Weights are what the formulas give: where a softmax has a
  * NaN or +infinity among the token's logits every weight is NaN, of a sigmoid's
  * the NaN's own and, renormalized, all of a token that chose it. Limits (else
  * MOE_ERR_UNSUPPORTED): E <= 4096, k <= 32, groups <= 64, T < 2^26 - 4, T k < 2^31. */

@@ -203,7 +203,13 @@ __global__ __launch_bounds__(256) void gate_kernel(const float* __restrict__ log
       b = fmax(fmin(a, oa), fmax(b, ob));
       a = fmax(a, oa);
     }
-    const uint64_t value = order_of(g.best > 1 ? a + b : a);
+    const double sum = g.best > 1 ? a + b : a;
+    uint64_t value = order_of(sum);
+    if (sum == -INFINITY && mine < g.groups) {  // of -inf, or of too few numbers beside NaN: below every number
+      int numbers = 0;
+      for (int i = 0; i < per; ++i) numbers += v[mine * per + i] == v[mine * per + i] ? 1 : 0;
+      if (numbers < g.best) value = order_of(NAN);
+    }
     int ahead = 0;  // groups that are better, or as good and before this one
     for (int o = 0; o < g.groups; ++o) {
       const uint64_t ov = lane_word(value, o << gs.log_lanes);

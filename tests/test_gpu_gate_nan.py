@@ -110,3 +110,25 @@ def test_gradients(E, score, renormalize):
             steps = 2 * (E / 64 + 6 + 14)   # as in test_gpu_gate.py
             assert np.all(np.abs(got - want)[fine] <= U * steps * mag[fine] + 1e-38)
             assert not got[8].any()
+
+
+@pytest.mark.parametrize("G,per", [(4, 8), (4, 16), (8, 32), (16, 40), (64, 3)])
+def test_groups_of_nan_come_after_groups_of_masked_experts(G, per):
+    """Group 1 has numbers, group 0 only NaN (or one number where two are added up), the others -inf (masked)."""
+    E = G * per
+    l = np.full((2, E), -np.inf, np.float32)
+    l[:, per:2 * per] = np.random.default_rng(G).standard_normal(per)
+    l[0, :per] = np.nan
+    l[1, :per] = np.nan
+    l[1, per // 2] = 3.0
+    k = min(per + 2, 32)
+    first = [per + i for i in ref._ranked(l[0, per:2 * per])]
+    want = (first + list(range(2 * per, E)))[:k]
+    r = moe.gate(dev(l), k, score="sigmoid", groups=G, top_groups=2)["topk_idx"].cpu().numpy()
+    assert r[0].tolist() == want
+    assert r[1, 0] == per // 2   # one number is enough for the largest
+    bias = np.where(np.isneginf(l[0]), -np.inf, 0).astype(np.float32)
+    for b in (None, bias):   # without a bias the scores are added up: those of -inf are 0
+        r = moe.gate(dev(l), k, score="sigmoid", groups=G, top_groups=2, group_best=2, bias=dev(b))["topk_idx"].cpu().numpy()
+        for row in r:
+            assert row.tolist() == want
