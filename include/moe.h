@@ -512,8 +512,8 @@ int moe_rmsnorm_backward(const void* dy, const void* h, const void* weight, cons
  * W_gate, W_up [E, d_ff, d], W_down [E, d, d_ff] in 8 bits:
  *   C = moe_capacity(T, E, k, cf); slot = stable token-order rank of each copy among its expert's, dropped (-1) if >= C
  *   h = silu(x W_gate^T) * (x W_up^T), put into 8 bits as moe_mx8_quantize does it
- *   y = h W_down^T, rounded to dtype
- *   out[t] = residual[t] + sum_j [slot >= 0] topk_w[t,j] y[t,j]      (j ascending, in fp32)
+ *   y = h W_down^T, in fp32
+ *   out[t] = residual[t] + sum_j [slot >= 0] topk_w[t,j] y[t,j]      (j ascending, in fp32, rounded to dtype)
  * residual, out [T, d]: dtype, 16-byte aligned (out may be residual itself); a token
  * without a kept copy passes bit for bit. A topk_idx entry outside [0, E) is
  * dropped and counted nowhere; an expert that a token names twice counts twice.

@@ -57,14 +57,14 @@ struct ExpertsMx8 {
   const float* w;
   int64_t T, d, f, C;
   int E, k;
-  bool bf16;       // residual, y and out
+  bool bf16;       // residual and out
   void* out;
   int32_t *slot, *routed, *kept;
   // workspace
   ExpertLists ls;
   int32_t *tile_cnt, *tile_off;  // [ceil(T / kTileTokens)][E]
   Mx8Ptr h;        // rows [T k][f]
-  void* y;         // [T k][d]
+  float* y;        // [T k][d]
   float* parts;    // mx8_parts_bytes(T k, min(E, T k), f), or NULL
 };
 // Sums of down's split tiles (mx8_tiles.hip); 0 where none can be.

@@ -1568,12 +1568,11 @@ struct ExpertsPlan {
   moe::ExpertLists ls;
   moe::Mx8Ptr h;
   int32_t *slot, *routed, *kept, *tile_cnt, *tile_off;
-  void* y;
-  float* parts;
+  float *y, *parts;
   size_t bytes;
 };
 
-ExpertsPlan plan_experts_mx8(void* ws, int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k, int eb) {
+ExpertsPlan plan_experts_mx8(void* ws, int64_t T, int64_t d, int64_t d_ff, int32_t E, int32_t k) {
   Carver c(ws);
   ExpertsPlan p;
   const size_t n = static_cast<size_t>(T) * k;
@@ -1590,7 +1589,7 @@ ExpertsPlan plan_experts_mx8(void* ws, int64_t T, int64_t d, int64_t d_ff, int32
   p.tile_off = c.take<int32_t>(counts);
   p.h.codes = c.take<uint8_t>(n * d_ff);
   p.h.scale = c.take<uint32_t>(mx8_scale_bytes(1, n, d_ff) / 4);
-  p.y = c.take<char>(n * d * eb);
+  p.y = c.take<float>(n * d);
   const int64_t parts = n ? moe::mx8_parts_bytes(n, std::min<int64_t>(E, n), d_ff) : 0;
   p.parts = c.take<float>(parts / 4);
   if (!parts) p.parts = nullptr;
@@ -1622,7 +1621,7 @@ int moe_experts_mx8_workspace_size(int64_t T, int64_t d, int64_t d_ff, int32_t E
   int64_t C;
   const int st = check_experts_mx8(T, d, d_ff, E, k, cf, dtype, &C);
   if (st != MOE_OK) return st;
-  *bytes = plan_experts_mx8(nullptr, T, d, d_ff, E, k, elem_bytes(dtype)).bytes;
+  *bytes = plan_experts_mx8(nullptr, T, d, d_ff, E, k).bytes;
   return MOE_OK;
 }
 
@@ -1646,10 +1645,9 @@ int moe_experts_mx8(const moe_mx8_t* x, const void* residual, const int32_t* top
   if (!residual || !topk_idx || !topk_w || !out) return fail(MOE_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned16(residual) || !aligned16(out))
     return fail(MOE_ERR_INVALID_ARG, "residual and out must be 16-byte aligned");
-  const int eb = elem_bytes(dtype);
-  if (overlaps_askew(out, residual, static_cast<size_t>(T) * d * eb))
+  if (overlaps_askew(out, residual, static_cast<size_t>(T) * d * elem_bytes(dtype)))
     return fail(MOE_ERR_INVALID_ARG, "out overlaps residual");
-  const ExpertsPlan p = plan_experts_mx8(workspace, T, d, d_ff, E, k, eb);
+  const ExpertsPlan p = plan_experts_mx8(workspace, T, d, d_ff, E, k);
   if (!workspace || workspace_bytes < p.bytes || reinterpret_cast<uintptr_t>(workspace) % kAlign)
     return fail(MOE_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned", p.bytes);
   moe::ExpertsMx8 L;

@@ -38,8 +38,7 @@ struct Mx8Gemm {
   uint8_t* hcodes;    // GU: h [rows][N], scale [steps][H]
   uint8_t* hscale;
   int64_t H;
-  void* y;            // else: [copies][N]
-  bool y_bf16;
+  float* y;           // else: [copies][N]
   float* parts;       // or NULL: of down's tiles that are split over K
 };
 

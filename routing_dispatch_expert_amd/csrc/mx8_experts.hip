@@ -5,8 +5,8 @@
 // matrices per expert; "Expert Parallelism & All-to-All" (neelmishra.github.io),
 // "All-to-all: the distributed transpose" - gate-weighted sum into the residual.
 //
-//   h = mx8(silu(x Wg^T) * (x Wu^T));  y = h Wd^T, rounded to the output's type
-//   out[t] = residual[t] + sum_j [slot[t, j] >= 0] w[t, j] y[t, j]
+//   h = mx8(silu(x Wg^T) * (x Wu^T));  y = h Wd^T, in fp32
+//   out[t] = residual[t] + sum_j [slot[t, j] >= 0] w[t, j] y[t, j], rounded once
 //
 // The products run on the scaled 8-bit matrix instructions: 128 (or 64) columns
 // an instruction, a scale for every 32. The weights are the A operand (an
@@ -354,12 +354,7 @@ __device__ inline void few_rows(const Mx8Gemm& a, int e, int row0, int n, int st
       for (int i = 0; i < NA; ++i) {
         const int64_t f = n0 + 16 * i + 4 * quad;
         if (f >= a.N) continue;
-        if (a.y_bf16)
-          *reinterpret_cast<uint2*>(static_cast<bf16_t*>(a.y) + r * a.N + f) =
-              uint2{f32_to_bf16(v[i][0]) | static_cast<uint32_t>(f32_to_bf16(v[i][1])) << 16,
-                    f32_to_bf16(v[i][2]) | static_cast<uint32_t>(f32_to_bf16(v[i][3])) << 16};
-        else
-          *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + r * a.N + f) = v[i];
+        *reinterpret_cast<f32x4*>(a.y + r * a.N + f) = v[i];
       }
     }
   }
@@ -392,6 +387,11 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(Mx8Gemm a, int str
 
 // out[t] = residual[t] + sum_j w y[t, j] over the kept copies, j ascending, in
 // fp32; a token without a kept copy passes bit for bit.
+// y comes in fp32: in bf16 its rounding adds to out's own as much as all else does
+// (64 tokens, DeepSeek-V3-shaped: 1.84e-3 against 64 bits instead of 1.75e-3, of which
+// out's rounding is 1.66e-3). Twice the bytes of y cost nothing there, and 1.1% on 4096
+// Mixtral-shaped tokens (1542 -> 1559 us), 6% on 8192 DeepSeek-V3-shaped ones (4430 ->
+// 4690 us).
 template <bool BF16>
 __global__ __launch_bounds__(256) void experts_combine_kernel(const uint4* residual, const uint4* __restrict__ y,
                                                               const float* __restrict__ w,
@@ -408,17 +408,17 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(const uint4* resid
   for (int j = 0; j < k; ++j) {
     if (slot[t * k + j] < 0) continue;
     any = true;
-    const uint4 word = load_stream(y + (t * k + j) * V + v);
-    const float g = w[t * k + j];
-    const uint32_t u[4] = {word.x, word.y, word.z, word.w};
+    const uint4* row = y + ((t * k + j) * V + v) * (P / 4);
+    uint4 word[P / 4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if constexpr (BF16) {
-        acc[2 * q] = fmaf(g, __uint_as_float(u[q] << 16), acc[2 * q]);
-        acc[2 * q + 1] = fmaf(g, __uint_as_float(u[q] & 0xffff0000u), acc[2 * q + 1]);
-      } else {
-        acc[q] = fmaf(g, __uint_as_float(u[q]), acc[q]);
-      }
+    for (int h = 0; h < P / 4; ++h) word[h] = load_stream(row + h);
+    const float g = w[t * k + j];
+#pragma unroll
+    for (int h = 0; h < P / 4; ++h) {
+      const uint32_t u[4] = {word[h].x, word[h].y, word[h].z, word[h].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[4 * h + q] = fmaf(g, __uint_as_float(u[q]), acc[4 * h + q]);
+    }
   }
   uint32_t u[4] = {in.x, in.y, in.z, in.w};
   if (any) {
@@ -466,7 +466,6 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   a.hscale = reinterpret_cast<uint8_t*>(L.h.scale);
   a.H = copies;
   a.y = nullptr;
-  a.y_bf16 = L.bf16;
   a.parts = nullptr;
   const bool many = mx8_many(copies, act);
   const int64_t tiles = copies / tile_rows + act;
@@ -491,7 +490,7 @@ hipError_t launch_experts_mx8(const ExpertsMx8& L, hipStream_t s) {
   const int64_t V = L.d / (L.bf16 ? 8 : 4), blocks = ceil_div(V, 256);
   const dim3 grid(static_cast<unsigned>(L.T * blocks));
   const auto* rv = static_cast<const uint4*>(L.residual);
-  const auto* yv = static_cast<const uint4*>(L.y);
+  const auto* yv = reinterpret_cast<const uint4*>(L.y);
   if (L.bf16)
     experts_combine_kernel<true><<<grid, dim3(256), 0, s>>>(rv, yv, L.w, L.slot, L.k, V, blocks, static_cast<uint4*>(L.out));
   else

@@ -422,29 +422,12 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         const int64_t f0 = nw + 32 * i;
-        if (a.y_bf16) {
-          uint2 w[4];  // features 8 g + 4 lq .. + 3
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            w[g] = uint2{f32_to_bf16(acc[i][j][4 * g]) | static_cast<uint32_t>(f32_to_bf16(acc[i][j][4 * g + 1])) << 16,
-                         f32_to_bf16(acc[i][j][4 * g + 2]) | static_cast<uint32_t>(f32_to_bf16(acc[i][j][4 * g + 3])) << 16};
-#pragma unroll
-          for (int g = 0; g < 4; g += 2) {  // lanes 0 - 31 get features 8 g .. + 7, the others 8 g + 8 .. + 15
-            const uint2 give = lq ? w[g] : w[g + 1];
-            const uint2 got = uint2{static_cast<uint32_t>(__shfl_xor(give.x, 32, 64)), static_cast<uint32_t>(__shfl_xor(give.y, 32, 64))};
-            const int64_t f = f0 + 8 * g + 8 * lq;
-            if (c < rows && f < N)
-              *reinterpret_cast<uint4*>(static_cast<bf16_t*>(a.y) + r * N + f) =
-                  lq ? uint4{got.x, got.y, w[g + 1].x, w[g + 1].y} : uint4{w[g].x, w[g].y, got.x, got.y};
-          }
-        } else {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int64_t f = f0 + 8 * g + 4 * lq;
-            if (c < rows && f < N)
-              *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + r * N + f) =
-                  f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-          }
+        for (int g = 0; g < 4; ++g) {
+          const int64_t f = f0 + 8 * g + 4 * lq;
+          if (c < rows && f < N)
+            *reinterpret_cast<f32x4*>(a.y + r * N + f) =
+                f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
         }
       }
     }
@@ -475,12 +458,7 @@ __global__ __launch_bounds__(256) void join_parts_kernel(Mx8Gemm a, int E) {
     f32x4 sum = parts[v];
     for (int p = 1; p < sp.parts; ++p) sum += parts[static_cast<int64_t>(p) * (kPartFloats / 4) + v];
     const int64_t at = static_cast<int64_t>(a.ls.copy[first + c]) * a.N + f;
-    if (a.y_bf16)
-      *reinterpret_cast<uint2*>(static_cast<bf16_t*>(a.y) + at) =
-          uint2{f32_to_bf16(sum[0]) | static_cast<uint32_t>(f32_to_bf16(sum[1])) << 16,
-                f32_to_bf16(sum[2]) | static_cast<uint32_t>(f32_to_bf16(sum[3])) << 16};
-    else
-      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = sum;
+    *reinterpret_cast<f32x4*>(a.y + at) = sum;
   }
 }
 
