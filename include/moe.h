@@ -485,7 +485,8 @@ int moe_mx8_dequantize(const moe_mx8_t* q, int32_t E, int64_t N, int64_t K, moe_
  * For rows r < R of width d (a multiple of 8, fp32: of 4, with y8 of 16; at most
  * 65536, fp32 32768):
  *   h = x + residual, rounded to dtype (residual NULL: h = x, and h_out must be NULL)
- *   rstd = 1 / sqrt(mean(h^2) + eps)          fp32, sums of squares in fp32
+ *   rstd = 1 / sqrt(mean(h^2) + eps)          fp32; up to 64 squares at a time are summed in fp32
+ *                                             (|h| < 2^60), those sums in fp64
  *   y = h rstd weight                         rounded to dtype, and y8 to 8 bits, each from the fp32 value
  * x, residual, weight [d], h_out, y: dtype, 16-byte aligned; of h_out, y, y8 (rows
  * [R, d]) and rstd [R] any may be NULL. h_out may be x or residual itself; other

@@ -121,11 +121,13 @@ __device__ inline bool tile_at(const ExpertLists& ls, int E, int feature_tile, i
 
 // WM x WN waves of TM x TN tiles of 32 x 32, NS slots for stages: 2 x 2 of 4 x 4 and
 // two slots, or of 4 x 2 and three. The former's stage is 32 products
-// a wave (2048 clocks), 128 KiB of LDS read and 66 written, which together with
-// its loads' way through the L2 bounds it: 1.9 us a stage where the products alone
-// take 1.0 at the clock that they leave (4.25 PFLOP/s in registers). Mixtral-shaped,
-// 4096 tokens: gate and up 1.07 - 1.12 ms (1.92 TFLOP: 1.75 PFLOP/s), down 0.51
-// - 0.55 and 0.016 for the join of its split tiles (0.65 without the split).
+// a wave (2048 clocks), 128 KiB of LDS read and 66 written, and takes 1.9 us where
+// the products alone take 1.0 at the clock that they leave (4.25 PFLOP/s in
+// registers; the library's product of 16384^3 reaches 3.27). One wave a SIMD: its
+// waits for loads, LDS and the stages' barriers are filled by nothing (the matrix
+// cores are busy 52 - 54% of the time). Mixtral-shaped, 4096 tokens: gate and up 1.06
+// - 1.17 ms (1.92 TFLOP: 1.65 - 1.82 PFLOP/s), down 0.55 - 0.57 and 0.017 for the join
+// of its split tiles (some 0.65 without the split).
 // Measured and dropped: 2 x 4 waves of 4 x 2 tiles (256 registers do not hold them:
 // twice the time), 128 features a block (down 0.81 ms), a word of each weight line
 // asked for two stages before (down 0.61 ms, but 64 rows an expert 12% more).

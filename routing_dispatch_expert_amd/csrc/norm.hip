@@ -9,7 +9,8 @@
 //   dh = rstd (a - n mean(a n)) + dres;  dweight = sum over rows of dy n
 //
 // A row is read once: its 16-byte words stay in registers between the sum and
-// the use of it. Sums are in fp32, in a fixed order. Bound by memory: 8192 x 7168
+// the use of it. Sums are in fp32 within a thread (64 numbers at most) and, of the
+// squares, in fp64 between threads, in a fixed order. Bound by memory: 8192 x 7168
 // bf16 with a residual and all outputs 87 us (530 MB, 6.1 TB/s).
 #include "mx8.h"
 
@@ -153,6 +154,10 @@ __global__ __launch_bounds__(THR > 256 ? THR : 256) void rmsnorm_kernel(
 // Gradient of the rows that the block (THR = 64: each of its four waves) takes in
 // turn; its sum of dweight's terms stays in registers until the end and becomes a
 // row of parts [gridDim][d]. 8192 x 4096 bf16 with dh_in: 45 us (268 MB, 6 TB/s; with 1024 blocks 50).
+// Rows of more than 2048 words take 1024 threads, which have 128 registers each: three
+// rows of words and dweight's sums do not fit them (bf16 4 words a thread 336 bytes of
+// scratch a lane, 8 words 1112; fp32 8 words 468). With dweight_kernel, 268 MB each:
+// bf16 d = 16384 64 us, 32768 155, 65536 405; fp32 16384 46 us, 32768 140.
 template <bool BF16, int THR, int U>
 __global__ __launch_bounds__(THR > 256 ? THR : 256) void rmsnorm_backward_kernel(
     const uint4* dy, const uint4* h, const uint4* __restrict__ weight, const float* __restrict__ rstd,
