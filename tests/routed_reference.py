@@ -15,12 +15,12 @@ def _times(a, ea, b, eb):
 
 
 def gradients(x, idx, w, slot, W, dout, half):
-    """{name: (value, bound)} of dx, d_topk_w, dW_gate, dW_up, dW_down, and "parts" [T]: the norms of the copies' parts
-    of dx, added in squares. Tensors of 64 bits; idx and slot as they are."""
+    """{name: (value, bound)} of dx, d_topk_w, dW_gate, dW_up, dW_down; "parts" [T]: the norms of the copies' parts of dx,
+    added in squares; "terms" [T, k]: the terms of d_topk_w, the same. Tensors of 64 bits; idx and slot as they are."""
     T, k = idx.shape
     d, F, E = x.shape[1], W[0].shape[1], W[0].shape[0]
     dx, edx, size = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x)
-    dw, edw, parts = torch.zeros_like(w), torch.zeros_like(w), torch.zeros_like(w[:, 0])
+    dw, edw, terms, parts = torch.zeros_like(w), torch.zeros_like(w), torch.zeros_like(w), torch.zeros_like(w[:, 0])
     dW, eW = [torch.zeros_like(m) for m in W], [torch.zeros_like(m) for m in W]
     stored = lambda v, e, times=1: e + times * half * (v.abs() + e) + TINY  # noqa: E731
     for e in range(E):
@@ -43,6 +43,7 @@ def gradients(x, idx, w, slot, W, dout, half):
         edy = stored(dy, 0 * dy)
         edh = stored(dh, edy @ Wd.abs() + 2 * U * d * (dy.abs() @ Wd.abs()), 2)
         dw[t, j] = (dh * h).sum(1)
+        terms[t, j] = (dh * h).norm(dim=1)
         edw[t, j] = (_times(dh, edh, h, eh) + 2 * U * F * (dh * h).abs()).sum(1) + 2 * U * (dh * h).sum(1).abs()
         dy, edy, dh, edh = weight * dy, weight.abs() * edy + TINY, weight * dh, weight.abs() * edh + TINY
         a, ea = u * slope, _times(u, eu, slope, eslope)
@@ -62,4 +63,4 @@ def gradients(x, idx, w, slot, W, dout, half):
             eW[i][e] = stored(dW[i][e], err)
     edx = stored(dx, edx + k * U * size)
     return {"dx": (dx, edx), "d_topk_w": (dw, edw), "dW_gate": (dW[0], eW[0]), "dW_up": (dW[1], eW[1]), "dW_down": (dW[2], eW[2]),
-            "parts": parts.sqrt()}
+            "parts": parts.sqrt(), "terms": terms}

@@ -53,7 +53,7 @@ def check(b, cf, dtype):
     off = (got["dx"].double() - want["dx"][0]).norm(dim=1)
     assert (off <= part * want["parts"] + 1e-35).all(), f"dx: {(off / want['parts']).max()}"
     off = (got["d_topk_w"].double() - want["d_topk_w"][0]).norm()
-    assert off <= part * want["d_topk_w"][0].norm(), f"d_topk_w: {off / want['d_topk_w'][0].norm()}"
+    assert off <= part * want["terms"].norm(), f"d_topk_w: {off / want['terms'].norm()}"   # a sum may be far smaller than its terms
     assert not got["d_topk_w"][f["slot"] < 0].any()
     return f, got
 
