@@ -401,10 +401,10 @@ int moe_layer_forward_few_q4(const void* x, const void* W_router, const float* r
  * (0 where that sum is 0). Scores and order are evaluated in fp64, topk_w is
  * rounded to fp32. A NaN sorts below every number, also as a group's value (with
  * fewer numbers than group_best); the k experts are distinct whatever the logits are.
- * Weights are what the formulas give: where a softmax has a
- * NaN or +infinity among the token's logits every weight is NaN, of a sigmoid's
- * the NaN's own and, renormalized, all of a token that chose it. Limits (else
- * MOE_ERR_UNSUPPORTED): E <= 4096, k <= 32, groups <= 64, T < 2^26 - 4, T k < 2^31. */
+ * Weights are what the formulas give: where a softmax has a NaN or +infinity among
+ * the token's logits every weight is NaN; of a sigmoid's, the NaN's own and,
+ * renormalized, all of a token that chose it. Limits (else MOE_ERR_UNSUPPORTED):
+ * E <= 4096, k <= 32, groups <= 64, T < 2^26 - 4, T k < 2^31. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 typedef struct {
   int32_t score;
@@ -419,10 +419,11 @@ int moe_gate(const float* logits, const float* bias, const moe_gate_t* gate, int
 
 /* dlogits [T, E] of the gradients d_topk_w [T, k] of the weights of the chosen
  * topk_idx and, optionally, d_scores [T, E] of all scores s (a balance loss's);
- * the choice is held fixed, of `gate` score, renormalize and scale are used. NaN
- * scores give NaN: with d_scores or a softmax that is not renormalized the row's whole
- * gradient where a softmax's scores are NaN, else that of the chosen alone. An
+ * the choice is held fixed, of `gate` score, renormalize and scale are used. An
  * index that a row has twice counts twice; one outside [0, E) passes no gradient.
+ * NaN scores give NaN gradients: where a softmax's are, the whole row's with d_scores
+ * or not renormalized, else the chosen ones'; of a sigmoid the NaN's own, where it
+ * has one, and, renormalized, all of those chosen with it.
  * Written, not accumulated; dlogits must not overlap logits or d_scores. */
 int moe_gate_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w, const float* d_scores,
                       const moe_gate_t* gate, int64_t T, int32_t E, int32_t k, float* dlogits, void* stream);
